@@ -322,6 +322,148 @@ elsaa_status elsaa_race_value_grad(const elsaa_params* p, const void* k, const v
 #define ELSAA_PATH_TC_WIN 16
 int32_t elsaa_path_flags(const elsaa_params* p);
 
+/* ---- The operators next to ELSAA in an attention layer --------------------
+ *
+ * What goes directly before the attention (RMS norm of every query and key row
+ * and the position rotation), exact causal attention over a sliding window
+ * with sinks (token windows: the local pattern without chunks), and the
+ * serving forms of both over a cache in pages.  Conventions that differ from
+ * the ELSAA entry points:
+ *   - Grouped heads: Hkv key heads serve H query heads (H % Hkv == 0); query
+ *     head h reads key head h / (H / Hkv).
+ *   - Strides: `strides` is a host array of three element strides (batch,
+ *     head, token) per tensor, in the order the entry point names, or NULL for
+ *     dense [B, heads, N, d].  d is contiguous.  Every stride times the element
+ *     size is a multiple of 16 bytes and positive where the dimension is
+ *     larger than one (a broadcast input is materialised by the caller).
+ *   - The workspace's error word is only ever set by these calls: the caller
+ *     zeroes its first 256 bytes once, and elsaa_check() reads and clears it.
+ *   - Two calls that may run at the same time (two streams, two captured
+ *     graphs) need a workspace each. */
+
+typedef struct {
+  int32_t B, H, Hkv, N, d;   /* d in {32, 64, 128} */
+  int32_t dtype;             /* elsaa_dtype of q, k and their gradients */
+  int32_t rot_dim;           /* leading values of a row that rotate: 0..d, a multiple of 16 */
+  int32_t interleaved;       /* pairs (2i, 2i+1); 0: pairs (i, i + rot_dim/2) */
+  int32_t norm;              /* 1: RMS norm first; 0: rotation only */
+  int32_t max_pos;           /* rows of the (cos, sin) table */
+  float eps;                 /* added to the mean square, >= 0 */
+} elsaa_rotary_params;
+
+elsaa_status elsaa_rotary_validate(const elsaa_rotary_params* p);
+size_t elsaa_rotary_workspace_bytes(const elsaa_rotary_params* p);
+
+/* Every row x of q (H heads) and k (Hkv heads), in one launch:
+ *   n = x / sqrt(mean(x^2) + eps),  u = n * weight,
+ *   (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin) for its pairs (a, b),
+ * with the angles of table[position].  table: device fp32
+ * [max_pos, rot_dim / 2, 2] of (cos, sin).  positions: device int32 [B, N], or
+ * NULL for 0..N-1; a position outside the table is recorded (DEVICE_CHECK) and
+ * its row is written as zeros.  q_weight, k_weight: device fp32 [d], or NULL
+ * for ones.  strides: q, k, qo, ko.  Sums in fp32, one rounding at the end.  k
+ * and ko may be NULL (queries only).  qo may be q and ko may be k, with the same
+ * strides. */
+elsaa_status elsaa_rotary_forward(const elsaa_rotary_params* p, const void* q, const void* k,
+                                  const int64_t* strides, const int32_t* positions,
+                                  const float* table, const float* q_weight,
+                                  const float* k_weight, void* qo, void* ko, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Gradients of sum(qo * dqo) + sum(ko * dko): dq, dk in the data dtype, dq_weight
+ * and dk_weight device fp32 [d] (with norm; either may be NULL), all
+ * overwritten.  strides: q, k, dqo, dko, dq, dk.  The weights' sums run in a
+ * fixed order: the same inputs give the same bits.  dq may be dqo and dk may
+ * be dko, with the same strides.  k, dko and dk may be NULL together. */
+elsaa_status elsaa_rotary_backward(const elsaa_rotary_params* p, const void* q, const void* k,
+                                   const int64_t* strides, const int32_t* positions,
+                                   const float* table, const float* q_weight,
+                                   const float* k_weight, const void* dqo, const void* dko,
+                                   void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t B, H, Hkv, N, d;   /* d in {32, 64, 128} */
+  int32_t dtype;             /* elsaa_dtype of q, k, v, y and the gradients */
+  int32_t window;            /* keys a query sees up to and with its own; 0: all of them */
+  int32_t sinks;             /* first tokens that stay visible, >= 0 */
+  float scale;               /* <= 0: 1 / sqrt(d) */
+} elsaa_window_params;
+
+elsaa_status elsaa_window_validate(const elsaa_window_params* p);
+/* Bytes that forward (backward = 0) or forward and backward (1) need. */
+size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backward);
+
+/* y = softmax(scale q k^T) v over the keys j <= i with i - j < window or
+ * j < sinks.  lengths: device int32 [B] of a padded batch's token counts
+ * (clamped to [0, N]), or NULL for N: rows at or behind a length are read into
+ * no result, whatever they hold, and their y is zero and lse -inf.  Values that
+ * are not finite within a length are outside the contract (0 * inf in a masked
+ * place).  lse: device fp32 [B, H, N] dense, the log of the row's sum of
+ * exponentials.  strides: q, k, v, y. */
+elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, const void* k,
+                                  const void* v, const int64_t* strides, const int32_t* lengths,
+                                  void* y, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum(y * dy) from the y and lse of a forward with the same
+ * inputs; all overwritten, zeros at and behind a length.  No atomics: the same
+ * inputs give the same bits.  strides: q, k, v, y, dy, dq, dk, dv. */
+elsaa_status elsaa_window_backward(const elsaa_window_params* p, const void* q, const void* k,
+                                   const void* v, const int64_t* strides, const int32_t* lengths,
+                                   const void* y, const float* lse, const void* dy, void* dq,
+                                   void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t seqs;              /* sequences S */
+  int32_t rows;              /* rows T of q (at least starts[S]) */
+  int32_t H, Hkv, d;         /* d in {32, 64, 128}; H / Hkv at most 64 */
+  int32_t dtype;             /* elsaa_dtype of q, k, v, y and the pages */
+  int32_t page_size;         /* tokens of a page: a multiple of 16 */
+  int32_t pages;             /* pages of the pool */
+  int32_t table_width;       /* page table entries of a sequence */
+  int32_t window, sinks;     /* as in elsaa_window_params */
+  float scale;               /* <= 0: 1 / sqrt(d) */
+} elsaa_paged_params;
+
+elsaa_status elsaa_paged_validate(const elsaa_paged_params* p);
+size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p);
+
+/* The new tokens of sequence b are rows starts[b] .. starts[b + 1] - 1 of q
+ * [T, H, d], and the last of the lengths[b] tokens of its context: token t of
+ * n has position lengths[b] - n + t.  starts: device int32 [S + 1], never
+ * falling, starts[0] = 0.  lengths: device int32 [S], with the new tokens.
+ * k_pages, v_pages: [pages, Hkv, page_size, d]; token j of sequence b lies in
+ * page page_table[b][j / page_size] (device int32 [S, table_width]), slot
+ * j % page_size.  Entries that no token of the call needs are not read: behind
+ * the length, and before every new token's window and behind the sinks.  A
+ * needed entry that is no page, or a length that does not fit, is recorded
+ * (DEVICE_CHECK); such a page reads as zeros and is never written.  Rows of q
+ * from starts[S] on belong to no sequence.
+ * strides: q, q_out, k, v as (row, head); page_strides: k_pages, v_pages as
+ * (page, head, slot); host arrays of element strides or NULL for dense. */
+
+/* The serving form of elsaa_rotary_forward: norms and rotates the new tokens'
+ * q into q_out and k into the pages, and copies v into the pages (r->H, r->Hkv,
+ * r->d and r->dtype equal p's; r->B and r->N are not used).  Two tokens of one
+ * call must not share a slot. */
+elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_params* r,
+                               const void* q, const void* k, const void* v,
+                               const int64_t* strides, const float* table,
+                               const float* q_weight, const float* k_weight, void* q_out,
+                               void* k_pages, void* v_pages, const int64_t* page_strides,
+                               const int32_t* page_table, const int32_t* starts,
+                               const int32_t* lengths, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the new tokens over the cache, their own keys and values
+ * already written: the serving form of elsaa_window_forward, for any number of
+ * new tokens a sequence.  strides: q, y as (row, head).  Rows from starts[S] on
+ * are left as they were. */
+elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
+                                const int64_t* strides, const void* k_pages, const void* v_pages,
+                                const int64_t* page_strides, const int32_t* page_table,
+                                const int32_t* starts, const int32_t* lengths, void* y, void* ws,
+                                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

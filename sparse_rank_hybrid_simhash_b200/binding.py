@@ -78,7 +78,11 @@ EXPORTS = ("elsaa_validate", "elsaa_workspace_bytes", "elsaa_saved_bytes", "elsa
            "elsaa_kernel_launches", "elsaa_saved_views", "elsaa_check", "elsaa_status_str",
            "elsaa_uses_tensor_cores", "elsaa_sort_codes_noalloc", "elsaa_path_flags",
            "elsaa_sort_codes_of", "elsaa_sort_codes", "elsaa_race_tables", "elsaa_forward_tables",
-           "elsaa_backward_tables", "elsaa_race_value_grad")
+           "elsaa_backward_tables", "elsaa_race_value_grad", "elsaa_rotary_validate",
+           "elsaa_rotary_workspace_bytes", "elsaa_rotary_forward", "elsaa_rotary_backward",
+           "elsaa_window_validate", "elsaa_window_workspace_bytes", "elsaa_window_forward",
+           "elsaa_window_backward", "elsaa_paged_validate", "elsaa_paged_workspace_bytes",
+           "elsaa_paged_write", "elsaa_paged_attend")
 # elsaa_path_flags bits
 PATH_FLAGS = {"tc_hash": 1, "tc_attn": 2, "slab_fwd": 4, "slab_bwd": 8, "tc_win": 16}
 FWD_STAGES = ("hash", "sort", "race_build", "sparse_fwd", "race_fuse")
@@ -132,6 +136,22 @@ def lib() -> ctypes.CDLL:
     L.elsaa_saved_views.restype = st
     L.elsaa_check.argtypes, L.elsaa_check.restype = [vp, vp], st
     L.elsaa_status_str.argtypes, L.elsaa_status_str.restype = [st], ctypes.c_char_p
+    # the operators next to ELSAA (rotary.py, window.py, paged.py); vp: their parameter structs
+    i64p = ctypes.POINTER(ctypes.c_int64)
+    for kind in ("rotary", "window", "paged"):
+        f = getattr(L, f"elsaa_{kind}_validate")
+        f.argtypes, f.restype = [vp], st
+        f = getattr(L, f"elsaa_{kind}_workspace_bytes")
+        f.argtypes, f.restype = [vp] + ([ctypes.c_int32] if kind == "window" else []), sz
+    L.elsaa_rotary_forward.argtypes = [vp] * 3 + [i64p] + [vp] * 7 + [sz, vp]
+    L.elsaa_rotary_backward.argtypes = [vp] * 3 + [i64p] + [vp] * 11 + [sz, vp]
+    L.elsaa_window_forward.argtypes = [vp] * 4 + [i64p] + [vp] * 4 + [sz, vp]
+    L.elsaa_window_backward.argtypes = [vp] * 4 + [i64p] + [vp] * 8 + [sz, vp]
+    L.elsaa_paged_write.argtypes = [vp] * 5 + [i64p] + [vp] * 6 + [i64p] + [vp] * 4 + [sz, vp]
+    L.elsaa_paged_attend.argtypes = [vp] * 2 + [i64p] + [vp] * 2 + [i64p] + [vp] * 5 + [sz, vp]
+    for name in ("rotary_forward", "rotary_backward", "window_forward", "window_backward",
+                 "paged_write", "paged_attend"):
+        getattr(L, f"elsaa_{name}").restype = st
     _lib = L
     return L
 
@@ -405,6 +425,9 @@ class ElsaaFunction(torch.autograd.Function):
         return dq, dk, dv, dgw, dgb, dlam.view_as(lam), None, None, None
 
 
-def elsaa(q, k, v, gate_w, gate_b, lam, r_sort, r_race, params: Params):
-    """Differentiable ELSAA attention on [B, H, N, d] CUDA tensors."""
+def elsaa(q, k, v, gate_w, gate_b, lam, r_sort, r_race, params: Params, rotary=None):
+    """Differentiable ELSAA attention on [B, H, N, d] CUDA tensors.  ``rotary`` (a
+    rotary.QkRotary): q and k are normed and rotated first."""
+    if rotary is not None:
+        q, k = rotary.apply(q, k)
     return ElsaaFunction.apply(q, k, v, gate_w, gate_b, lam, r_sort, r_race, params)

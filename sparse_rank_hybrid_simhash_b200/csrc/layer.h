@@ -1,0 +1,84 @@
+// Host-side problem descriptions of the operators next to ELSAA (norm and
+// rotation, window attention, the paged cache) and the launchers each .cu file
+// provides.  Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/elsaa.h"
+
+namespace elsaa {
+
+// Element strides of a [batch, heads, tokens, d] tensor (d contiguous).
+struct Strides {
+  int64_t b, h, n;
+};
+
+// ---- norm and rotation -------------------------------------------------------
+
+// Most blocks that leave a partial sum of a weight's gradient (queries' and
+// keys' together): a fixed number, so the summation order is fixed.
+constexpr int kRotaryPartials = 1184;
+
+struct RotaryArgs {
+  const void *q, *k;
+  void *qo, *ko;              // outputs (forward), dq and dk (backward)
+  const void *dqo, *dko;      // backward
+  Strides sq, sk, sqo, sko, sdqo, sdko;
+  const int32_t* positions;   // [B, N] or null
+  const float* table;         // [max_pos, rot / 2, 2]
+  const float *wq, *wk;       // [d] or null
+  float *dwq, *dwk;           // [d] or null
+  float* partials;            // [kRotaryPartials][d]
+  uint32_t* err;
+  int B, H, Hkv, N, rot, norm, max_pos;
+  float eps;
+  // the write into pages
+  const void* v;
+  Strides sv;
+  void *k_pages, *v_pages;
+  Strides skp, svp;           // (page, head, slot)
+  const int32_t *page_table, *starts, *lengths;
+  int seqs, page_size, pages, table_width;
+};
+
+cudaError_t launch_rotary_forward(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                                  cudaStream_t s);
+cudaError_t launch_rotary_backward(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                                   cudaStream_t s);
+cudaError_t launch_paged_write(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                               cudaStream_t s);
+
+// ---- attention ---------------------------------------------------------------
+
+struct AttendArgs {
+  const void *q, *k, *v;
+  void* y;
+  float* lse;                 // [B, H, N] (window forward, backward)
+  const void* dy;
+  void *dq, *dk, *dv;
+  Strides sq, sk, sv, sy, sdy, sdq, sdk, sdv;   // pages: sk, sv are (page, head, slot)
+  const int32_t* lengths;     // window: [B] or null; pages: [S]
+  int B, H, Hkv, N, d, g;     // g = H / Hkv
+  int window;                 // INT32_MAX: no limit
+  int sinks;
+  float scale;
+  uint32_t* err;
+  float* delta;               // [B, H, N]: rowsum(y dy) (backward)
+  // pages
+  const int32_t *page_table, *starts;
+  int seqs, rows, page_size, pages, table_width;
+  char* scratch;              // split partials
+};
+
+// CUDA-core kernels: every type and head dim.
+cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
+
+}  // namespace elsaa

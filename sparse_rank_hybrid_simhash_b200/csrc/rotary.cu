@@ -1,0 +1,450 @@
+// RMS norm of query and key rows and the position rotation, in one pass, with
+// the gradients, and their serving form that writes keys and values into the
+// pages of a cache.
+//
+// A row x of d values:  n = x r,  r = 1 / sqrt(mean(x^2) + eps),  u = n w, and
+// for each of its rot / 2 pairs (a, b) with the angle of (position, pair)
+//   y_a = u_a cos - u_b sin,   y_b = u_b cos + u_a sin.
+// Backward: du is the transposed rotation of dy, dw = sum over rows of du n,
+// dn = du w, dx = r (dn - n mean(dn n)).
+//
+// Bound: HBM, each row read once and written once (backward: x and dy read, dx
+// written).  A row is held by a group of d / V lanes with one 16-byte load each
+// (V = 8 bf16 or 4 fp32 values), so the sums are shuffles within the group; in
+// halves a lane's partner values sit rot / (2 V) lanes away.  A group keeps its
+// token's cos and sin in registers and walks several heads of that token,
+// so the table (8 rot / 2 bytes a token, more than a bf16 row) is read once per
+// head chunk, not per head.
+#include "common.cuh"
+#include "internal.h"
+#include "layer.h"
+
+namespace elsaa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStarts = 2048;   // sequence starts kept in shared memory
+
+template <typename T>
+struct Vec {
+  static constexpr int V = 16 / sizeof(T);
+};
+
+ELSAA_DEV void load_row(const float* p, float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+ELSAA_DEV void load_row(const __nv_bfloat16* p, float* x) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+ELSAA_DEV void store_row(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+ELSAA_DEV void store_row(__nv_bfloat16* p, const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sum over the lane group of a row.
+template <int LANES>
+ELSAA_DEV float group_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The angles of a lane's V values: cos[i], sin[i] of value i's pair (in
+// halves), or of pair i / 2 in cos[i / 2] (interleaved).  Lanes past the
+// rotated part get (1, 0).
+template <int V, bool IL>
+struct Angles {
+  static constexpr int C = IL ? V / 2 : V;
+  float cs[C], sn[C];
+};
+template <int V, bool IL>
+ELSAA_DEV Angles<V, IL> load_angles(const float* row, int col, int rot) {
+  Angles<V, IL> a;
+  constexpr int C = Angles<V, IL>::C;
+#pragma unroll
+  for (int i = 0; i < C; ++i) a.cs[i] = 1.f, a.sn[i] = 0.f;
+  if (col < rot) {
+    const int first = IL ? col / 2 : (col < rot / 2 ? col : col - rot / 2);
+#pragma unroll
+    for (int i = 0; i < C; i += 2) {
+      const float4 t = *reinterpret_cast<const float4*>(row + 2 * (first + i));
+      a.cs[i] = t.x, a.sn[i] = t.y, a.cs[i + 1] = t.z, a.sn[i + 1] = t.w;
+    }
+  }
+  return a;
+}
+
+// u rotated in place (BACK: by the transposed rotation).  Every lane of the
+// warp takes part.
+template <int V, bool IL, bool BACK, int LANES>
+ELSAA_DEV void rotate(float* u, const Angles<V, IL>& a, int col, int rot) {
+  if (IL) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float c = a.cs[i / 2], s = BACK ? -a.sn[i / 2] : a.sn[i / 2];
+      const float x = u[i], y = u[i + 1];
+      u[i] = x * c - y * s;
+      u[i + 1] = y * c + x * s;
+    }
+  } else {
+    const int hop = rot / (2 * V);
+    const bool low = col < rot / 2, in = col < rot;
+    const int lane = threadIdx.x & 31;
+    const int from = !in ? lane : low ? lane + hop : lane - hop;
+    // the value a adds -sin b, the value b adds +sin a; both signs turn in BACK
+    const float sign = low != BACK ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float other = __shfl_sync(0xffffffffu, u[i], from);
+      u[i] = u[i] * a.cs[i] + sign * other * a.sn[i];
+    }
+  }
+}
+
+// Forward of one row (in x, out in x): norm, weight, rotation.
+template <int D, int V, bool IL>
+ELSAA_DEV void row_forward(float* x, const float* w, const Angles<V, IL>& a, int col,
+                           const RotaryArgs& g) {
+  constexpr int LANES = D / V;
+  if (g.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss += x[i] * x[i];
+    ss = group_sum<LANES>(ss);
+    const float r = 1.0f / sqrtf(ss * (1.0f / D) + g.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = x[i] * r * w[i];
+  }
+  rotate<V, IL, false, LANES>(x, a, col, g.rot);
+}
+
+template <int V>
+ELSAA_DEV void load_weight(const float* w, int col, float* out) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = w ? __ldg(w + col + i) : 1.f;
+}
+
+// The table row of a token's position; null (recorded) where it is none.
+ELSAA_DEV const float* table_row(const RotaryArgs& a, int pos, bool lead) {
+  if (a.rot == 0) return a.table;
+  if (pos < 0 || pos >= a.max_pos) {
+    if (lead) raise_error(a.err, ERR_CHECK);
+    return nullptr;
+  }
+  return a.table + (int64_t)pos * a.rot;
+}
+
+// blockIdx.y: chunks of HP query heads, then of HP key heads.
+template <typename T, int D, bool IL>
+__global__ void __launch_bounds__(kThreads)
+norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
+  constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
+  const int col = (threadIdx.x % LANES) * V;
+  const int64_t tok = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+  const bool live = tok < (int64_t)a.B * a.N;
+  const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok % a.N) : 0;
+  const bool is_q = (int)blockIdx.y < q_chunks;
+  const int h0 = (is_q ? blockIdx.y : blockIdx.y - q_chunks) * hp;
+  const int h1 = min(h0 + hp, is_q ? a.H : a.Hkv);
+  const Strides si = is_q ? a.sq : a.sk, so = is_q ? a.sqo : a.sko;
+  const T* in = static_cast<const T*>(is_q ? a.q : a.k) + b * si.b + n * si.n + col;
+  T* out = static_cast<T*>(is_q ? a.qo : a.ko) + b * so.b + n * so.n + col;
+  const int pos = a.positions && live ? a.positions[tok] : n;
+  const float* tab = table_row(a, pos, live && col == 0);
+  const bool ok = a.rot == 0 || tab != nullptr;
+  Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
+  float w[V];
+  load_weight<V>(is_q ? a.wq : a.wk, col, w);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+    if (live) load_row(in + h * si.h, x);
+    row_forward<D, V, IL>(x, w, ang, col, a);
+    if (!ok)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = 0.f;
+    if (live) store_row(out + h * so.h, x);
+  }
+}
+
+// Backward: blocks [0, q_blocks) walk (token group, head chunk) items of the
+// queries, the rest those of the keys; each block leaves one partial sum of
+// its weight's gradient.
+template <typename T, int D, bool IL>
+__global__ void __launch_bounds__(kThreads)
+norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
+  constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
+  const int col = (threadIdx.x % LANES) * V;
+  const bool is_q = (int)blockIdx.x < q_blocks;
+  const int heads = is_q ? a.H : a.Hkv;
+  const int chunks = (heads + hp - 1) / hp;
+  const int64_t groups = ((int64_t)a.B * a.N + ROWS - 1) / ROWS;
+  const int64_t items = groups * chunks;
+  const int first = is_q ? blockIdx.x : blockIdx.x - q_blocks;
+  const int step = is_q ? q_blocks : gridDim.x - q_blocks;
+  const Strides si = is_q ? a.sq : a.sk, sg = is_q ? a.sdqo : a.sdko, so = is_q ? a.sqo : a.sko;
+  float w[V], dw[V];
+  load_weight<V>(is_q ? a.wq : a.wk, col, w);
+#pragma unroll
+  for (int i = 0; i < V; ++i) dw[i] = 0.f;
+  for (int64_t it = first; it < items; it += step) {
+    const int64_t tok = it / chunks * ROWS + threadIdx.x / LANES;
+    const int h0 = (int)(it % chunks) * hp, h1 = min(h0 + hp, heads);
+    const bool live = tok < (int64_t)a.B * a.N;
+    const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok % a.N) : 0;
+    const T* in = static_cast<const T*>(is_q ? a.q : a.k) + b * si.b + n * si.n + col;
+    const T* dy = static_cast<const T*>(is_q ? a.dqo : a.dko) + b * sg.b + n * sg.n + col;
+    T* out = static_cast<T*>(is_q ? a.qo : a.ko) + b * so.b + n * so.n + col;
+    const int pos = a.positions && live ? a.positions[tok] : n;
+    const float* tab = table_row(a, pos, live && col == 0);
+    const bool ok = a.rot == 0 || tab != nullptr;
+    const Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
+#pragma unroll 2
+    for (int h = h0; h < h1; ++h) {
+      float x[V], g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = g[i] = 0.f;
+      if (live && ok) {   // (a row without a position was written as zeros: no gradient)
+        load_row(in + h * si.h, x);
+        load_row(dy + h * sg.h, g);
+      }
+      rotate<V, IL, true, LANES>(g, ang, col, a.rot);
+      if (a.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss += x[i] * x[i];
+        ss = group_sum<LANES>(ss);
+        const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          x[i] *= r;
+          if (ok) dw[i] += g[i] * x[i];
+          g[i] *= w[i];
+          dot += g[i] * x[i];
+        }
+        dot = group_sum<LANES>(dot) * (1.0f / D);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = ok ? r * (g[i] - x[i] * dot) : 0.f;
+      }
+      if (live) store_row(out + h * so.h, g);
+    }
+  }
+  if ((is_q ? a.dwq : a.dwk) == nullptr) return;
+  // the block's sum, lane groups in order
+  __shared__ float part[ROWS][D + 1];
+#pragma unroll
+  for (int i = 0; i < V; ++i) part[threadIdx.x / LANES][col + i] = dw[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float s = 0.f;
+    for (int r = 0; r < ROWS; ++r) s += part[r][threadIdx.x];
+    a.partials[(int64_t)blockIdx.x * D + threadIdx.x] = s;
+  }
+}
+
+// dw of the queries (block y = 0) and keys (1): 32 columns a block, warps over
+// the partials in a fixed order, in 64 bits.
+__global__ void __launch_bounds__(kThreads)
+weight_reduce_kernel(const RotaryArgs a, int d, int q_blocks, int blocks) {
+  const bool is_q = blockIdx.y == 0;
+  float* to = is_q ? a.dwq : a.dwk;
+  if (to == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const int lo = is_q ? 0 : q_blocks, hi = is_q ? q_blocks : blocks;
+  double s = 0.0;
+  for (int r = lo + warp; r < hi; r += kThreads / 32) s += (double)a.partials[(int64_t)r * d + c];
+  __shared__ double part[kThreads / 32][32];
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0) {
+    for (int i = 1; i < kThreads / 32; ++i) s += part[i][lane];
+    to[c] = (float)s;
+  }
+}
+
+// The write into the cache: blockIdx.y walks chunks of hp query heads, key
+// heads and value heads.
+template <typename T, int D, bool IL>
+__global__ void __launch_bounds__(kThreads)
+paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
+  constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
+  __shared__ int32_t first[kStarts + 1];
+  const bool cached = a.seqs <= kStarts;
+  if (cached) {
+    for (int i = threadIdx.x; i <= a.seqs; i += kThreads) first[i] = a.starts[i];
+    __syncthreads();
+  }
+  const int32_t* st = cached ? first : a.starts;
+  const int col = (threadIdx.x % LANES) * V;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+  const int end = min(st[a.seqs], a.N);
+  const bool live = row < end;
+  // the last sequence that starts at or before the row (empty ones share a start)
+  int lo = 0, hi = a.seqs - 1;
+  while (live && lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (st[mid] <= row) lo = mid; else hi = mid - 1;
+  }
+  const int seq = lo;
+  const int len = live ? a.lengths[seq] : 0;
+  const int pos = live ? len - st[seq + 1] + (int)row : 0;
+  const int kind = (int)blockIdx.y < q_chunks ? 0 : (int)blockIdx.y < q_chunks + k_chunks ? 1 : 2;
+  const int y = blockIdx.y - (kind == 0 ? 0 : kind == 1 ? q_chunks : q_chunks + k_chunks);
+  const int h0 = y * hp, h1 = min(h0 + hp, kind == 0 ? a.H : a.Hkv);
+  // keys and values: the token's page and slot, checked before anything is written
+  int64_t page = -1;
+  bool ok = live && pos >= 0 && pos < len && len <= (int64_t)a.page_size * a.table_width;
+  if (ok && kind != 0) {
+    page = a.page_table[(int64_t)seq * a.table_width + pos / a.page_size];
+    ok = page >= 0 && page < a.pages;
+  }
+  if (live && !ok && col == 0) raise_error(a.err, ERR_CHECK);
+  const int slot = ok ? pos % a.page_size : 0;
+  if (kind == 2) {
+    const T* in = static_cast<const T*>(a.v) + row * a.sv.n + col;
+    T* out = static_cast<T*>(a.v_pages) + page * a.svp.b + slot * a.svp.n + col;
+    if (ok)
+#pragma unroll 4
+      for (int h = h0; h < h1; ++h)
+        *reinterpret_cast<uint4*>(out + h * a.svp.h) =
+            *reinterpret_cast<const uint4*>(in + h * a.sv.h);
+    return;
+  }
+  const Strides si = kind == 0 ? a.sq : a.sk;
+  const T* in = static_cast<const T*>(kind == 0 ? a.q : a.k) + row * si.n + col;
+  T* out = kind == 0 ? static_cast<T*>(a.qo) + row * a.sqo.n + col
+                     : static_cast<T*>(a.k_pages) + page * a.skp.b + slot * a.skp.n + col;
+  const int64_t oh = kind == 0 ? a.sqo.h : a.skp.h;
+  const float* tab = ok ? table_row(a, pos, col == 0) : nullptr;
+  const bool pos_ok = ok && (a.rot == 0 || tab != nullptr);
+  const Angles<V, IL> ang = load_angles<V, IL>(tab, pos_ok ? col : D, pos_ok ? a.rot : 0);
+  float w[V];
+  load_weight<V>(kind == 0 ? a.wq : a.wk, col, w);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+    if (pos_ok) load_row(in + h * si.h, x);
+    row_forward<D, V, IL>(x, w, ang, col, a);
+    if (!pos_ok)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = 0.f;
+    // a query row without a position is zeros; a key row is written with a page only
+    if (kind == 0 ? live : ok) store_row(out + h * oh, x);
+  }
+}
+
+// Heads that a lane group walks: as many as keep the card filled (148 SMs x
+// 2048 threads), at most 8.
+int head_chunk(int64_t tokens, int lanes, int heads) {
+  int hp = 8;
+  while (hp > 1 && tokens * lanes * ((heads + hp - 1) / hp) < (int64_t)148 * 2048) hp >>= 1;
+  return hp;
+}
+
+template <typename F>
+cudaError_t by_shape(int d, bool bf16, bool il, F&& f) {
+#define ELSAA_ROW(T, D)                                         \
+  return il ? f.template operator()<T, D, true>() : f.template operator()<T, D, false>()
+  if (bf16) {
+    if (d == 32) ELSAA_ROW(__nv_bfloat16, 32);
+    if (d == 64) ELSAA_ROW(__nv_bfloat16, 64);
+    ELSAA_ROW(__nv_bfloat16, 128);
+  }
+  if (d == 32) ELSAA_ROW(float, 32);
+  if (d == 64) ELSAA_ROW(float, 64);
+  ELSAA_ROW(float, 128);
+#undef ELSAA_ROW
+}
+
+struct Forward {
+  const RotaryArgs& a;
+  cudaStream_t s;
+  template <typename T, int D, bool IL>
+  cudaError_t operator()() const {
+    constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
+    const int64_t tokens = (int64_t)a.B * a.N;
+    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
+    const int qc = (a.H + hp - 1) / hp, kc = (a.Hkv + hp - 1) / hp;
+    const dim3 grid((unsigned)((tokens + ROWS - 1) / ROWS), qc + kc);
+    norm_rotate_kernel<T, D, IL><<<grid, kThreads, 0, s>>>(a, hp, qc);
+    return cudaGetLastError();
+  }
+};
+
+struct Backward {
+  const RotaryArgs& a;
+  cudaStream_t s;
+  template <typename T, int D, bool IL>
+  cudaError_t operator()() const {
+    constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
+    const int64_t tokens = (int64_t)a.B * a.N, groups = (tokens + ROWS - 1) / ROWS;
+    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
+    const int64_t qi = groups * ((a.H + hp - 1) / hp), ki = groups * ((a.Hkv + hp - 1) / hp);
+    // blocks by the share of the items, all resident at once (4 x 148, at most two waves)
+    const int64_t cap = kRotaryPartials;
+    int64_t qb = qi, kb = ki;
+    if (qi + ki > cap) {
+      qb = cap * qi / (qi + ki);
+      qb = qb < 1 ? 1 : qb;
+      kb = a.Hkv ? (cap - qb < 1 ? 1 : cap - qb) : 0;
+      if (qb + kb > cap) qb = cap - kb;
+    }
+    norm_rotate_back_kernel<T, D, IL><<<(unsigned)(qb + kb), kThreads, 0, s>>>(a, hp, (int)qb);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;
+    weight_reduce_kernel<<<dim3(D / 32, 2), kThreads, 0, s>>>(a, D, (int)qb, (int)(qb + kb));
+    return cudaGetLastError();
+  }
+};
+
+struct Write {
+  const RotaryArgs& a;
+  cudaStream_t s;
+  template <typename T, int D, bool IL>
+  cudaError_t operator()() const {
+    constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
+    const int hp = head_chunk(a.N, LANES, a.H + 2 * a.Hkv);
+    const int qc = (a.H + hp - 1) / hp, kc = (a.Hkv + hp - 1) / hp;
+    const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS), qc + 2 * kc);
+    paged_write_kernel<T, D, IL><<<grid, kThreads, 0, s>>>(a, hp, qc, kc);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_rotary_forward(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                                  cudaStream_t s) {
+  return by_shape(d, bf16, interleaved, Forward{a, s});
+}
+cudaError_t launch_rotary_backward(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                                   cudaStream_t s) {
+  return by_shape(d, bf16, interleaved, Backward{a, s});
+}
+cudaError_t launch_paged_write(const RotaryArgs& a, int d, bool bf16, bool interleaved,
+                               cudaStream_t s) {
+  return by_shape(d, bf16, interleaved, Write{a, s});
+}
+
+}  // namespace elsaa

@@ -1,0 +1,145 @@
+"""What rotary.py, window.py and paged.py share: argument checks, strides and
+the call into libelsaa on the tensors' own device."""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from . import binding
+from .binding import ELSAA_BF16, ELSAA_F32
+
+_TORCH = {ELSAA_BF16: torch.bfloat16, ELSAA_F32: torch.float32}
+
+
+def dtype_code(dtype) -> int:
+    """elsaa_dtype of "bf16" / "f32" or the torch dtype."""
+    if dtype in ("bf16", torch.bfloat16):
+        return ELSAA_BF16
+    if dtype in ("f32", torch.float32):
+        return ELSAA_F32
+    raise TypeError(f"dtype must be bf16 or f32, got {dtype}")
+
+
+def torch_dtype(code: int) -> torch.dtype:
+    return _TORCH[code]
+
+
+def alloc_workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace whose error word is clear (later calls only ever set it)."""
+    if nbytes == 0:
+        raise ValueError("not a valid problem")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def check(where: str, t: Optional[torch.Tensor], shape: Sequence[int], dtype: torch.dtype,
+          device: torch.device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{where}: on {t.device}, expected {device}")
+
+
+def strided(t: torch.Tensor) -> bool:
+    """Whether the library takes the tensor where it lies: the last dimension
+    contiguous, the other strides positive multiples of 16 bytes that no two
+    rows share, the start on 16 bytes."""
+    if t.is_contiguous():
+        return t.data_ptr() & 15 == 0
+    e, d = t.element_size(), t.shape[-1]
+    if t.stride(-1) != 1 or t.data_ptr() & 15:
+        return False
+    return all(n == 1 or (s >= d and s * e % 16 == 0)
+               for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+
+
+def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
+    """The checked tensor, or a dense copy of one the library does not take
+    where it lies (a broadcast one, an odd stride or offset)."""
+    check(where, t, shape, dtype, device)
+    if strided(t):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    check(where, t, shape, dtype, device)
+    if not strided(t):
+        raise ValueError(f"{where}: an output needs a contiguous last dimension and strides and "
+                         "a start that are multiples of 16 bytes")
+    return t
+
+
+def as_small(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> Optional[torch.Tensor]:
+    """An optional dense int32 / fp32 tensor."""
+    if t is None:
+        return None
+    check(where, t, shape, dtype, device)
+    t = t.contiguous()
+    return t if t.data_ptr() & 15 == 0 else t.clone()
+
+
+def as_workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if ws is None:
+        return alloc_workspace(nbytes, device)
+    if ws.device != device:
+        raise ValueError(f"ws: on {ws.device}, expected {device}")
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous uint8 tensor")
+    return ws
+
+
+def strides_of(dims: int, *tensors: Optional[torch.Tensor]):
+    """Host array of the first `dims` strides of every tensor, or None where
+    all are dense."""
+    if all(t is None or t.is_contiguous() for t in tensors):
+        return None
+    flat = []
+    for t in tensors:
+        flat += [0] * dims if t is None else t.stride()[:dims]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class on:
+    """Makes the tensors' device current and, where a stream is given, makes it
+    the one that allocations inside belong to."""
+
+    __slots__ = ("stream", "guards")
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        self.guards = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self.guards.append(torch.cuda.stream(stream))
+        self.stream = stream
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return (self.stream or torch.cuda.current_stream()).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def ok(where: str, code: int) -> None:
+    if code != 0:
+        raise binding.ElsaaError(where, code)

@@ -1,0 +1,123 @@
+"""Exact causal attention over a sliding window of tokens with sinks, forward and
+backward.
+
+Query i sees the keys j <= i with i - j < window (0: all of them) or j < sinks.
+Hkv key heads serve H query heads (query head h reads key head h // (H // Hkv)).
+A padded batch gives its ``lengths``: rows at or behind a length take part in
+nothing, their output and gradients are zero and their lse is -inf.  ``forward``
+and ``backward`` take caller-owned outputs and workspace; ``window_attention`` is
+differentiable.  The serving form over a paged cache is ``paged.attend``.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Tuple
+
+import torch
+
+from . import layer
+from .binding import lib
+
+
+class WindowParams(ctypes.Structure):
+    """Mirror of ``elsaa_window_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "Hkv", "N", "d", "dtype", "window",
+                                              "sinks")] + [("scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, B, H, Hkv, N, d, dtype, window=0, sinks=0, scale=0.0) -> "WindowParams":
+        return cls(B, H, Hkv, N, d, layer.dtype_code(dtype), window, sinks, float(scale))
+
+
+def validate(p: WindowParams) -> int:
+    return lib().elsaa_window_validate(ctypes.byref(p))
+
+
+def workspace_bytes(p: WindowParams, backward: bool = True) -> int:
+    return lib().elsaa_window_workspace_bytes(ctypes.byref(p), int(backward))
+
+
+def alloc_workspace(p: WindowParams, device, backward: bool = True) -> torch.Tensor:
+    return layer.alloc_workspace(workspace_bytes(p, backward), device)
+
+
+def _shapes(p: WindowParams):
+    return (p.B, p.H, p.N, p.d), (p.B, p.Hkv, p.N, p.d)
+
+
+def forward(p: WindowParams, q, k, v, lengths=None, y=None, lse=None, ws=None,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(y [B, H, N, d], lse [B, H, N] fp32).  Views of q, k, v, y with other strides are taken
+    in place."""
+    dev, dt = q.device, layer.torch_dtype(p.dtype)
+    sq, sk = _shapes(p)
+    with layer.on(dev, stream) as st:
+        q = layer.as_input("q", q, sq, dt, dev)
+        k = layer.as_input("k", k, sk, dt, dev)
+        v = layer.as_input("v", v, sk, dt, dev)
+        y = layer.as_output("y", y, sq, dt, dev)
+        if lse is None:
+            lse = torch.empty(sq[:3], dtype=torch.float32, device=dev)
+        layer.check("lse", lse, sq[:3], torch.float32, dev)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+        ws = layer.as_workspace(ws, workspace_bytes(p, False), dev)
+        ptr = layer.ptr
+        layer.ok("elsaa_window_forward", lib().elsaa_window_forward(
+            ctypes.byref(p), ptr(q), ptr(k), ptr(v), layer.strides_of(3, q, k, v, y), ptr(lengths),
+            ptr(y), ptr(lse), ptr(ws), ws.numel(), st))
+    return y, lse
+
+
+def backward(p: WindowParams, q, k, v, y, lse, dy, lengths=None, dq=None, dk=None, dv=None,
+             ws=None, stream=None):
+    """(dq, dk, dv) of sum(y * dy), from the y and lse of ``forward`` on the same inputs."""
+    dev, dt = q.device, layer.torch_dtype(p.dtype)
+    sq, sk = _shapes(p)
+    with layer.on(dev, stream) as st:
+        q = layer.as_input("q", q, sq, dt, dev)
+        k = layer.as_input("k", k, sk, dt, dev)
+        v = layer.as_input("v", v, sk, dt, dev)
+        y = layer.as_input("y", y, sq, dt, dev)
+        dy = layer.as_input("dy", dy, sq, dt, dev)
+        layer.check("lse", lse, sq[:3], torch.float32, dev)
+        lse = lse.contiguous()
+        dq = layer.as_output("dq", dq, sq, dt, dev)
+        dk = layer.as_output("dk", dk, sk, dt, dev)
+        dv = layer.as_output("dv", dv, sk, dt, dev)
+        lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+        ws = layer.as_workspace(ws, workspace_bytes(p, True), dev)
+        ptr = layer.ptr
+        layer.ok("elsaa_window_backward", lib().elsaa_window_backward(
+            ctypes.byref(p), ptr(q), ptr(k), ptr(v),
+            layer.strides_of(3, q, k, v, y, dy, dq, dk, dv), ptr(lengths), ptr(y), ptr(lse),
+            ptr(dy), ptr(dq), ptr(dk), ptr(dv), ptr(ws), ws.numel(), st))
+    return dq, dk, dv
+
+
+class WindowFunction(torch.autograd.Function):
+    """Autograd wrapper: forward and backward both run in libelsaa."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lengths, params: WindowParams):
+        y, lse = forward(params, q, k, v, lengths)
+        ctx.params = params
+        ctx.save_for_backward(q, k, v, y, lse, lengths)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        q, k, v, y, lse, lengths = ctx.saved_tensors
+        return (*backward(ctx.params, q, k, v, y, lse, dy, lengths), None, None)
+
+
+def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0):
+    """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d]."""
+    B, H, N, d = q.shape
+    if k.dim() != 4:
+        raise ValueError("k must be [B, Hkv, N, d]")
+    p = WindowParams.make(B, H, k.shape[1], N, d, q.dtype, window, sinks, scale)
+    return WindowFunction.apply(q, k, v, lengths, p)
