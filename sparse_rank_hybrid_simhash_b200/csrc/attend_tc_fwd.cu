@@ -1,0 +1,976 @@
+// Causal attention over a sliding window with sinks, and over a paged cache, on
+// the tensor cores (bf16, d = 64 or 128): a persistent warp-specialized tcgen05
+// pipeline, one pass over the keys with the running maximum and sum.
+//
+// Two streams of 128 query rows share every 128-key block of K and V: S = Q K^T
+// (TMEM), P = 2^(scale log2e S - m) written over S as bf16, O += P V (TMEM).  While
+// one stream's softmax works, the tensor cores run the other's products.  A row
+// belongs to one thread, so maximum, sum and rescaling stay in its registers.  O is
+// rescaled only when a row's maximum has grown by more than 2^8 over the one it
+// used so far (P <= 2^8 otherwise; bf16 keeps the same relative precision there,
+// and the final division cancels the reference): a rare event after the first
+// blocks, where a rescaling of every block costs a pass over O.
+//
+// Streams of an item:
+//   window, g even    two query heads of one key head at the same 128 tokens
+//   window, g odd     two successive 128-token tiles of one head
+//   pages, long       two successive tiles of (token, head of the group) rows
+//   pages, short      one tile of rows (a decoding step); the streams take
+//                     alternate key blocks and are merged at the end
+// Paged work is one list of (tile pair, key head, key block) units cut into equal
+// runs, one per CTA (the cuts are found from the lengths on the device, so a
+// captured launch follows them); an item cut between CTAs leaves unnormalised
+// partial rows in the workspace, which attend_combine_kernel adds up in order.
+//
+// Roles (384 threads, one CTA per SM): warps 0..3 and 4..7 softmax and output of
+// the two streams, warp 8 TMA, warp 9 MMA issue and TMEM, warp 10 hands out the
+// items through a ring in shared memory (registers move between whole warpgroups:
+// a softmax thread holds its row of S).  K and V blocks pass
+// through one ring of slots (K0 V0 K1 V1 ...).  Keys behind a length may hold
+// anything: their scores are replaced, and the MMA warp zeroes their value rows
+// in shared memory (0 times a stray infinity is not 0).
+//
+// Bound: at d = 128 a block costs 1024 cycles of products and 1024 of
+// exponentials (16 a cycle an SM) a stream, at d = 64 512 and 1024; decoding is
+// bound by the pages' bytes.
+//
+// Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
+// its loop, and copies and products in flight end before TMEM is freed.
+#include <math.h>
+
+#include "attend.cuh"
+#include "internal.h"
+#include "layer.h"
+#include "tc_common.cuh"
+
+namespace elsaa {
+namespace {
+
+using namespace tc;
+
+constexpr int kBlock = 128;              // rows of a stream, keys of a block
+constexpr int kThreads = 384;
+// registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kAtom = 128 * 128;    // 128 rows x 64 bf16
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTO = 256;            // O of stream s at kTO + 128 s; S (and P) at 128 s
+constexpr float kGrow = 8.0f;            // log2 of the growth that rescales O
+constexpr int kMaxCtas = 160;            // of a paged call (the workspace holds their partials)
+constexpr int kMinUnits = 2;             // a run shorter than this is not worth a CTA
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kBars = kRing + kSlots * kTile;
+  static constexpr uint32_t kMl = kBars + 1024;                // m, l of stream 1 [2][128]
+  static constexpr uint32_t kDyn = kMl + 1024;
+};
+static_assert(Lay<128>::kDyn <= 232448, "shared memory at d = 128");
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Shape {
+  int tiles;        // window: 128-token tiles (g even) or pairs of them (g odd)
+  int pair_heads;   // window: the streams are two heads
+  int tt;           // pages: tokens of a row tile, 128 / g
+  int sub;          // pages: rows of a page box
+  float scale_log2;
+  int slot_rows;    // pages: rows of a partial slot
+};
+
+// x[s] of a pair that stays in registers.
+template <typename T>
+ELSAA_DEV T pick(const T (&x)[2], int s) { return s ? x[1] : x[0]; }
+
+// One CTA's piece of work: rows of both streams against the blocks n0 .. n1 - 1
+// of the item's block list.
+struct Item {
+  int b, hk, len;
+  int h[2], r0[2];          // window: head and first token; pages: - and first new token
+  int p_first[2], p_last[2];   // positions of a stream's rows (p_last < 0: no rows)
+  int start, tokens;        // pages: first row of q, new tokens
+  bool split;               // one tile, alternate blocks
+  int sink_blocks, first, nblk, n0, n1;
+  int k_first[2], k_last[2], sink_top;
+  int order;                // the CTA's items before it; -1: there are no more
+  ELSAA_DEV int block(int n) const { return n < sink_blocks ? n : first + n - sink_blocks; }
+  ELSAA_DEV bool uses(int s, int n) const {
+    if (split) return (n & 1) == s;
+    const int kb = block(n);
+    return kb <= pick(k_last, s) && (kb >= pick(k_first, s) || kb < sink_top);
+  }
+  // the last block of [n0, n1) that the stream uses; n0 - 1: none
+  ELSAA_DEV int last_use(int s) const {
+    int n = n1 - 1;
+    while (n >= n0 && !uses(s, n)) --n;
+    return n;
+  }
+};
+
+ELSAA_DEV void item_blocks(Item& it, const AttendArgs& a) {
+  it.sink_top = (int)(((int64_t)a.sinks + kBlock - 1) / kBlock);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    it.k_first[s] = 0;
+    it.k_last[s] = -1;
+    if (it.p_last[s] >= 0) {
+      const KeyBlocks k = key_blocks(it.p_first[s], it.p_last[s], a.window, a.sinks, kBlock);
+      it.k_first[s] = k.first;
+      it.k_last[s] = k.last;
+    }
+  }
+  // the union: stream 0 starts and ends no later than stream 1 (where that has rows)
+  it.nblk = it.sink_blocks = it.first = 0;
+  if (it.p_last[0] < 0) return;
+  it.first = it.k_first[0];
+  it.sink_blocks = min(it.sink_top, it.first);
+  it.nblk = it.sink_blocks + max(it.k_last[0], it.k_last[1]) - it.first + 1;
+}
+
+constexpr int kItems = 4;
+struct Bars {
+  uint64_t full[8], empty[8];   // ring slots
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t x_full, x_done;      // a split item: O of stream 1 given, and read
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t drain;
+  uint32_t tmem;
+  int32_t cut[6];               // a paged CTA's first item (Cut)
+  Item items[kItems];
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+// ---- window items ----------------------------------------------------------
+
+// Item x, the longest (last) tiles first, heads and batches inside.
+ELSAA_DEV Item window_item(const AttendArgs& a, const Shape& sh, int64_t x) {
+  Item it;
+  const int hh = sh.pair_heads ? a.H / 2 : a.H;
+  const int t = sh.tiles - 1 - (int)(x / ((int64_t)a.B * hh));
+  const int bh = (int)(x % ((int64_t)a.B * hh));
+  it.b = bh / hh;
+  const int h = sh.pair_heads ? bh % hh * 2 : bh % hh;
+  it.hk = h / a.g;
+  it.len = a.lengths ? min(max(a.lengths[it.b], 0), a.N) : a.N;
+  it.split = false;
+  it.start = it.tokens = 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    it.h[s] = sh.pair_heads ? h + s : h;
+    it.r0[s] = sh.pair_heads ? t * kBlock : (2 * t + s) * kBlock;
+    it.p_first[s] = it.r0[s];
+    it.p_last[s] = it.r0[s] < it.len ? min(it.len, it.r0[s] + kBlock) - 1 : -1;
+  }
+  item_blocks(it, a);
+  it.n0 = 0;
+  it.n1 = it.nblk;
+  return it;
+}
+
+// ---- paged items -----------------------------------------------------------
+
+ELSAA_DEV int pairs_of(int tokens, int tt) { return (tokens + 2 * tt - 1) / (2 * tt); }
+
+// Tile pair `pair` of sequence b (tokens new tokens from row start, context len).
+ELSAA_DEV Item paged_item(const AttendArgs& a, const Shape& sh, int b, int pair, int hk, int start,
+                          int tokens, int len) {
+  Item it;
+  it.b = b;
+  it.hk = hk;
+  it.len = len;
+  it.start = start;
+  it.tokens = tokens;
+  const int t0 = 2 * pair * sh.tt;
+  it.split = t0 + sh.tt >= tokens;   // the pair has one tile
+  const int pos0 = len - tokens;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int r = it.split ? t0 : t0 + s * sh.tt;
+    it.h[s] = 0;
+    it.r0[s] = r;
+    it.p_first[s] = pos0 + r;
+    it.p_last[s] = pos0 + min(tokens, r + sh.tt) - 1;
+  }
+  item_blocks(it, a);
+  it.n0 = 0;
+  it.n1 = it.nblk;
+  return it;
+}
+
+struct Cut {
+  int b, pair, hk, off;   // where a run begins: its item and block
+  int units;              // its length
+  int fresh;              // it begins an item
+};
+
+// Units (tile pair, key head, block) of sequence b.
+ELSAA_DEV int64_t seq_units(const AttendArgs& a, const Shape& sh, int b, bool lead) {
+  int start, len;
+  const int n = new_tokens(a, b, &start, &len, lead);
+  int64_t u = 0;
+  const int pairs = pairs_of(n, sh.tt);
+  for (int p = 0; p < pairs; ++p) u += paged_item(a, sh, b, p, 0, start, n, len).nblk;
+  return u * a.Hkv;
+}
+
+ELSAA_DEV int64_t run_length(int64_t total, int ctas) {
+  const int64_t per = (total + ctas - 1) / ctas;
+  return per > kMinUnits ? per : kMinUnits;
+}
+
+ELSAA_DEV int64_t all_units(const AttendArgs& a, const Shape& sh, bool lead) {
+  const int lane = threadIdx.x & 31;
+  int64_t u = 0;
+  for (int b = lane; b < a.seqs; b += 32) u += seq_units(a, sh, b, lead);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  return u;
+}
+
+// The item and block of unit w (0 <= w < total), by one warp.
+ELSAA_DEV Cut find_unit(const AttendArgs& a, const Shape& sh, int64_t w) {
+  const int lane = threadIdx.x & 31;
+  Cut c{0, 0, 0, 0, 0, 0};
+  for (int b0 = 0; b0 < a.seqs; b0 += 32) {
+    const int64_t mine = b0 + lane < a.seqs ? seq_units(a, sh, b0 + lane, false) : 0;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, w < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      int64_t rest = w - __shfl_sync(0xffffffffu, upto - mine, l);
+      c.b = b0 + l;
+      int start, len;
+      const int n = new_tokens(a, c.b, &start, &len, false);
+      const int pairs = pairs_of(n, sh.tt);
+      for (c.pair = 0; c.pair < pairs; ++c.pair) {
+        const int64_t blk = paged_item(a, sh, c.b, c.pair, 0, start, n, len).nblk;
+        if (rest < blk * a.Hkv) {
+          c.hk = (int)(rest / blk);
+          c.off = (int)(rest % blk);
+          break;
+        }
+        rest -= blk * a.Hkv;
+      }
+      c.fresh = c.off == 0;
+      return c;
+    }
+    w -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return c;
+}
+
+// Walks a CTA's items.
+template <bool PAGED>
+struct Walk {
+  const AttendArgs& a;
+  const Shape& sh;
+  int64_t x, items;                          // window
+  int b, pair, hk, off, left, start, tokens, len;   // pages
+  int order;                                 // items so far
+  ELSAA_DEV Walk(const AttendArgs& a_, const Shape& sh_, int64_t items_, const int32_t* cut)
+      : a(a_), sh(sh_), x(blockIdx.x), items(items_), order(0) {
+    if (PAGED) {
+      b = cut[0], pair = cut[1], hk = cut[2], off = cut[3], left = cut[4];
+      start = tokens = len = 0;
+      if (left > 0) tokens = new_tokens(a, b, &start, &len, false);
+    }
+  }
+  ELSAA_DEV bool next(Item& it) {
+    if (!PAGED) {
+      if (x >= items) return false;
+      it = window_item(a, sh, x);
+      it.order = order++;
+      x += gridDim.x;
+      return true;
+    }
+    if (left <= 0) return false;
+    while (pair >= pairs_of(tokens, sh.tt)) {   // (a later sequence holds the units left)
+      if (++b >= a.seqs) return false;
+      pair = hk = off = 0;
+      tokens = new_tokens(a, b, &start, &len, false);
+    }
+    it = paged_item(a, sh, b, pair, hk, start, tokens, len);
+    it.n0 = off;
+    it.n1 = min(it.nblk, off + left);
+    left -= it.n1 - it.n0;
+    off = 0;
+    if (++hk == a.Hkv) hk = 0, ++pair;
+    it.order = order++;
+    return true;
+  }
+};
+
+// ---- kernel ------------------------------------------------------------------
+
+// 2^x on the special-function unit (approximate, flushes denormals).
+ELSAA_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+ELSAA_DEV void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// Registers of this thread, by whole warpgroups.
+template <int N>
+ELSAA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+ELSAA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+ELSAA_DEV void store32(__nv_bfloat16* p, const float* v) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Columns <= x of 32.
+ELSAA_DEV uint32_t upto_bits(int x) { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; }
+
+// The scratch of a paged call: partial rows [slot][row][D] and (m, l) [slot][row];
+// slot = ((cta * 2 + (not the run's first item)) * 2 + stream).
+struct Partial {
+  float* o;
+  float2* ml;
+};
+ELSAA_DEV Partial partial_row(const AttendArgs& a, const Shape& sh, int d, int slot, int row) {
+  const int64_t slots = (int64_t)kMaxCtas * 4, at = (int64_t)slot * sh.slot_rows + row;
+  float* o = reinterpret_cast<float*>(a.scratch);
+  return {o + at * d, reinterpret_cast<float2*>(o + slots * sh.slot_rows * d) + at};
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const Shape sh,
+                  int64_t items) {
+  using L = Lay<D>;
+  constexpr int SL = L::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((sbase & 1023u) != 0) {
+    if (tid == 0) raise_error(a.err, ERR_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < SL; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 128);
+      mbar_init(&bars->o_full[s], 1);
+    }
+    mbar_init(&bars->x_full, 128);
+    mbar_init(&bars->x_done, 128);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 10);   // eight softmax warps, TMA, MMA
+    }
+    mbar_init(&bars->drain, 1);
+    fence_mbar_init();
+  }
+  if (PAGED && warp == 0) {   // this CTA's run of units
+    const int64_t total = all_units(a, sh, blockIdx.x == 0);
+    const int64_t per = run_length(total, gridDim.x), w0 = per * blockIdx.x;
+    Cut c{0, 0, 0, 0, 0, 0};
+    if (w0 < total) {
+      c = find_unit(a, sh, w0);
+      c.units = (int)(per < total - w0 ? per : total - w0);
+    }
+    if (lane == 0) {
+      bars->cut[0] = c.b, bars->cut[1] = c.pair, bars->cut[2] = c.hk;
+      bars->cut[3] = c.off, bars->cut[4] = c.units, bars->cut[5] = c.fresh;
+    }
+  }
+  __syncthreads();
+  if (PAGED && bars->cut[4] == 0) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+  bool ok = true;
+  uint32_t ni = 0;   // items taken so far
+  // the next item, or null behind the last one (or where a wait gave up)
+  auto take = [&]() -> const Item* {
+    if (!ok) return nullptr;
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[ni % kItems], (ni / kItems) & 1, a.err));
+    const Item* it = &bars->items[ni % kItems];
+    return ok && it->order >= 0 ? it : nullptr;
+  };
+  auto give_back = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[ni % kItems]);
+    ++ni;
+  };
+
+  if (warp < kTmaWarp) {
+    regs_up<kSoftmaxRegs>();
+    // ------------------------------------------------------------------ softmax and output
+    const int st = warp >> 2, row = tid & 127;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + 128 * st + lane_off, tO = tmem + kTO + 128 * st + lane_off;
+    float* ml1 = reinterpret_cast<float*>(smem + L::kMl);
+    uint32_t ns = 0, no = 0, nx = 0;
+    const int tok_of_row = PAGED ? row / a.g : row;
+    while (const Item* item = take()) {
+      const Item& it = *item;
+      // the row's position; rows past the tile or its tokens have none
+      const int r = pick(it.r0, st) + tok_of_row;
+      const int pos = pick(it.p_first, st) + tok_of_row;
+      const bool live = PAGED ? tok_of_row < sh.tt && r < it.tokens : r < it.len;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int n = it.n0; n < it.n1; ++n) {
+        if (!it.uses(st, n)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[st], ns & 1, a.err));
+        if (!ok) break;
+        ++ns;
+        fence_after();
+        if (warp_live) {
+          const int j0 = it.block(n) * kBlock;
+          float sv[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sv + 32 * c);
+          tmem_ld_wait();
+          if (j0 + kBlock - 1 > pick(it.p_first, st) ||
+              (int64_t)j0 <= (int64_t)pick(it.p_last, st) - a.window) {
+            const int hi = pos - j0, lo = pos - a.window + 1 - j0;
+            const int sk = (int)min((int64_t)a.sinks - j0, (int64_t)kBlock);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = upto_bits(hi - 32 * c) &
+                                   (~upto_bits(lo - 1 - 32 * c) | upto_bits(sk - 1 - 32 * c));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) sv[32 * c + e] = -INFINITY;
+            }
+          }
+          float t0 = sv[0], t1 = sv[1], t2 = sv[2], t3 = sv[3];
+#pragma unroll
+          for (int e = 4; e < 128; e += 4) {
+            t0 = fmaxf(t0, sv[e]);
+            t1 = fmaxf(t1, sv[e + 1]);
+            t2 = fmaxf(t2, sv[e + 2]);
+            t3 = fmaxf(t3, sv[e + 3]);
+          }
+          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sh.scale_log2;   // scale > 0
+          const bool grow = top > m + kGrow;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m - top) : 1.f;
+            if (grow) m = top;
+            l *= f;
+            if (any) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                float ov[16];
+                uint32_t ow[16];
+                tmem_ld16(tO + 16 * c, ov);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(ov[e] * f);
+                tmem_st16(tO + 16 * c, ow);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t packed[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float a0 = sv[32 * c + e], a1 = sv[32 * c + e + 1];
+              fma2(a0, a1, sh.scale_log2, sh.scale_log2, -base, -base);
+              const float p0 = ex2(a0), p1 = ex2(a1);
+              add2(l0, l1, p0, p1);
+              const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
+              packed[e >> 1] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            tmem_st16(tS + 16 * c, packed);   // over S, which is all in registers
+          }
+          l += l0 + l1;
+          tmem_st_wait();
+        }
+        any = true;
+        fence_before();
+        mbar_arrive(&bars->p_full[st]);
+      }
+      if (!ok) break;
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[st], no & 1, a.err));
+        if (!ok) break;
+        ++no;
+        fence_after();
+      }
+      // rows of the result: final (the item is whole in this CTA) or partial
+      const bool whole = !PAGED || (it.n0 == 0 && it.n1 == it.nblk);
+      float w0 = any ? 1.f : 0.f, w1 = 0.f;   // weights of O of this stream and of stream 1
+      if (PAGED && it.split) {
+        // stream 0 reads both O (a row's lane is the same in both)
+        if (st == 1) {
+          ml1[row] = any ? m : -INFINITY;
+          ml1[128 + row] = any ? l : 0.f;
+          fence_before();
+          mbar_arrive(&bars->x_full);
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_full, nx & 1, a.err));
+          if (!ok) break;
+          fence_after();
+          const float m1 = ml1[row], l1 = ml1[128 + row], mm = fmaxf(m, m1);
+          w0 = m > -INFINITY ? ex2(m - mm) : 0.f;
+          w1 = m1 > -INFINITY ? ex2(m1 - mm) : 0.f;
+          l = l * w0 + l1 * w1;
+          m = mm;
+        }
+      }
+      const bool out = !(PAGED && it.split && st == 1);
+      if (out && PAGED && warp_live) {
+        const bool two = it.split && __any_sync(0xffffffffu, w1 > 0.f);
+        const int slot = ((int)blockIdx.x * 2 + (it.order > 0 ? 1 : 0)) * 2 + st;
+        const float inv = !whole ? 1.f : l > 0.f ? 1.0f / l : 0.f;
+        __nv_bfloat16* yrow = nullptr;
+        float* prow = nullptr;
+        if (live && whole)
+          yrow = static_cast<__nv_bfloat16*>(a.y) + (int64_t)(it.start + r) * a.sy.n +
+                 (int64_t)(it.hk * a.g + row % a.g) * a.sy.h;
+        if (live && !whole) {
+          const Partial p = partial_row(a, sh, D, slot, row);
+          *p.ml = make_float2(m, l);
+          prow = p.o;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32], ow[32];
+          tmem_ld32(tO + 32 * c, ov);
+          if (two) tmem_ld32(tO + 128 + 32 * c, ow);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            ov[e] = w0 > 0.f ? ov[e] * (w0 * inv) : 0.f;
+            if (two && w1 > 0.f) ov[e] += ow[e] * (w1 * inv);
+          }
+          if (yrow != nullptr) store32(yrow + 32 * c, ov);
+          if (prow != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
+                  make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+      }
+      if (!PAGED) {
+        // rows at and behind the length: zeros
+        const float inv = live && l > 0.f ? 1.0f / l : 0.f;
+        const bool store = r < a.N;
+        if (store)
+          a.lse[((int64_t)it.b * a.H + pick(it.h, st)) * a.N + r] =
+              live && l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        __nv_bfloat16* yrow = static_cast<__nv_bfloat16*>(a.y) + (int64_t)it.b * a.sy.b +
+                              (int64_t)pick(it.h, st) * a.sy.h + (int64_t)r * a.sy.n;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          if (warp_live) {
+            tmem_ld32(tO + 32 * c, ov);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = inv > 0.f ? ov[e] * inv : 0.f;
+          if (store) store32(yrow + 32 * c, ov);
+        }
+      }
+      fence_before();
+      if (PAGED && it.split) {
+        if (st == 0) {
+          mbar_arrive(&bars->x_done);
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_done, nx & 1, a.err));
+          if (!ok) break;
+        }
+        ++nx;
+      }
+      give_back();
+    }
+  } else {
+    regs_down<kOtherRegs>();
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------------ copies
+      uint32_t nr = 0, nq = 0;   // ring loads and Q loads so far
+      const int subs = PAGED ? kBlock / sh.sub : 1;
+      // the slot for the next load, free and armed
+      auto acquire = [&]() -> uint32_t {
+        const uint32_t s = nr % SL;
+        if (nr >= SL) ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (nr / SL - 1) & 1, a.err));
+        if (ok && lane == 0) mbar_arrive_expect_tx(&bars->full[s], L::kTile);
+        __syncwarp();
+        if (ok) ++nr;
+        return s;
+      };
+      auto load_block = [&](const Item& it, int n) {
+        const int j0 = it.block(n) * kBlock;
+        int page = 0, slot = 0;
+        if (PAGED && lane < subs) {
+          // boxes behind the length, or that no row of the item sees, are not looked
+          // up; a page outside the pool reads as zeros
+          const int j = j0 + lane * sh.sub;
+          const int p_hi = max(it.p_last[0], it.p_last[1]);
+          page = a.pages;
+          if (j <= p_hi && (j < a.sinks || (int64_t)j + sh.sub - 1 > (int64_t)it.p_first[0] - a.window)) {
+            page = page_of(a, it.b, j);
+            if (page < 0) page = a.pages;
+            slot = j % a.page_size;
+          }
+        }
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const uint32_t s = acquire();
+          if (!ok) break;
+          const CUtensorMap* map = kv ? &maps.v : &maps.k;
+          const uint32_t dst = sbase + L::kRing + s * L::kTile;
+          if (lane < subs) {
+  #pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              if (PAGED)
+                tma_load_4d(dst + c * kAtom + lane * sh.sub * 128, map, 64 * c, slot, it.hk, page,
+                            &bars->full[s]);
+              else
+                tma_load_4d(dst + c * kAtom, map, 64 * c, j0, it.hk, it.b, &bars->full[s]);
+            }
+          }
+          __syncwarp();
+        }
+      };
+      while (const Item* item = take()) {
+        const Item& it = *item;
+        if (it.n0 >= it.n1) {
+          give_back();
+          continue;
+        }
+        load_block(it, it.n0);
+        // Q behind the first block: its slots wait for the previous item's last scores
+        if (ok && nq > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (nq - 1) & 1, a.err));
+        if (!ok) break;
+        if (lane == 0) {
+          const int tiles = it.split ? 1 : 2;
+          const uint32_t rows = PAGED ? sh.tt * a.g : kBlock;
+          mbar_arrive_expect_tx(&bars->q_full, tiles * rows * D * 2);
+  #pragma unroll
+          for (int s = 0; s < 2; ++s)
+            for (int c = 0; c < (s < tiles ? D / 64 : 0); ++c) {
+              const uint32_t dst = sbase + L::kQ + s * L::kTile + c * kAtom;
+              if (PAGED)
+                tma_load_4d(dst, &maps.q, 64 * c, it.hk * a.g, it.start + it.r0[s], 0, &bars->q_full);
+              else
+                tma_load_4d(dst, &maps.q, 64 * c, it.r0[s], it.h[s], it.b, &bars->q_full);
+            }
+        }
+        __syncwarp();
+        ++nq;
+        for (int n = it.n0 + 1, n1 = it.n1; n < n1 && ok; ++n) load_block(it, n);
+        give_back();
+      }
+      // every copy this warp started has landed before the CTA may exit
+      if (lane == 0) {
+        for (uint32_t i = nr > SL ? nr - SL : 0; i < nr; ++i)
+          mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
+        if (nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, a.err);
+      }
+      __syncwarp();
+
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ products
+      const uint32_t id_s = idesc_bf16(128, kBlock, false, false);
+      const uint32_t id_pv = idesc_bf16(128, D, false, true);
+      const uint64_t q_d = sw128_desc(sbase + L::kQ, 16, 1024);
+      const uint64_t k_d = sw128_desc(sbase + L::kRing, 16, 1024);
+      const uint64_t v_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      uint32_t nr = 0, nq = 0, np[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
+      };
+      while (const Item* item = take()) {
+        const Item& it = *item;
+        if (it.n0 >= it.n1) {
+          give_back();
+          continue;
+        }
+        const int last[2] = {it.last_use(0), it.last_use(1)};
+        int pend[2] = {-1, -1};
+        bool any[2] = {false, false};
+        const uint32_t base = nr;          // ring index of K of block n0
+        nr += 2 * (it.n1 - it.n0);
+        for (int n = it.n0; n <= it.n1 && ok; ++n) {
+          const uint32_t ik = base + 2 * (n - it.n0), iv = ik - 1;   // K of n, V of n - 1
+          if (n < it.n1) {
+            ok = wait(&bars->full[ik % SL], (ik / SL) & 1);
+            if (ok && n == it.n0) ok = wait(&bars->q_full, nq & 1);
+          }
+          if (ok && n > it.n0) {
+            ok = wait(&bars->full[iv % SL], (iv / SL) & 1);
+            const int live = it.len - it.block(n - 1) * kBlock;
+            if (ok && live < kBlock && (PAGED || a.lengths != nullptr)) {
+              // value rows behind the length: zeros
+              uint8_t* v = smem + L::kRing + (iv % SL) * L::kTile;
+              for (int r = live * 8 + lane; r < kBlock * 8; r += 32)
+  #pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  *reinterpret_cast<uint4*>(v + c * kAtom + r * 16) = make_uint4(0, 0, 0, 0);
+              fence_async_smem();
+              __syncwarp();
+            }
+          }
+  #pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (ok && pend[s] >= 0) {            // O_s (+)= P_s V of block n - 1
+              ok = wait(&bars->p_full[s], np[s] & 1);
+              ++np[s];
+              fence_after();
+              if (ok && lane == 0) {
+                const uint64_t vd = desc_add(v_d, (iv % SL) * L::kTile);
+  #pragma unroll
+                for (int x = 0; x < kBlock; x += 16)
+                  mma_bf16_ts(tmem + kTO + 128 * s, tmem + 128 * s + (x >> 1),
+                              desc_add(vd, (uint32_t)(x >> 4) * 2048), id_pv,
+                              (any[s] || x > 0) ? 1u : 0u);
+                if (pend[s] == last[s]) mma_commit(&bars->o_full[s]);
+              }
+              __syncwarp();
+              any[s] = true;
+              pend[s] = -1;
+            }
+            if (ok && n < it.n1 && it.uses(s, n)) {   // S_s = Q_s K^T of block n
+              fence_after();
+              if (lane == 0) {
+                const uint64_t qd = desc_add(q_d, it.split ? 0 : s * L::kTile);
+                const uint64_t kd = desc_add(k_d, (ik % SL) * L::kTile);
+  #pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32;
+                  mma_bf16_ss(tmem + 128 * s, desc_add(qd, off), desc_add(kd, off), id_s,
+                              kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&bars->s_full[s]);
+              }
+              __syncwarp();
+              pend[s] = n;
+            }
+          }
+          if (ok && lane == 0) {
+            if (n < it.n1) mma_commit(&bars->empty[ik % SL]);
+            if (n > it.n0) mma_commit(&bars->empty[iv % SL]);
+            if (n + 1 == it.n1) mma_commit(&bars->q_empty);
+          }
+          __syncwarp();
+        }
+        ++nq;
+        give_back();
+      }
+      if (lane == 0) {   // the products issued so far end before TMEM is freed
+        mma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, a.err);
+      }
+      __syncwarp();
+
+    } else if (warp == kMmaWarp + 1) {
+      // ------------------------------------------------------------------ items
+      if (lane == 0) {
+        Walk<PAGED> walk(a, sh, items, bars->cut);
+        for (bool more = true; more; ++ni) {
+          if (ni >= kItems &&
+              !mbar_wait(&bars->item_empty[ni % kItems], (ni / kItems - 1) & 1, a.err))
+            break;
+          Item it;
+          more = walk.next(it);
+          if (!more) it.order = -1;
+          bars->items[ni % kItems] = it;
+          mbar_arrive(&bars->item_full[ni % kItems]);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Items cut between CTAs: their partial rows added up in the CTAs' order.  Block
+// x = 1 .. CTAs - 1 takes the item that CTA x begins inside of, if x is its second
+// CTA; a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+attend_combine_kernel(const AttendArgs a, const Shape sh, int ctas) {
+  __shared__ int64_t found[4];
+  __shared__ Cut cut;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x + 1;
+  if (warp == 0) {
+    const int64_t total = all_units(a, sh, false), per = run_length(total, ctas);
+    const int64_t w0 = per * c;
+    Cut f{0, 0, 0, 0, 0, 1};
+    if (w0 < total) f = find_unit(a, sh, w0);
+    if (lane == 0) {
+      cut = f;
+      found[0] = per;
+      found[1] = w0;
+    }
+  }
+  __syncthreads();
+  if (cut.fresh) return;
+  const int64_t per = found[0], begin = found[1] - cut.off;
+  const int first = (int)(begin / per);
+  if (first != c - 1) return;
+  int start, len;
+  const int n = new_tokens(a, cut.b, &start, &len, false);
+  const Item it = paged_item(a, sh, cut.b, cut.pair, cut.hk, start, n, len);
+  const int last = (int)((begin + it.nblk - 1) / per);
+  const int first_slot = begin == first * per ? 0 : 1;   // the item is that run's first, or its last
+  const int per_stream = sh.tt * a.g;
+  for (int x = blockIdx.y * 8 + warp; x < per_stream * (it.split ? 1 : 2); x += 8 * gridDim.y) {
+    const int st = x / per_stream, row = x % per_stream, r = it.r0[st] + row / a.g;
+    if (r >= n) continue;
+    auto part = [&](int cta) {
+      return partial_row(a, sh, D, (cta * 2 + (cta == first ? first_slot : 0)) * 2 + st, row);
+    };
+    float m = -INFINITY;
+    for (int i = first + lane; i <= last; i += 32) m = fmaxf(m, part(i).ml->x);
+    m = warp_max(m);
+    float l = 0.f, o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int i = first; i <= last; ++i) {
+      const Partial p = part(i);
+      const float2 ml = *p.ml;
+      if (ml.x == -INFINITY) continue;   // (a stream without blocks in that run)
+      const float w = exp2f(ml.x - m);
+      l += ml.y * w;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] += p.o[lane + 32 * e] * w;
+    }
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + (int64_t)(start + r) * a.sy.n +
+                       (int64_t)(cut.hk * a.g + row % a.g) * a.sy.h;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
+  }
+}
+
+// ---- launches ------------------------------------------------------------------
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+int slot_rows(int64_t rows, int g) {
+  const int64_t most = (128 / g) * g;
+  return (int)(rows * g < most ? rows * g : most);
+}
+
+template <int D>
+cudaError_t window(const AttendArgs& a, cudaStream_t s) {
+  Shape sh = {};
+  sh.pair_heads = a.g % 2 == 0;
+  const int t = (a.N + kBlock - 1) / kBlock;
+  sh.tiles = sh.pair_heads ? t : (t + 1) / 2;
+  sh.scale_log2 = a.scale * 1.4426950408889634f;
+  const int64_t items = (int64_t)a.B * (sh.pair_heads ? a.H / 2 : a.H) * sh.tiles;
+  Maps maps;
+  cudaError_t e;
+  const uint32_t box[4] = {64, kBlock, 1, 1};
+  if ((e = make_map_4d(&maps.q, a.q, D, a.N, a.H, a.B, a.sq.n, a.sq.h, a.sq.b, box)) != cudaSuccess ||
+      (e = make_map_4d(&maps.k, a.k, D, a.N, a.Hkv, a.B, a.sk.n, a.sk.h, a.sk.b, box)) != cudaSuccess ||
+      (e = make_map_4d(&maps.v, a.v, D, a.N, a.Hkv, a.B, a.sv.n, a.sv.h, a.sv.b, box)) != cudaSuccess)
+    return e;
+  e = cudaFuncSetAttribute(attend_fwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Lay<D>::kDyn);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  attend_fwd_kernel<D, false><<<(int)(items < sms ? items : sms), kThreads, Lay<D>::kDyn, s>>>(
+      maps, a, sh, items);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
+  Shape sh = {};
+  sh.tt = 128 / a.g;
+  sh.sub = a.page_size & -a.page_size;
+  if (sh.sub > kBlock) sh.sub = kBlock;
+  sh.scale_log2 = a.scale * 1.4426950408889634f;
+  sh.slot_rows = slot_rows(a.rows, a.g);
+  Maps maps;
+  cudaError_t e;
+  const uint32_t qbox[4] = {64, (uint32_t)a.g, (uint32_t)sh.tt, 1};
+  const uint32_t box[4] = {64, (uint32_t)sh.sub, 1, 1};
+  if ((e = make_map_4d(&maps.q, a.q, D, a.H, a.rows, 1, a.sq.h, a.sq.n, a.sq.b, qbox)) != cudaSuccess ||
+      (e = make_map_4d(&maps.k, a.k, D, a.page_size, a.Hkv, a.pages, a.sk.n, a.sk.h, a.sk.b, box)) !=
+          cudaSuccess ||
+      (e = make_map_4d(&maps.v, a.v, D, a.page_size, a.Hkv, a.pages, a.sv.n, a.sv.h, a.sv.b, box)) !=
+          cudaSuccess)
+    return e;
+  e = cudaFuncSetAttribute(attend_fwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Lay<D>::kDyn);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  attend_fwd_kernel<D, true><<<ctas, kThreads, Lay<D>::kDyn, s>>>(maps, a, sh, 0);
+  if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
+  const int rows = 2 * sh.slot_rows;
+  attend_combine_kernel<D><<<dim3(ctas - 1, rows < 64 ? (rows + 7) / 8 : 8), 256, 0, s>>>(a, sh, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attend_tc_supported(int d, bool bf16) { return bf16 && (d == 64 || d == 128); }
+
+size_t paged_scratch_bytes(int d, bool bf16, int64_t rows, int g) {
+  if (!attend_tc_supported(d, bf16)) return 0;
+  return (size_t)kMaxCtas * 4 * slot_rows(rows, g) * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_window_fwd_tc(const AttendArgs& a, cudaStream_t s) {
+  return a.d == 64 ? window<64>(a, s) : window<128>(a, s);
+}
+cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s) {
+  return a.d == 64 ? pages<64>(a, s) : pages<128>(a, s);
+}
+
+}  // namespace elsaa

@@ -81,4 +81,16 @@ cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t 
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 
+// tcgen05 kernels: bf16, d = 64 or 128.
+bool attend_tc_supported(int d, bool bf16);
+cudaError_t launch_window_fwd_tc(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
+// Workspace bytes of launch_paged_tc's partial rows.
+size_t paged_scratch_bytes(int d, bool bf16, int64_t rows, int g);
+
+// A 128-byte-swizzled bf16 tensor map of a [n3, n2, n1, d] tensor with the
+// given element strides (d contiguous) and box.
+cudaError_t make_map_4d(CUtensorMap* map, const void* base, uint64_t d, uint64_t n1, uint64_t n2,
+                        uint64_t n3, int64_t s1, int64_t s2, int64_t s3, const uint32_t* box);
+
 }  // namespace elsaa

@@ -248,7 +248,10 @@ elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, c
   if (st != ELSAA_OK) return st;
   if (!lse) return ELSAA_ERR_INVALID_ARG;
   a.lse = lse;
-  return cuda_status(launch_window_fwd_simt(a, p->dtype == ELSAA_BF16, (cudaStream_t)stream));
+  const bool bf16 = p->dtype == ELSAA_BF16;
+  return cuda_status(attend_tc_supported(p->d, bf16)
+                         ? launch_window_fwd_tc(a, (cudaStream_t)stream)
+                         : launch_window_fwd_simt(a, bf16, (cudaStream_t)stream));
 }
 
 elsaa_status elsaa_window_backward(const elsaa_window_params* p, const void* q, const void* k,
@@ -277,7 +280,7 @@ elsaa_status elsaa_paged_validate(const elsaa_paged_params* p) { return check(p)
 
 size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p) {
   if (check(p) != ELSAA_OK) return 0;
-  return kErrBytes;
+  return kErrBytes + paged_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->rows, p->H / p->Hkv);
 }
 
 static bool page_strides_of(const elsaa_paged_params* p, const int64_t* given, Strides* kp,
@@ -376,7 +379,10 @@ elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
   a.page_size = p->page_size;
   a.pages = p->pages;
   a.table_width = p->table_width;
-  return cuda_status(launch_paged_simt(a, p->dtype == ELSAA_BF16, (cudaStream_t)stream));
+  const bool bf16 = p->dtype == ELSAA_BF16;
+  return cuda_status(attend_tc_supported(p->d, bf16)
+                         ? launch_paged_tc(a, (cudaStream_t)stream)
+                         : launch_paged_simt(a, bf16, (cudaStream_t)stream));
 }
 
 }  // extern "C"

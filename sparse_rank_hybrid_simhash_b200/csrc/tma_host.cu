@@ -1,12 +1,14 @@
 // Host side of the TMA copies: 2-D tensor maps over [rows, 64] or [rows, 128]
 // bf16 matrices (a box of one row of 64 columns, 128-byte swizzle) for the
 // attention kernels' row gathers, and 3-D maps over [units, N, d] bf16 with
-// 8-column boxes for the RACE slab kernels; encoded through the driver entry
+// 8-column boxes for the RACE slab kernels, and 4-D maps of strided tensors for
+// the window and paged attention; encoded through the driver entry
 // point the runtime resolves (no direct driver-API calls).
 #include <cudaTypedefs.h>
 #include <mutex>
 
 #include "internal.h"
+#include "layer.h"
 
 namespace elsaa {
 
@@ -51,6 +53,20 @@ cudaError_t make_slab_map(CUtensorMap* map, const void* base, uint64_t units, ui
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_map_4d(CUtensorMap* map, const void* base, uint64_t d, uint64_t n1, uint64_t n2,
+                        uint64_t n3, int64_t s1, int64_t s2, int64_t s3, const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {d, n1, n2, n3};
+  const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                        strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
