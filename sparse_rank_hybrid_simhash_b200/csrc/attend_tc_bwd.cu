@@ -1,0 +1,1016 @@
+// Backward of the window attention on the tensor cores (bf16, d = 64 or 128).
+//
+//   P = exp(scale q k - lse),  dS = P (dy v - delta),  delta = y . dy,
+//   dv = P^T dy,  dk = scale dS^T q,  dq = scale dS k.
+//
+// Two persistent warp-specialized tcgen05 kernels, so that every output element
+// has one writer and no atomics:
+//   window_dkv_kernel  key tiles: S^T = K Q^T and dP^T = V dY^T, keys in the TMEM
+//                      lanes; P^T and dS^T go back over them as bf16 and are the A
+//                      operands of dV += P^T dY, dK += dS^T Q.  All query heads of
+//                      the group walk past a key tile, so grouped heads add up in
+//                      TMEM.  4 products a block.
+//   window_dq_kernel   query tiles: S = Q K^T, dP = dY V^T, dQ += dS K.  3 products.
+// A single kernel would save two products of seven and one exponential a block,
+// but would add 64 KB of fp32 dQ a block to memory in an order that changes.
+//
+// window_dkv_kernel's work is one list of (key tile, query head, query block) units
+// cut into equal runs, one per CTA: a tile of sinks is seen by every query behind
+// it, an order of magnitude more than the others.  A tile cut between CTAs leaves
+// fp32 partials that dkv_combine_kernel adds up in the CTAs' order.
+//
+// Elementwise work of a block: 256 threads, each one lane and 64 of the 128
+// columns.  The products of one block run under the elementwise work of the
+// previous one: dV and the next S under dS, dK and the next dP under P.
+//
+// Bound at d = 128: 2048 (dkv) and 1536 (dq) cycles of products a block against
+// 1024 of exponentials and about as many of other instructions; at d = 64 the
+// elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
+//
+// Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
+// its loop, and copies and products in flight end before TMEM is freed.
+#include <math.h>
+
+#include "attend_tc.cuh"
+#include "internal.h"
+
+namespace elsaa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;            // 8 elementwise warps, TMA, MMA, items, one idle
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+// registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
+constexpr int kWorkRegs = 216, kOtherRegs = 72;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kItems = 4;
+constexpr int kMinUnits = 2;
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr uint32_t kFix = 0;                          // K, V (dkv) or Q, dY (dq)
+  static constexpr uint32_t kRing = 2 * kTile;
+  // dkv: query blocks' statistics, each in a ring of its own.  They are written with
+  // the loads of Q and dY, whose ring slots came free with the dV or dK of an earlier
+  // block: with 5 slots Q of block t + 3 waits for dV of t (-lse of t has been read)
+  // and dY of t + 2 for dK of t (-delta too); with 8, Q of t + 4 for dK of t and dY
+  // of t + 5 for dV of t + 1.
+  static constexpr int kNl = D == 128 ? 3 : 4, kNd = D == 128 ? 2 : 5;
+  static constexpr uint32_t kStatL = kRing + kSlots * kTile;   // [kNl][128]
+  static constexpr uint32_t kStatD = kStatL + kNl * 512;       // [kNd][128]
+  static constexpr uint32_t kBars = kStatD + kNd * 512;
+  static constexpr uint32_t kDyn = kBars + 512;
+};
+static_assert(Lay<128>::kDyn <= 232448, "shared memory at d = 128");
+
+struct Maps {
+  CUtensorMap q, k, v, dy;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t fix_full[2], fix_empty[2];    // dkv: K, V; dq: Q, dY
+  uint64_t s_full[2], s_read[2], dp_full, p_full, ds_full, acc_full;
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t drain;
+  uint32_t tmem;
+  int32_t cut[5];
+  int32_t items[kItems][12];
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// Row statistics in the workspace, rows padded to whole blocks per head:
+// -log2e lse and -delta; (-inf, 0) for rows without keys, which makes P zero.
+struct Stats {
+  float *nl, *nd;
+  int64_t pad;   // rows of a head
+};
+
+ELSAA_DEV int length_of(const AttendArgs& a, int b) {
+  return a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+}
+
+// ---- row statistics ------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const Stats st) {
+  constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  const int c = (threadIdx.x % LANES) * 8;
+  const int64_t x = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+  const bool in = x < (int64_t)a.B * a.H * st.pad;
+  const int n = in ? (int)(x % st.pad) : 0;
+  const int64_t bh = in ? x / st.pad : 0;
+  const int h = (int)(bh % a.H), b = (int)(bh / a.H);
+  float s = 0.f, nl = -INFINITY;
+  if (in && n < length_of(a, b)) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) +
+                                                    b * a.sy.b + h * a.sy.h + n * a.sy.n + c);
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy) +
+                                                    b * a.sdy.b + h * a.sdy.h + n * a.sdy.n + c);
+    const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s += __uint_as_float(ua[i] << 16) * __uint_as_float(wa[i] << 16) +
+           __uint_as_float(ua[i] & 0xffff0000u) * __uint_as_float(wa[i] & 0xffff0000u);
+    const float l = a.lse[bh * a.N + n];
+    if (l > -INFINITY) nl = -l * 1.4426950408889634f;
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (in && c == 0) {
+    st.nl[x] = nl;
+    st.nd[x] = -s;
+  }
+}
+
+// ---- shared pieces ---------------------------------------------------------------
+
+// 16-byte-aligned bytes (a multiple of 16) into shared memory.
+ELSAA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Rows live .. 127 of a tile in shared memory become zeros (rows behind a length
+// may hold anything, and meet zero factors in a product); one warp.
+template <int D>
+ELSAA_DEV void zero_rows(uint8_t* tile, int live) {
+  for (int r = live * 8 + (threadIdx.x & 31); r < kBlock * 8; r += 32)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<uint4*>(tile + c * kAtom + r * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  __syncwarp();
+}
+
+// 128 x 128 product of two K-major tiles over D.
+template <int D>
+ELSAA_DEV void mma_tiles(uint32_t d_tmem, uint64_t ad, uint64_t bd) {
+  constexpr uint32_t id = idesc_bf16(128, kBlock, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32;
+    mma_bf16_ss(d_tmem, desc_add(ad, off), desc_add(bd, off), id, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[128 x D] (+)= A X, A the bf16 tile that both halves of the elementwise threads
+// left in TMEM (columns 0..63 packed from `a`, 64..127 from a + 64), X [128, D] in
+// shared memory.
+template <int D>
+ELSAA_DEV void mma_packed(uint32_t d_tmem, uint32_t a, uint64_t xd, bool accumulate) {
+  constexpr uint32_t id = idesc_bf16(128, D, false, true);
+#pragma unroll
+  for (int x = 0; x < kBlock; x += 16)
+    mma_bf16_ts(d_tmem, a + (uint32_t)((x >> 6) * 64 + ((x & 63) >> 1)),
+                desc_add(xd, (uint32_t)(x >> 4) * 2048), id, (accumulate || x > 0) ? 1u : 0u);
+}
+
+// 64 fp32 values to 32 packed columns.
+ELSAA_DEV void store_packed(uint32_t taddr, const float* v) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    tmem_st16(taddr + 16 * c, w);
+  }
+}
+
+// The item ring between the items warp and the others.
+struct ItemRing {
+  Bars* bars;
+  uint32_t* err;
+  uint32_t taken = 0;
+  // the next item, or null behind the last one; ok turns false where a wait gave up
+  ELSAA_DEV const int32_t* take(bool& ok) {
+    if (!ok) return nullptr;
+    const uint32_t i = taken % kItems;
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[i], (taken / kItems) & 1, err));
+    const int32_t* it = bars->items[i];
+    if (!ok || it[0] < 0) return nullptr;
+    ++taken;
+    return it;
+  }
+  ELSAA_DEV void give_back(const int32_t* it) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+      mbar_arrive(&bars->item_empty[(it - &bars->items[0][0]) / 12]);
+  }
+};
+
+ELSAA_DEV void init_bars(Bars* b) {
+  for (int i = 0; i < 8; ++i) {
+    mbar_init(&b->full[i], 1);
+    mbar_init(&b->empty[i], 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&b->fix_full[i], 1);
+    mbar_init(&b->fix_empty[i], 1);
+    mbar_init(&b->s_full[i], 1);
+    mbar_init(&b->s_read[i], 256);
+  }
+  mbar_init(&b->dp_full, 1);
+  mbar_init(&b->p_full, 256);
+  mbar_init(&b->ds_full, 256);
+  mbar_init(&b->acc_full, 1);
+  for (int i = 0; i < kItems; ++i) {
+    mbar_init(&b->item_full[i], 1);
+    mbar_init(&b->item_empty[i], 10);   // eight elementwise warps, TMA, MMA
+  }
+  mbar_init(&b->drain, 1);
+  fence_mbar_init();
+}
+
+// ---- dk, dv ----------------------------------------------------------------------
+
+// Fields of a key tile's item; [0] < 0: no more items.
+enum { kB, kHk, kLen, kKt, kNb, kNq, kN0, kN1, kOrder };
+
+// Query blocks (of one head) that see key tile kt.
+ELSAA_DEV int query_blocks(const AttendArgs& a, int len, int kt) {
+  const int j0 = kt * kBlock;
+  if (j0 >= len) return 0;
+  const int64_t reach = j0 < a.sinks ? len : (int64_t)j0 + kBlock - 1 + a.window;
+  return ((int)(reach < len ? reach : len) - 1) / kBlock - kt + 1;
+}
+
+// Units of one key head of a sequence, by one warp.
+ELSAA_DEV int64_t head_units(const AttendArgs& a, int len) {
+  int64_t u = 0;
+  for (int kt = threadIdx.x & 31; kt * kBlock < len; kt += 32) u += query_blocks(a, len, kt);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  return u * a.g;
+}
+ELSAA_DEV int64_t all_units(const AttendArgs& a) {
+  if (!a.lengths) return head_units(a, a.N) * a.Hkv * a.B;
+  int64_t u = 0;
+  for (int b = 0; b < a.B; ++b) u += head_units(a, length_of(a, b)) * a.Hkv;
+  return u;
+}
+ELSAA_DEV int64_t run_length(int64_t total, int ctas) {
+  const int64_t per = (total + ctas - 1) / ctas;
+  return per > kMinUnits ? per : kMinUnits;
+}
+
+struct Cut {
+  int b, hk, kt, off;
+};
+
+// The key tile and block of unit w (0 <= w < all units), by one warp.
+ELSAA_DEV Cut find_unit(const AttendArgs& a, int64_t w) {
+  const int lane = threadIdx.x & 31;
+  Cut c{0, 0, 0, 0};
+  int64_t per_head = 0;
+  if (!a.lengths) {
+    per_head = head_units(a, a.N);
+    c.b = (int)(w / (per_head * a.Hkv));
+    w -= c.b * per_head * a.Hkv;
+  } else {
+    for (; c.b < a.B; ++c.b) {
+      per_head = head_units(a, length_of(a, c.b));
+      if (w < per_head * a.Hkv) break;
+      w -= per_head * a.Hkv;
+    }
+    if (c.b == a.B) return c;   // (w was no unit)
+  }
+  c.hk = (int)(w / per_head);
+  w -= c.hk * per_head;
+  const int len = length_of(a, c.b);
+  for (int t0 = 0; t0 * kBlock < len; t0 += 32) {
+    const int64_t mine = (int64_t)query_blocks(a, len, t0 + lane) * a.g;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, w < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      c.kt = t0 + l;
+      c.off = (int)(w - __shfl_sync(0xffffffffu, upto - mine, l));
+      return c;
+    }
+    w -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return c;
+}
+
+// The partials of a key tile cut between CTAs: [slot][dv, dk][128][D], slot = 2 cta +
+// (not the run's first item).
+ELSAA_DEV float* partial(const AttendArgs& a, int d, int slot, int which, int row) {
+  return reinterpret_cast<float*>(a.scratch) + (((int64_t)slot * 2 + which) * kBlock + row) * d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const Stats stats) {
+  using L = Lay<D>;
+  constexpr int SL = L::kSlots;
+  constexpr uint32_t kTS = 0, kTP = 128, kTV = 256, kTK = 256 + D;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((sbase & 1023u) != 0) {
+    if (tid == 0) raise_error(a.err, ERR_CHECK);
+    return;
+  }
+  if (tid == 0) init_bars(bars);
+  if (warp == 0) {   // this CTA's run of units
+    const int64_t total = all_units(a), per = run_length(total, gridDim.x), w0 = per * blockIdx.x;
+    Cut c{0, 0, 0, 0};
+    int units = 0;
+    if (w0 < total) {
+      c = find_unit(a, w0);
+      units = (int)(per < total - w0 ? per : total - w0);
+    }
+    if (lane == 0) {
+      bars->cut[0] = c.b, bars->cut[1] = c.hk, bars->cut[2] = c.kt, bars->cut[3] = c.off;
+      bars->cut[4] = units;
+    }
+  }
+  __syncthreads();
+  if (bars->cut[4] == 0) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+  bool ok = true;
+  ItemRing ring{bars, a.err};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
+  };
+
+  if (warp < kTmaWarp) {
+    // ------------------------------------------------------------------ elementwise
+    regs_up<kWorkRegs>();
+    const int half = warp >> 2, row = tid & 127;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + kTS + 64 * half + lane_off, tP = tmem + kTP + 64 * half + lane_off;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    uint32_t t = 0, ni = 0;
+    while (const int32_t* it = ring.take(ok)) {
+      const int j0 = it[kKt] * kBlock, j = j0 + row;
+      for (int n = it[kN0], n1 = it[kN1]; n < n1; ++n, ++t) {
+        const int i0 = (it[kKt] + n % it[kNq]) * kBlock;
+        ok = wait(&bars->s_full[0], t & 1) &&
+             wait(&bars->full[(2 * t) % SL], ((2 * t) / SL) & 1);   // (-lse has landed)
+        if (!ok) break;
+        fence_after();
+        const float* nl = reinterpret_cast<const float*>(smem + L::kStatL) + (t % L::kNl) * 128 + 64 * half;
+        const float* nd = reinterpret_cast<const float*>(smem + L::kStatD) + (t % L::kNd) * 128 + 64 * half;
+        float p[64];
+        tmem_ld32(tS, p);
+        tmem_ld32(tS + 32, p + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(nl + e);
+          fma2(p[e], p[e + 1], scale_log2, scale_log2, l.x, l.y);
+          fma2(p[e + 2], p[e + 3], scale_log2, scale_log2, l.z, l.w);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) p[e + x] = ex2(p[e + x]);
+        }
+        if (i0 < j0 + kBlock - 1 ||
+            (j0 + kBlock > a.sinks && (int64_t)i0 + kBlock - 1 >= (int64_t)j0 + a.window)) {
+          const int lo = j - i0 - 64 * half;   // queries from the key on
+          const int hi = j < a.sinks ? 63
+                                     : (int)min((int64_t)j + a.window - 1 - i0 - 64 * half, (int64_t)63);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t see = upto_bits(hi - 32 * c) & ~upto_bits(lo - 1 - 32 * c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) p[32 * c + e] = 0.f;
+          }
+        }
+        store_packed(tS, p);   // P^T over S^T
+        tmem_st_wait();
+        // -delta has landed (asked before P is given: with dV its slot may be loaded anew)
+        ok = wait(&bars->full[(2 * t + 1) % SL], ((2 * t + 1) / SL) & 1);
+        if (!ok) break;
+        fence_before();
+        mbar_arrive(&bars->p_full);
+        ok = wait(&bars->dp_full, t & 1);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dp[32];
+          tmem_ld32(tP + 32 * c, dp);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(nd + 32 * c + e);
+            add2(dp[e], dp[e + 1], x.x, x.y);
+            add2(dp[e + 2], dp[e + 3], x.z, x.w);
+            mul2(p[32 * c + e], p[32 * c + e + 1], dp[e], dp[e + 1]);
+            mul2(p[32 * c + e + 2], p[32 * c + e + 3], dp[e + 2], dp[e + 3]);
+          }
+        }
+        store_packed(tP, p);   // dS^T over dP^T
+        tmem_st_wait();
+        fence_before();
+        mbar_arrive(&bars->ds_full);
+      }
+      if (!ok) break;
+      ok = wait(&bars->acc_full, ni & 1);
+      if (!ok) break;
+      ++ni;
+      fence_after();
+      // dV by the first half of the threads, dK by the second
+      const bool whole = it[kN0] == 0 && it[kN1] == it[kNb];
+      const uint32_t acc = tmem + (half ? kTK : kTV) + lane_off;
+      const float f = half ? a.scale : 1.f;
+      float* prow = partial(a, D, (int)blockIdx.x * 2 + (it[kOrder] > 0 ? 1 : 0), half, row);
+      const Strides so = half ? a.sdk : a.sdv;
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + it[kB] * so.b +
+                            it[kHk] * so.h + (int64_t)j * so.n;
+      const bool live = j < it[kLen];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        tmem_ld32(acc + 32 * c, v);
+        tmem_ld_wait();
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = live ? v[e] * f : 0.f;
+          if (j < a.N) store32(orow + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      }
+      fence_before();
+      ring.give_back(it);
+    }
+  } else {
+    regs_down<kOtherRegs>();
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------------- copies
+      uint32_t nr = 0, t = 0, nf[2] = {0, 0};
+      auto load = [&](const CUtensorMap* map, uint32_t dst, int n, int h, int b, uint64_t* bar) {
+        if (lane < D / 64) tma_load_4d(dst + lane * kAtom, map, 64 * lane, n, h, b, bar);
+        __syncwarp();
+      };
+      // the item's fixed tile x (0: K, 1: V)
+      auto load_fix = [&](const int32_t* it, int x) {
+        if (nf[x] > 0) ok = ok && wait(&bars->fix_empty[x], (nf[x] - 1) & 1);
+        if (!ok) return;
+        ++nf[x];
+        if (lane == 0) mbar_arrive_expect_tx(&bars->fix_full[x], L::kTile);
+        __syncwarp();
+        load(x ? &maps.v : &maps.k, sbase + L::kFix + x * L::kTile, it[kKt] * kBlock, it[kHk], it[kB],
+             &bars->fix_full[x]);
+      };
+      // Q and -lse (x = 0) or dY and -delta (1) of block n
+      auto load_block = [&](const int32_t* it, int n, int x) {
+        const uint32_t s = nr % SL;
+        if (nr >= SL) ok = ok && wait(&bars->empty[s], (nr / SL - 1) & 1);
+        if (!ok) return;
+        const int h = it[kHk] * a.g + n / it[kNq], qb = it[kKt] + n % it[kNq];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->full[s], L::kTile + 512);
+          const int64_t at = ((int64_t)it[kB] * a.H + h) * stats.pad + (int64_t)qb * kBlock;
+          if (x)
+            bulk_load(sbase + L::kStatD + (t % L::kNd) * 512, stats.nd + at, 512, &bars->full[s]);
+          else
+            bulk_load(sbase + L::kStatL + (t % L::kNl) * 512, stats.nl + at, 512, &bars->full[s]);
+        }
+        __syncwarp();
+        load(x ? &maps.dy : &maps.q, sbase + L::kRing + s * L::kTile, qb * kBlock, h, it[kB],
+             &bars->full[s]);
+        ++nr;
+        if (x) ++t;
+      };
+      while (const int32_t* it = ring.take(ok)) {
+        const int n0 = it[kN0], n1 = it[kN1];
+        load_fix(it, 0);
+        load_block(it, n0, 0);
+        load_fix(it, 1);
+        load_block(it, n0, 1);
+        for (int n = n0 + 1; n < n1 && ok; ++n) {
+          load_block(it, n, 0);
+          load_block(it, n, 1);
+        }
+        ring.give_back(it);
+      }
+      if (lane == 0) {   // every copy has landed before the CTA may exit
+        for (uint32_t i = nr > SL ? nr - SL : 0; i < nr; ++i)
+          mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
+        for (int x = 0; x < 2; ++x)
+          if (nf[x] > 0) mbar_wait(&bars->fix_full[x], (nf[x] - 1) & 1, a.err);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- products
+      const uint64_t fix_d = sw128_desc(sbase + L::kFix, 16, 1024);
+      const uint64_t row_d = sw128_desc(sbase + L::kRing, 16, 1024);
+      const uint64_t col_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      // S^T (x = 0) or dP^T (1) of block n of the item (the ni-th), the t-th block
+      auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
+        const uint32_t i = 2 * t + x, s = i % SL;
+        ok = ok && wait(&bars->full[s], (i / SL) & 1);
+        if (ok && n == it[kN0]) ok = wait(&bars->fix_full[x], ni & 1);
+        if (!ok) return;
+        const int live = it[kLen] - (it[kKt] + n % it[kNq]) * kBlock;
+        if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
+        fence_after();
+        if (lane == 0) {
+          mma_tiles<D>(tmem + (x ? kTP : kTS), desc_add(fix_d, x * L::kTile),
+                       desc_add(row_d, s * L::kTile));
+          mma_commit(x ? &bars->dp_full : &bars->s_full[0]);
+          if (n + 1 == it[kN1]) mma_commit(&bars->fix_empty[x]);
+        }
+        __syncwarp();
+      };
+      uint32_t t = 0, ni = 0;
+      const int32_t* it = ring.take(ok);
+      if (it != nullptr) {
+        issue(it, it[kN0], 0, 0, 0);
+        issue(it, it[kN0], 0, 0, 1);
+      }
+      while (it != nullptr && ok) {
+        const int n0 = it[kN0], n1 = it[kN1];
+        const int32_t* nx = it;
+        for (int n = n0; n < n1 && ok; ++n, ++t) {
+          const bool end = n + 1 == n1;
+          if (end) nx = ring.take(ok);
+          const int nn = end ? (nx ? nx[kN0] : 0) : n + 1;
+          const uint32_t sq = (2 * t) % SL, sg = (2 * t + 1) % SL;
+          ok = ok && wait(&bars->p_full, t & 1);
+          if (!ok) break;
+          fence_after();
+          if (lane == 0) {
+            mma_packed<D>(tmem + kTV, tmem + kTS, desc_add(col_d, sg * L::kTile), n > n0);
+            mma_commit(&bars->empty[sg]);
+          }
+          __syncwarp();
+          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 0);
+          ok = ok && wait(&bars->ds_full, t & 1);
+          if (!ok) break;
+          fence_after();
+          if (lane == 0) {
+            mma_packed<D>(tmem + kTK, tmem + kTP, desc_add(col_d, sq * L::kTile), n > n0);
+            mma_commit(&bars->empty[sq]);
+            if (end) mma_commit(&bars->acc_full);
+          }
+          __syncwarp();
+          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 1);
+        }
+        ring.give_back(it);
+        it = nx;
+        ++ni;
+      }
+      if (lane == 0) {
+        mma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, a.err);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp + 1 && lane == 0) {
+      // ---------------------------------------------------------------- items
+      int b = bars->cut[0], hk = bars->cut[1], kt = bars->cut[2], off = bars->cut[3], left = bars->cut[4];
+      int order = 0;
+      for (uint32_t n = 0;; ++n) {
+        if (n >= kItems && !mbar_wait(&bars->item_empty[n % kItems], (n / kItems - 1) & 1, a.err)) break;
+        int32_t* it = bars->items[n % kItems];
+        int len = b < a.B ? length_of(a, b) : 0;
+        while (b < a.B && kt * kBlock >= len) {   // the next key head, the next sequence
+          kt = 0;
+          if (++hk == a.Hkv) {
+            hk = 0;
+            ++b;
+            len = b < a.B ? length_of(a, b) : 0;
+          }
+        }
+        const bool more = left > 0 && b < a.B;
+        if (more) {
+          const int nq = query_blocks(a, len, kt), nb = nq * a.g;
+          it[kB] = b, it[kHk] = hk, it[kLen] = len, it[kKt] = kt, it[kNb] = nb, it[kNq] = nq;
+          it[kN0] = off;
+          it[kN1] = min(nb, off + left);
+          it[kOrder] = order++;
+          left -= it[kN1] - off;
+          off = 0;
+          ++kt;
+        } else {
+          it[kB] = -1;
+        }
+        mbar_arrive(&bars->item_full[n % kItems]);
+        if (!more) break;
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Key tiles cut between CTAs: their partials added up in the CTAs' order.  Block
+// x = 1 .. CTAs - 1 takes the tile that CTA x begins inside of, if x is its second
+// CTA.
+template <int D>
+__global__ void __launch_bounds__(256) dkv_combine_kernel(const AttendArgs a, int ctas) {
+  __shared__ int64_t found[2];
+  __shared__ Cut cut;
+  const int c = blockIdx.x + 1;
+  if (threadIdx.x < 32) {
+    const int64_t total = all_units(a), per = run_length(total, ctas), w0 = per * c;
+    Cut f{0, 0, 0, 0};
+    if (w0 < total) f = find_unit(a, w0);
+    if (threadIdx.x == 0) {
+      cut = f;
+      found[0] = per;
+      found[1] = w0;
+    }
+  }
+  __syncthreads();
+  if (cut.off == 0) return;
+  const int64_t per = found[0], begin = found[1] - cut.off;
+  const int first = (int)(begin / per);
+  if (first != c - 1) return;
+  const int len = length_of(a, cut.b);
+  const int nb = query_blocks(a, len, cut.kt) * a.g;
+  const int last = (int)((begin + nb - 1) / per);
+  const int first_slot = begin == first * per ? 0 : 1;   // the tile is that run's first item, or its last
+  for (int x = blockIdx.y * 256 + threadIdx.x; x < 2 * kBlock * (D / 4); x += 256 * gridDim.y) {
+    const int which = x / (kBlock * (D / 4)), row = x / (D / 4) % kBlock, col = x % (D / 4) * 4;
+    const int j = cut.kt * kBlock + row;
+    if (j >= a.N) continue;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < len) {
+#pragma unroll 4
+      for (int i = first; i <= last; ++i) {
+        const float4 p = *reinterpret_cast<const float4*>(
+            partial(a, D, i * 2 + (i == first ? first_slot : 0), which, row) + col);
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+      }
+    }
+    const float f = which ? a.scale : 1.f;
+    const Strides so = which ? a.sdk : a.sdv;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(which ? a.dk : a.dv) + cut.b * so.b + cut.hk * so.h +
+                       (int64_t)j * so.n + col;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(s.x * f, s.y * f);
+    const __nv_bfloat162 w = __floats2bfloat162_rn(s.z * f, s.w * f);
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
+  }
+}
+
+// ---- dq ----------------------------------------------------------------------------
+
+// Fields of a query tile's item.
+enum { qB, qH, qLen, qT, qSink, qFirst, qN };
+ELSAA_DEV int key_block(const int32_t* it, int n) {
+  return n < it[qSink] ? n : it[qFirst] + n - it[qSink];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const Stats stats, int tiles) {
+  using L = Lay<D>;
+  constexpr int SL = L::kSlots;
+  constexpr uint32_t kTP = 256, kTQ = 384;   // S at 0 and 128
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((sbase & 1023u) != 0) {
+    if (tid == 0) raise_error(a.err, ERR_CHECK);
+    return;
+  }
+  if (tid == 0) init_bars(bars);
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+  bool ok = true;
+  ItemRing ring{bars, a.err};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
+  };
+
+  if (warp < kTmaWarp) {
+    // ------------------------------------------------------------------ elementwise
+    regs_up<kWorkRegs>();
+    const int half = warp >> 2, row = tid & 127;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    uint32_t t = 0, ni = 0;
+    while (const int32_t* it = ring.take(ok)) {
+      const int r0 = it[qT] * kBlock, r = r0 + row, blocks = it[qN], len = it[qLen];
+      const int64_t at = ((int64_t)it[qB] * a.H + it[qH]) * stats.pad + r;
+      const float nl = stats.nl[at], nd = stats.nd[at];
+      const int p_last = min(len, r0 + kBlock) - 1;
+      for (int n = 0; n < blocks; ++n, ++t) {
+        const int j0 = key_block(it, n) * kBlock;
+        ok = wait(&bars->s_full[t & 1], (t >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        float p[64];
+        const uint32_t tS = tmem + 128 * (t & 1) + 64 * half + lane_off;
+        const uint32_t tP = tmem + kTP + 64 * half + lane_off;
+        tmem_ld32(tS, p);
+        tmem_ld32(tS + 32, p + 32);
+        tmem_ld_wait();
+        fence_before();
+        mbar_arrive(&bars->s_read[t & 1]);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          fma2(p[e], p[e + 1], scale_log2, scale_log2, nl, nl);
+          p[e] = ex2(p[e]);
+          p[e + 1] = ex2(p[e + 1]);
+        }
+        if (j0 + kBlock - 1 > r0 || (int64_t)j0 <= (int64_t)p_last - a.window) {
+          const int hi = r - j0 - 64 * half, lo = r - a.window + 1 - j0 - 64 * half;
+          const int sk = (int)min((int64_t)a.sinks - j0 - 64 * half, (int64_t)64);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t see =
+                upto_bits(hi - 32 * c) & (~upto_bits(lo - 1 - 32 * c) | upto_bits(sk - 1 - 32 * c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) p[32 * c + e] = 0.f;
+          }
+        }
+        ok = wait(&bars->dp_full, t & 1);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dp[32];
+          tmem_ld32(tP + 32 * c, dp);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            add2(dp[e], dp[e + 1], nd, nd);
+            mul2(p[32 * c + e], p[32 * c + e + 1], dp[e], dp[e + 1]);
+          }
+        }
+        store_packed(tP, p);   // dS over dP
+        tmem_st_wait();
+        fence_before();
+        mbar_arrive(&bars->ds_full);
+      }
+      if (!ok) break;
+      if (blocks > 0) {
+        ok = wait(&bars->acc_full, ni & 1);
+        if (!ok) break;
+        ++ni;
+        fence_after();
+      }
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.dq) + it[qB] * a.sdq.b + it[qH] * a.sdq.h +
+                            (int64_t)r * a.sdq.n + half * (D / 2);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        float v[32];
+        if (blocks > 0) {
+          tmem_ld32(tmem + kTQ + half * (D / 2) + 32 * c + lane_off, v);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = blocks > 0 && r < len ? v[e] * a.scale : 0.f;
+        if (r < a.N) store32(orow + 32 * c, v);
+        // a tile behind the length has no key tile either: its zeros
+        if (blocks == 0 && it[qH] % a.g == 0 && r < a.N) {
+          const int hk = it[qH] / a.g;
+          store32(static_cast<__nv_bfloat16*>(a.dk) + it[qB] * a.sdk.b + hk * a.sdk.h +
+                      (int64_t)r * a.sdk.n + half * (D / 2) + 32 * c, v);
+          store32(static_cast<__nv_bfloat16*>(a.dv) + it[qB] * a.sdv.b + hk * a.sdv.h +
+                      (int64_t)r * a.sdv.n + half * (D / 2) + 32 * c, v);
+        }
+      }
+      fence_before();
+      ring.give_back(it);
+    }
+  } else {
+    regs_down<kOtherRegs>();
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------------- copies
+      uint32_t nr = 0, nf[2] = {0, 0};
+      auto load = [&](const CUtensorMap* map, uint32_t dst, int n, int h, int b, uint64_t* bar) {
+        if (lane < D / 64) tma_load_4d(dst + lane * kAtom, map, 64 * lane, n, h, b, bar);
+        __syncwarp();
+      };
+      auto load_fix = [&](const int32_t* it, int x) {   // Q, dY
+        if (nf[x] > 0) ok = ok && wait(&bars->fix_empty[x], (nf[x] - 1) & 1);
+        if (!ok) return;
+        ++nf[x];
+        if (lane == 0) mbar_arrive_expect_tx(&bars->fix_full[x], L::kTile);
+        __syncwarp();
+        load(x ? &maps.dy : &maps.q, sbase + L::kFix + x * L::kTile, it[qT] * kBlock, it[qH], it[qB],
+             &bars->fix_full[x]);
+      };
+      auto load_block = [&](const int32_t* it, int n, int x) {   // K, V
+        const uint32_t s = nr % SL;
+        if (nr >= SL) ok = ok && wait(&bars->empty[s], (nr / SL - 1) & 1);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], L::kTile);
+        __syncwarp();
+        load(x ? &maps.v : &maps.k, sbase + L::kRing + s * L::kTile, key_block(it, n) * kBlock,
+             it[qH] / a.g, it[qB], &bars->full[s]);
+        ++nr;
+      };
+      while (const int32_t* it = ring.take(ok)) {
+        const int blocks = it[qN];
+        if (blocks > 0) {
+          load_fix(it, 0);
+          load_block(it, 0, 0);
+          load_fix(it, 1);
+          load_block(it, 0, 1);
+          for (int n = 1; n < blocks && ok; ++n) {
+            load_block(it, n, 0);
+            load_block(it, n, 1);
+          }
+        }
+        ring.give_back(it);
+      }
+      if (lane == 0) {   // every copy has landed before the CTA may exit
+        for (uint32_t i = nr > SL ? nr - SL : 0; i < nr; ++i)
+          mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
+        for (int x = 0; x < 2; ++x)
+          if (nf[x] > 0) mbar_wait(&bars->fix_full[x], (nf[x] - 1) & 1, a.err);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- products
+      const uint64_t fix_d = sw128_desc(sbase + L::kFix, 16, 1024);
+      const uint64_t row_d = sw128_desc(sbase + L::kRing, 16, 1024);
+      const uint64_t col_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      // S (x = 0) or dP (1) of block n of the item (the ni-th with blocks), the t-th block
+      auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
+        const uint32_t i = 2 * t + x, s = i % SL;
+        if (x == 0 && t >= 2) ok = ok && wait(&bars->s_read[t & 1], ((t >> 1) - 1) & 1);
+        ok = ok && wait(&bars->full[s], (i / SL) & 1);
+        if (ok && n == 0) ok = wait(&bars->fix_full[x], ni & 1);
+        if (!ok) return;
+        const int live = it[qLen] - key_block(it, n) * kBlock;
+        if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
+        fence_after();
+        if (lane == 0) {
+          mma_tiles<D>(tmem + (x ? kTP : 128 * (t & 1)), desc_add(fix_d, x * L::kTile),
+                       desc_add(row_d, s * L::kTile));
+          mma_commit(x ? &bars->dp_full : &bars->s_full[t & 1]);
+          if (x) mma_commit(&bars->empty[s]);
+          if (n + 1 == it[qN]) mma_commit(&bars->fix_empty[x]);
+        }
+        __syncwarp();
+      };
+      // the next item that has blocks
+      auto take = [&]() -> const int32_t* {
+        const int32_t* it = ring.take(ok);
+        while (it != nullptr && it[qN] == 0) {
+          ring.give_back(it);
+          it = ring.take(ok);
+        }
+        return it;
+      };
+      uint32_t t = 0, ni = 0;
+      const int32_t* it = take();
+      if (it != nullptr) {
+        issue(it, 0, 0, 0, 0);
+        issue(it, 0, 0, 0, 1);
+      }
+      while (it != nullptr && ok) {
+        const int blocks = it[qN];
+        const int32_t* nx = it;
+        for (int n = 0; n < blocks && ok; ++n, ++t) {
+          const bool end = n + 1 == blocks;
+          if (end) nx = take();
+          const int nn = end ? 0 : n + 1;
+          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 0);
+          ok = ok && wait(&bars->ds_full, t & 1);
+          if (!ok) break;
+          fence_after();
+          const uint32_t sk = (2 * t) % SL;
+          if (lane == 0) {
+            mma_packed<D>(tmem + kTQ, tmem + kTP, desc_add(col_d, sk * L::kTile), n > 0);
+            mma_commit(&bars->empty[sk]);
+            if (end) mma_commit(&bars->acc_full);
+          }
+          __syncwarp();
+          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 1);
+        }
+        ring.give_back(it);
+        it = nx;
+        ++ni;
+      }
+      if (lane == 0) {
+        mma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, a.err);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp + 1 && lane == 0) {
+      // ---------------------------------------------------------------- items
+      const int64_t bh = (int64_t)a.B * a.H, items = bh * tiles;
+      int64_t x = blockIdx.x;
+      for (uint32_t n = 0;; ++n, x += gridDim.x) {
+        if (n >= kItems && !mbar_wait(&bars->item_empty[n % kItems], (n / kItems - 1) & 1, a.err)) break;
+        int32_t* it = bars->items[n % kItems];
+        const bool more = x < items;
+        if (more) {   // the longest (last) tiles first, heads and batches inside
+          const int t = tiles - 1 - (int)(x / bh), b = (int)(x % bh / a.H), h = (int)(x % a.H);
+          const int len = length_of(a, b);
+          const KeyBlocks k = key_blocks(t * kBlock, min(len, (t + 1) * kBlock) - 1, a.window, a.sinks, kBlock);
+          it[qB] = b, it[qH] = h, it[qLen] = len, it[qT] = t;
+          it[qSink] = k.sink_blocks, it[qFirst] = k.first, it[qN] = k.count();
+        } else {
+          it[qB] = -1;
+        }
+        mbar_arrive(&bars->item_full[n % kItems]);
+        if (!more) break;
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- launches ------------------------------------------------------------------------
+
+int64_t padded_rows(int N) { return ((int64_t)N + kBlock - 1) / kBlock * kBlock; }
+
+template <int D>
+cudaError_t backward(const AttendArgs& args, cudaStream_t s) {
+  AttendArgs a = args;
+  const int tiles = (a.N + kBlock - 1) / kBlock;
+  Stats st;
+  st.pad = padded_rows(a.N);
+  const int64_t rows = (int64_t)a.B * a.H * st.pad;
+  st.nl = a.delta;
+  st.nd = st.nl + rows;
+  a.scratch = reinterpret_cast<char*>(st.nd + rows);
+  Maps maps;
+  cudaError_t e;
+  const uint32_t box[4] = {64, kBlock, 1, 1};
+  if ((e = make_map_4d(&maps.q, a.q, D, a.N, a.H, a.B, a.sq.n, a.sq.h, a.sq.b, box)) != cudaSuccess ||
+      (e = make_map_4d(&maps.k, a.k, D, a.N, a.Hkv, a.B, a.sk.n, a.sk.h, a.sk.b, box)) != cudaSuccess ||
+      (e = make_map_4d(&maps.v, a.v, D, a.N, a.Hkv, a.B, a.sv.n, a.sv.h, a.sv.b, box)) != cudaSuccess ||
+      (e = make_map_4d(&maps.dy, a.dy, D, a.N, a.H, a.B, a.sdy.n, a.sdy.h, a.sdy.b, box)) != cudaSuccess)
+    return e;
+  constexpr int kRows = 256 / (D / 8);
+  stats_kernel<D><<<(unsigned)((rows + kRows - 1) / kRows), 256, 0, s>>>(a, st);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int smem = (int)Lay<D>::kDyn;
+  e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  window_dkv_kernel<D><<<ctas, kThreads, smem, s>>>(maps, a, st);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (ctas > 1) {
+    dkv_combine_kernel<D><<<dim3(ctas - 1, 8), 256, 0, s>>>(a, ctas);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t items = (int64_t)a.B * a.H * tiles;
+  window_dq_kernel<D><<<(int)(items < sms ? items : sms), kThreads, smem, s>>>(maps, a, st, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N) {
+  if (!attend_tc_supported(d, bf16)) return align_up((size_t)(B * H * N) * sizeof(float));
+  return (size_t)(B * H * padded_rows((int)N)) * 2 * sizeof(float) +
+         (size_t)kMaxCtas * 2 * 2 * kBlock * d * sizeof(float);
+}
+
+cudaError_t launch_window_bwd_tc(const AttendArgs& a, cudaStream_t s) {
+  return a.d == 64 ? backward<64>(a, s) : backward<128>(a, s);
+}
+
+}  // namespace elsaa

@@ -38,26 +38,21 @@
 // its loop, and copies and products in flight end before TMEM is freed.
 #include <math.h>
 
-#include "attend.cuh"
+#include "attend_tc.cuh"
 #include "internal.h"
-#include "layer.h"
-#include "tc_common.cuh"
 
 namespace elsaa {
 namespace {
 
 using namespace tc;
 
-constexpr int kBlock = 128;              // rows of a stream, keys of a block
 constexpr int kThreads = 384;
 // registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr uint32_t kAtom = 128 * 128;    // 128 rows x 64 bf16
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTO = 256;            // O of stream s at kTO + 128 s; S (and P) at 128 s
 constexpr float kGrow = 8.0f;            // log2 of the growth that rescales O
-constexpr int kMaxCtas = 160;            // of a paged call (the workspace holds their partials)
 constexpr int kMinUnits = 2;             // a run shorter than this is not worth a CTA
 
 template <int D>
@@ -84,10 +79,6 @@ struct Shape {
   float scale_log2;
   int slot_rows;    // pages: rows of a partial slot
 };
-
-// x[s] of a pair that stays in registers.
-template <typename T>
-ELSAA_DEV T pick(const T (&x)[2], int s) { return s ? x[1] : x[0]; }
 
 // One CTA's piece of work: rows of both streams against the blocks n0 .. n1 - 1
 // of the item's block list.
@@ -314,41 +305,6 @@ struct Walk {
 };
 
 // ---- kernel ------------------------------------------------------------------
-
-// 2^x on the special-function unit (approximate, flushes denormals).
-ELSAA_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-ELSAA_DEV void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-// Registers of this thread, by whole warpgroups.
-template <int N>
-ELSAA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-ELSAA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-ELSAA_DEV void store32(__nv_bfloat16* p, const float* v) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-      w[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// Columns <= x of 32.
-ELSAA_DEV uint32_t upto_bits(int x) { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; }
 
 // The scratch of a paged call: partial rows [slot][row][D] and (m, l) [slot][row];
 // slot = ((cta * 2 + (not the run's first item)) * 2 + stream).

@@ -84,7 +84,11 @@ cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 // tcgen05 kernels: bf16, d = 64 or 128.
 bool attend_tc_supported(int d, bool bf16);
 cudaError_t launch_window_fwd_tc(const AttendArgs& a, cudaStream_t s);
+// (a.delta: window_scratch_bytes of workspace)
+cudaError_t launch_window_bwd_tc(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
+// Workspace bytes of the window backward: row statistics, and partials of cut tiles.
+size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N);
 // Workspace bytes of launch_paged_tc's partial rows.
 size_t paged_scratch_bytes(int d, bool bf16, int64_t rows, int g);
 

@@ -202,7 +202,7 @@ elsaa_status elsaa_window_validate(const elsaa_window_params* p) { return check(
 size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backward) {
   if (check(p) != ELSAA_OK) return 0;
   if (!backward) return kErrBytes;
-  return kErrBytes + align_up((size_t)p->B * p->H * p->N * sizeof(float));
+  return kErrBytes + window_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->B, p->H, p->N);
 }
 
 static elsaa_status window_args(const elsaa_window_params* p, const void* const* tensors,
@@ -269,6 +269,7 @@ elsaa_status elsaa_window_backward(const elsaa_window_params* p, const void* q, 
   a.dk = dk;
   a.dv = dv;
   const bool bf16 = p->dtype == ELSAA_BF16;
+  if (attend_tc_supported(p->d, bf16)) return cuda_status(launch_window_bwd_tc(a, (cudaStream_t)stream));
   cudaError_t e = launch_window_delta(a, bf16, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_window_bwd_simt(a, bf16, (cudaStream_t)stream);
   return cuda_status(e);
