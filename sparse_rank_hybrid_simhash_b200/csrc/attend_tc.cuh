@@ -28,6 +28,67 @@ ELSAA_DEV void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+// One lane of the warp (always the same one), by the instruction that tells the
+// compiler so: operands of the tensor-core instructions live in uniform registers,
+// and behind a plain lane test each is moved there by itself (a 128 x 128 x 128
+// product took 1400 cycles to issue instead of about 100).
+ELSAA_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// A value that is the same in every lane, known to be.
+ELSAA_DEV uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Low words of the shared-memory descriptors of a tile at `saddr` (128-byte
+// swizzle, 8-row groups 1024 bytes apart): read by rows (K-major), or by columns
+// (the next 64 of them kAtom further on).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+ELSAA_DEV uint32_t row_desc(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+ELSAA_DEV uint32_t col_desc(uint32_t saddr) { return (saddr >> 4) | ((kAtom >> 4) << 16); }
+
+// D[tmem] (+)= A B of descriptors' low words (mma_bf16_ss, _ts); the elected lane.
+ELSAA_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+ELSAA_DEV void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+
+// 128 x 128 product of two K-major tiles over D.
+template <int D>
+ELSAA_DEV void mma_tiles(uint32_t d_tmem, uint32_t ad, uint32_t bd) {
+  constexpr uint32_t id = idesc_bf16(128, kBlock, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32) >> 4;
+    mma_ss(d_tmem, ad + off, bd + off, id, kk > 0 ? 1u : 0u);
+  }
+}
+
+// One arrival for the warp: what its lanes did before is ordered by the warp's
+// barrier (32 arrivals at one address would queue up).
+ELSAA_DEV void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 // Registers of this thread, by whole warpgroups.
 template <int N>
 ELSAA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }

@@ -148,27 +148,16 @@ ELSAA_DEV void zero_rows(uint8_t* tile, int live) {
   __syncwarp();
 }
 
-// 128 x 128 product of two K-major tiles over D.
-template <int D>
-ELSAA_DEV void mma_tiles(uint32_t d_tmem, uint64_t ad, uint64_t bd) {
-  constexpr uint32_t id = idesc_bf16(128, kBlock, false, false);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32;
-    mma_bf16_ss(d_tmem, desc_add(ad, off), desc_add(bd, off), id, kk > 0 ? 1u : 0u);
-  }
-}
-
 // D[128 x D] (+)= A X, A the bf16 tile that both halves of the elementwise threads
 // left in TMEM (columns 0..63 packed from `a`, 64..127 from a + 64), X [128, D] in
 // shared memory.
 template <int D>
-ELSAA_DEV void mma_packed(uint32_t d_tmem, uint32_t a, uint64_t xd, bool accumulate) {
+ELSAA_DEV void mma_packed(uint32_t d_tmem, uint32_t a, uint32_t xd, bool accumulate) {
   constexpr uint32_t id = idesc_bf16(128, D, false, true);
 #pragma unroll
   for (int x = 0; x < kBlock; x += 16)
-    mma_bf16_ts(d_tmem, a + (uint32_t)((x >> 6) * 64 + ((x & 63) >> 1)),
-                desc_add(xd, (uint32_t)(x >> 4) * 2048), id, (accumulate || x > 0) ? 1u : 0u);
+    mma_ts(d_tmem, a + (uint32_t)((x >> 6) * 64 + ((x & 63) >> 1)), xd + (uint32_t)x * 8, id,
+           (accumulate || x > 0) ? 1u : 0u);
 }
 
 // 64 fp32 values to 32 packed columns.
@@ -216,11 +205,11 @@ ELSAA_DEV void init_bars(Bars* b) {
     mbar_init(&b->fix_full[i], 1);
     mbar_init(&b->fix_empty[i], 1);
     mbar_init(&b->s_full[i], 1);
-    mbar_init(&b->s_read[i], 256);
+    mbar_init(&b->s_read[i], 8);   // elementwise warps
   }
   mbar_init(&b->dp_full, 1);
-  mbar_init(&b->p_full, 256);
-  mbar_init(&b->ds_full, 256);
+  mbar_init(&b->p_full, 8);
+  mbar_init(&b->ds_full, 8);
   mbar_init(&b->acc_full, 1);
   for (int i = 0; i < kItems; ++i) {
     mbar_init(&b->item_full[i], 1);
@@ -405,7 +394,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         ok = wait(&bars->full[(2 * t + 1) % SL], ((2 * t + 1) / SL) & 1);
         if (!ok) break;
         fence_before();
-        mbar_arrive(&bars->p_full);
+        warp_arrive(&bars->p_full);
         ok = wait(&bars->dp_full, t & 1);
         if (!ok) break;
         fence_after();
@@ -426,7 +415,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         store_packed(tP, p);   // dS^T over dP^T
         tmem_st_wait();
         fence_before();
-        mbar_arrive(&bars->ds_full);
+        warp_arrive(&bars->ds_full);
       }
       if (!ok) break;
       ok = wait(&bars->acc_full, ni & 1);
@@ -521,9 +510,11 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- products
-      const uint64_t fix_d = sw128_desc(sbase + L::kFix, 16, 1024);
-      const uint64_t row_d = sw128_desc(sbase + L::kRing, 16, 1024);
-      const uint64_t col_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      const uint32_t tm = uniform(tmem);
+      const uint32_t fix_d = row_desc(sbase + L::kFix);
+      const uint32_t row_d = row_desc(sbase + L::kRing);
+      const uint32_t col_d = col_desc(sbase + L::kRing);
+      constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
       // S^T (x = 0) or dP^T (1) of block n of the item (the ni-th), the t-th block
       auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
         const uint32_t i = 2 * t + x, s = i % SL;
@@ -533,9 +524,9 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         const int live = it[kLen] - (it[kKt] + n % it[kNq]) * kBlock;
         if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
         fence_after();
-        if (lane == 0) {
-          mma_tiles<D>(tmem + (x ? kTP : kTS), desc_add(fix_d, x * L::kTile),
-                       desc_add(row_d, s * L::kTile));
+        const uint32_t bd = uniform(row_d + s * kStep);
+        if (elect_one()) {
+          mma_tiles<D>(tm + (x ? kTP : kTS), fix_d + x * kStep, bd);
           mma_commit(x ? &bars->dp_full : &bars->s_full[0]);
           if (n + 1 == it[kN1]) mma_commit(&bars->fix_empty[x]);
         }
@@ -558,8 +549,10 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           ok = ok && wait(&bars->p_full, t & 1);
           if (!ok) break;
           fence_after();
-          if (lane == 0) {
-            mma_packed<D>(tmem + kTV, tmem + kTS, desc_add(col_d, sg * L::kTile), n > n0);
+          const uint32_t gd = uniform(col_d + sg * kStep), qd = uniform(col_d + sq * kStep);
+          const bool add = uniform(n > n0) != 0;
+          if (elect_one()) {
+            mma_packed<D>(tm + kTV, tm + kTS, gd, add);
             mma_commit(&bars->empty[sg]);
           }
           __syncwarp();
@@ -567,8 +560,8 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           ok = ok && wait(&bars->ds_full, t & 1);
           if (!ok) break;
           fence_after();
-          if (lane == 0) {
-            mma_packed<D>(tmem + kTK, tmem + kTP, desc_add(col_d, sq * L::kTile), n > n0);
+          if (elect_one()) {
+            mma_packed<D>(tm + kTK, tm + kTP, qd, add);
             mma_commit(&bars->empty[sq]);
             if (end) mma_commit(&bars->acc_full);
           }
@@ -579,7 +572,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         it = nx;
         ++ni;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, a.err);
       }
@@ -739,7 +732,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         tmem_ld32(tS + 32, p + 32);
         tmem_ld_wait();
         fence_before();
-        mbar_arrive(&bars->s_read[t & 1]);
+        warp_arrive(&bars->s_read[t & 1]);
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           fma2(p[e], p[e + 1], scale_log2, scale_log2, nl, nl);
@@ -775,7 +768,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         store_packed(tP, p);   // dS over dP
         tmem_st_wait();
         fence_before();
-        mbar_arrive(&bars->ds_full);
+        warp_arrive(&bars->ds_full);
       }
       if (!ok) break;
       if (blocks > 0) {
@@ -859,9 +852,11 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- products
-      const uint64_t fix_d = sw128_desc(sbase + L::kFix, 16, 1024);
-      const uint64_t row_d = sw128_desc(sbase + L::kRing, 16, 1024);
-      const uint64_t col_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      const uint32_t tm = uniform(tmem);
+      const uint32_t fix_d = row_desc(sbase + L::kFix);
+      const uint32_t row_d = row_desc(sbase + L::kRing);
+      const uint32_t col_d = col_desc(sbase + L::kRing);
+      constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
       // S (x = 0) or dP (1) of block n of the item (the ni-th with blocks), the t-th block
       auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
         const uint32_t i = 2 * t + x, s = i % SL;
@@ -872,9 +867,9 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         const int live = it[qLen] - key_block(it, n) * kBlock;
         if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
         fence_after();
-        if (lane == 0) {
-          mma_tiles<D>(tmem + (x ? kTP : 128 * (t & 1)), desc_add(fix_d, x * L::kTile),
-                       desc_add(row_d, s * L::kTile));
+        const uint32_t bd = uniform(row_d + s * kStep), td = uniform(tm + (x ? kTP : 128 * (t & 1)));
+        if (elect_one()) {
+          mma_tiles<D>(td, fix_d + x * kStep, bd);
           mma_commit(x ? &bars->dp_full : &bars->s_full[t & 1]);
           if (x) mma_commit(&bars->empty[s]);
           if (n + 1 == it[qN]) mma_commit(&bars->fix_empty[x]);
@@ -907,9 +902,10 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
           ok = ok && wait(&bars->ds_full, t & 1);
           if (!ok) break;
           fence_after();
-          const uint32_t sk = (2 * t) % SL;
-          if (lane == 0) {
-            mma_packed<D>(tmem + kTQ, tmem + kTP, desc_add(col_d, sk * L::kTile), n > 0);
+          const uint32_t sk = (2 * t) % SL, kd = uniform(col_d + sk * kStep);
+          const bool add = uniform(n > 0) != 0;
+          if (elect_one()) {
+            mma_packed<D>(tm + kTQ, tm + kTP, kd, add);
             mma_commit(&bars->empty[sk]);
             if (end) mma_commit(&bars->acc_full);
           }
@@ -920,7 +916,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         it = nx;
         ++ni;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, a.err);
       }

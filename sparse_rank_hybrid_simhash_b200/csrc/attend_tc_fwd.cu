@@ -341,11 +341,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_full[s], 128);
+      mbar_init(&bars->p_full[s], 4);   // a stream's warps
       mbar_init(&bars->o_full[s], 1);
     }
-    mbar_init(&bars->x_full, 128);
-    mbar_init(&bars->x_done, 128);
+    mbar_init(&bars->x_full, 4);
+    mbar_init(&bars->x_done, 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
       mbar_init(&bars->item_empty[i], 10);   // eight softmax warps, TMA, MMA
@@ -482,7 +482,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
         any = true;
         fence_before();
-        mbar_arrive(&bars->p_full[st]);
+        warp_arrive(&bars->p_full[st]);
       }
       if (!ok) break;
       if (any) {
@@ -500,7 +500,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           ml1[row] = any ? m : -INFINITY;
           ml1[128 + row] = any ? l : 0.f;
           fence_before();
-          mbar_arrive(&bars->x_full);
+          warp_arrive(&bars->x_full);
         } else {
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_full, nx & 1, a.err));
           if (!ok) break;
@@ -571,7 +571,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       fence_before();
       if (PAGED && it.split) {
         if (st == 0) {
-          mbar_arrive(&bars->x_done);
+          warp_arrive(&bars->x_done);
         } else {
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_done, nx & 1, a.err));
           if (!ok) break;
@@ -667,11 +667,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
 
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------ products
-      const uint32_t id_s = idesc_bf16(128, kBlock, false, false);
-      const uint32_t id_pv = idesc_bf16(128, D, false, true);
-      const uint64_t q_d = sw128_desc(sbase + L::kQ, 16, 1024);
-      const uint64_t k_d = sw128_desc(sbase + L::kRing, 16, 1024);
-      const uint64_t v_d = sw128_desc(sbase + L::kRing, kAtom, 1024);
+      constexpr uint32_t id_pv = idesc_bf16(128, D, false, true);
+      constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
+      const uint32_t tm = uniform(tmem);
+      const uint32_t q_d = row_desc(sbase + L::kQ);
+      const uint32_t k_d = row_desc(sbase + L::kRing), v_d = col_desc(sbase + L::kRing);
       uint32_t nr = 0, nq = 0, np[2] = {0, 0};
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
@@ -713,13 +713,13 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
               ok = wait(&bars->p_full[s], np[s] & 1);
               ++np[s];
               fence_after();
-              if (ok && lane == 0) {
-                const uint64_t vd = desc_add(v_d, (iv % SL) * L::kTile);
-  #pragma unroll
+              const uint32_t vd = uniform(v_d + (iv % SL) * kStep);
+              const uint32_t add = uniform(any[s]);
+              if (ok && elect_one()) {
+#pragma unroll
                 for (int x = 0; x < kBlock; x += 16)
-                  mma_bf16_ts(tmem + kTO + 128 * s, tmem + 128 * s + (x >> 1),
-                              desc_add(vd, (uint32_t)(x >> 4) * 2048), id_pv,
-                              (any[s] || x > 0) ? 1u : 0u);
+                  mma_ts(tm + kTO + 128 * s, tm + 128 * s + (x >> 1), vd + x * 8, id_pv,
+                         x > 0 ? 1u : add);
                 if (pend[s] == last[s]) mma_commit(&bars->o_full[s]);
               }
               __syncwarp();
@@ -728,22 +728,17 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             }
             if (ok && n < it.n1 && it.uses(s, n)) {   // S_s = Q_s K^T of block n
               fence_after();
-              if (lane == 0) {
-                const uint64_t qd = desc_add(q_d, it.split ? 0 : s * L::kTile);
-                const uint64_t kd = desc_add(k_d, (ik % SL) * L::kTile);
-  #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32;
-                  mma_bf16_ss(tmem + 128 * s, desc_add(qd, off), desc_add(kd, off), id_s,
-                              kk > 0 ? 1u : 0u);
-                }
+              const uint32_t qd = uniform(q_d + (it.split ? 0 : s * kStep));
+              const uint32_t kd = uniform(k_d + (ik % SL) * kStep);
+              if (elect_one()) {
+                mma_tiles<D>(tm + 128 * s, qd, kd);
                 mma_commit(&bars->s_full[s]);
               }
               __syncwarp();
               pend[s] = n;
             }
           }
-          if (ok && lane == 0) {
+          if (ok && elect_one()) {
             if (n < it.n1) mma_commit(&bars->empty[ik % SL]);
             if (n > it.n0) mma_commit(&bars->empty[iv % SL]);
             if (n + 1 == it.n1) mma_commit(&bars->q_empty);
@@ -753,7 +748,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         ++nq;
         give_back();
       }
-      if (lane == 0) {   // the products issued so far end before TMEM is freed
+      if (elect_one()) {   // the products issued so far end before TMEM is freed
         mma_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, a.err);
       }
