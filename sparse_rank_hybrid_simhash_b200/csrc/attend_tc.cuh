@@ -83,6 +83,23 @@ ELSAA_DEV void mma_tiles(uint32_t d_tmem, uint32_t ad, uint32_t bd) {
   }
 }
 
+// A place in a ring of N slots, and the parity of its phase there.
+template <int N>
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  ELSAA_DEV void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
+// The whole warp waits for the barrier's phase; bounded (ERR_TIMEOUT).
+ELSAA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  for (uint32_t i = 0; i < kMaxSpin; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  raise_error(err, ERR_TIMEOUT);
+  return false;
+}
+
 // One arrival for the warp: what its lanes did before is ordered by the warp's
 // barrier (32 arrivals at one address would queue up).
 ELSAA_DEV void warp_arrive(uint64_t* bar) {

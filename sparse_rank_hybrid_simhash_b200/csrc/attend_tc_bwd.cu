@@ -152,12 +152,12 @@ ELSAA_DEV void zero_rows(uint8_t* tile, int live) {
 // left in TMEM (columns 0..63 packed from `a`, 64..127 from a + 64), X [128, D] in
 // shared memory.
 template <int D>
-ELSAA_DEV void mma_packed(uint32_t d_tmem, uint32_t a, uint32_t xd, bool accumulate) {
+ELSAA_DEV void mma_packed(uint32_t d_tmem, uint32_t a, uint32_t xd, uint32_t accumulate) {
   constexpr uint32_t id = idesc_bf16(128, D, false, true);
 #pragma unroll
   for (int x = 0; x < kBlock; x += 16)
     mma_ts(d_tmem, a + (uint32_t)((x >> 6) * 64 + ((x & 63) >> 1)), xd + (uint32_t)x * 8, id,
-           (accumulate || x > 0) ? 1u : 0u);
+           x > 0 ? 1u : accumulate);
 }
 
 // 64 fp32 values to 32 packed columns.
@@ -183,7 +183,7 @@ struct ItemRing {
   ELSAA_DEV const int32_t* take(bool& ok) {
     if (!ok) return nullptr;
     const uint32_t i = taken % kItems;
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[i], (taken / kItems) & 1, err));
+    ok = warp_wait(&bars->item_full[i], (taken / kItems) & 1, err);
     const int32_t* it = bars->items[i];
     if (!ok || it[0] < 0) return nullptr;
     ++taken;
@@ -342,7 +342,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   bool ok = true;
   ItemRing ring{bars, a.err};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
+    return warp_wait(bar, parity, a.err);
   };
 
   if (warp < kTmaWarp) {
@@ -354,11 +354,13 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     const float scale_log2 = a.scale * 1.4426950408889634f;
     uint32_t t = 0, ni = 0;
     while (const int32_t* it = ring.take(ok)) {
-      const int j0 = it[kKt] * kBlock, j = j0 + row;
-      for (int n = it[kN0], n1 = it[kN1]; n < n1; ++n, ++t) {
-        const int i0 = (it[kKt] + n % it[kNq]) * kBlock;
-        ok = wait(&bars->s_full[0], t & 1) &&
-             wait(&bars->full[(2 * t) % SL], ((2 * t) / SL) & 1);   // (-lse has landed)
+      const int kt = it[kKt], nq = it[kNq], j0 = kt * kBlock, j = j0 + row;
+      int q = it[kN0] % nq;   // query block of the head, from the key tile's on
+      for (int left = it[kN1] - it[kN0]; left > 0; --left, ++t) {
+        const int i0 = j0 + q * kBlock;
+        if (++q == nq) q = 0;
+        // (S^T is there: its Q has landed before it, and -lse with Q)
+        ok = wait(&bars->s_full[0], t & 1);
         if (!ok) break;
         fence_after();
         const float* nl = reinterpret_cast<const float*>(smem + L::kStatL) + (t % L::kNl) * 128 + 64 * half;
@@ -390,12 +392,9 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
         store_packed(tS, p);   // P^T over S^T
         tmem_st_wait();
-        // -delta has landed (asked before P is given: with dV its slot may be loaded anew)
-        ok = wait(&bars->full[(2 * t + 1) % SL], ((2 * t + 1) / SL) & 1);
-        if (!ok) break;
         fence_before();
         warp_arrive(&bars->p_full);
-        ok = wait(&bars->dp_full, t & 1);
+        ok = wait(&bars->dp_full, t & 1);   // (and -delta with dY)
         if (!ok) break;
         fence_after();
 #pragma unroll
@@ -474,7 +473,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         const uint32_t s = nr % SL;
         if (nr >= SL) ok = ok && wait(&bars->empty[s], (nr / SL - 1) & 1);
         if (!ok) return;
-        const int h = it[kHk] * a.g + n / it[kNq], qb = it[kKt] + n % it[kNq];
+        const int nq = it[kNq], h = it[kHk] * a.g + n / nq, qb = it[kKt] + n % nq;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->full[s], L::kTile + 512);
           const int64_t at = ((int64_t)it[kB] * a.H + h) * stats.pad + (int64_t)qb * kBlock;
@@ -515,62 +514,98 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       const uint32_t row_d = row_desc(sbase + L::kRing);
       const uint32_t col_d = col_desc(sbase + L::kRing);
       constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
-      // S^T (x = 0) or dP^T (1) of block n of the item (the ni-th), the t-th block
-      auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
-        const uint32_t i = 2 * t + x, s = i % SL;
-        ok = ok && wait(&bars->full[s], (i / SL) & 1);
-        if (ok && n == it[kN0]) ok = wait(&bars->fix_full[x], ni & 1);
-        if (!ok) return;
-        const int live = it[kLen] - (it[kKt] + n % it[kNq]) * kBlock;
-        if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
+      // the block whose S^T and dP^T come next
+      struct {
+        const int32_t* it;
+        int left, q, nq, j0, len;   // blocks of the item from it on; its query block
+        bool first;
+        uint32_t item;              // items before its own
+      } nx;
+      uint32_t items = 0;
+      auto open = [&]() {   // the next item's first block
+        nx.it = ring.take(ok);
+        if (nx.it == nullptr) return;
+        nx.left = nx.it[kN1] - nx.it[kN0];
+        nx.nq = nx.it[kNq];
+        nx.q = nx.it[kN0] % nx.nq;
+        nx.j0 = nx.it[kKt] * kBlock;
+        nx.len = nx.it[kLen];
+        nx.first = true;
+        nx.item = items++;
+      };
+      // Q (x = 0) or dY (1) of that block is in shared memory, zeros behind the length
+      auto ready = [&](int x, const RingPos<SL>& at) {
+        ok = ok && wait(&bars->full[at.slot], at.phase);
+        if (ok && nx.first) ok = wait(&bars->fix_full[x], nx.item & 1);
+        const int live = nx.len - nx.j0 - nx.q * kBlock;
+        if (ok && a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + at.slot * L::kTile, live);
+      };
+      // its product (the elected lane)
+      auto issue = [&](int x, uint32_t d, uint32_t bd) {
+        mma_tiles<D>(d, fix_d + x * kStep, bd);
+        mma_commit(x ? &bars->dp_full : &bars->s_full[0]);
+        if (nx.left == 1) mma_commit(&bars->fix_empty[x]);
+      };
+      auto advance = [&]() {
+        if (++nx.q == nx.nq) nx.q = 0;
+        --nx.left;
+        nx.first = false;
+      };
+      RingPos<SL> at;   // the ring slot to wait for next
+      uint32_t t = 0;
+      open();
+      uint32_t sq = 0, sg = 0;   // slots of Q and dY of block t
+      const int32_t* it = nx.it;
+      bool first = true, more = it != nullptr;
+      if (more) {
+        for (int x = 0; x < 2; ++x) {
+          ready(x, at);
+          (x ? sg : sq) = at.slot;
+          const uint32_t bd = uniform(row_d + at.slot * kStep);
+          at.next();
+          if (ok && elect_one()) issue(x, tm + (x ? kTP : kTS), bd);
+          __syncwarp();
+        }
+        advance();
+      }
+      while (more && ok) {
+        // block t: dV += P^T dY and the next S^T, then dK += dS^T Q and the next dP^T
+        const bool end = nx.left == 0;
+        if (end) open();
+        more = nx.it != nullptr;
+        const uint32_t gd = uniform(col_d + sg * kStep), qd = uniform(col_d + sq * kStep);
+        const uint32_t add = uniform(first ? 0u : 1u);
+        const uint32_t nq = at.slot, nqd = uniform(row_d + nq * kStep);
+        if (more) ready(0, at), at.next();
+        ok = ok && wait(&bars->p_full, t & 1);
+        if (!ok) break;
         fence_after();
-        const uint32_t bd = uniform(row_d + s * kStep);
         if (elect_one()) {
-          mma_tiles<D>(tm + (x ? kTP : kTS), fix_d + x * kStep, bd);
-          mma_commit(x ? &bars->dp_full : &bars->s_full[0]);
-          if (n + 1 == it[kN1]) mma_commit(&bars->fix_empty[x]);
+          mma_packed<D>(tm + kTV, tm + kTS, gd, add);
+          mma_commit(&bars->empty[sg]);
+          if (more) issue(0, tm + kTS, nqd);
         }
         __syncwarp();
-      };
-      uint32_t t = 0, ni = 0;
-      const int32_t* it = ring.take(ok);
-      if (it != nullptr) {
-        issue(it, it[kN0], 0, 0, 0);
-        issue(it, it[kN0], 0, 0, 1);
-      }
-      while (it != nullptr && ok) {
-        const int n0 = it[kN0], n1 = it[kN1];
-        const int32_t* nx = it;
-        for (int n = n0; n < n1 && ok; ++n, ++t) {
-          const bool end = n + 1 == n1;
-          if (end) nx = ring.take(ok);
-          const int nn = end ? (nx ? nx[kN0] : 0) : n + 1;
-          const uint32_t sq = (2 * t) % SL, sg = (2 * t + 1) % SL;
-          ok = ok && wait(&bars->p_full, t & 1);
-          if (!ok) break;
-          fence_after();
-          const uint32_t gd = uniform(col_d + sg * kStep), qd = uniform(col_d + sq * kStep);
-          const bool add = uniform(n > n0) != 0;
-          if (elect_one()) {
-            mma_packed<D>(tm + kTV, tm + kTS, gd, add);
-            mma_commit(&bars->empty[sg]);
-          }
-          __syncwarp();
-          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 0);
-          ok = ok && wait(&bars->ds_full, t & 1);
-          if (!ok) break;
-          fence_after();
-          if (elect_one()) {
-            mma_packed<D>(tm + kTK, tm + kTP, qd, add);
-            mma_commit(&bars->empty[sq]);
-            if (end) mma_commit(&bars->acc_full);
-          }
-          __syncwarp();
-          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 1);
+        const uint32_t ng = at.slot, ngd = uniform(row_d + ng * kStep);
+        if (more) ready(1, at), at.next();
+        ok = ok && wait(&bars->ds_full, t & 1);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          mma_packed<D>(tm + kTK, tm + kTP, qd, add);
+          mma_commit(&bars->empty[sq]);
+          if (end) mma_commit(&bars->acc_full);
+          if (more) issue(1, tm + kTP, ngd);
         }
-        ring.give_back(it);
-        it = nx;
-        ++ni;
+        __syncwarp();
+        first = end;
+        if (end) {
+          ring.give_back(it);
+          it = nx.it;
+        }
+        if (more) advance();
+        sq = nq, sg = ng;
+        ++t;
       }
       if (elect_one()) {
         mma_commit(&bars->drain);
@@ -705,7 +740,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
   bool ok = true;
   ItemRing ring{bars, a.err};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
+    return warp_wait(bar, parity, a.err);
   };
 
   if (warp < kTmaWarp) {
@@ -857,64 +892,90 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
       const uint32_t row_d = row_desc(sbase + L::kRing);
       const uint32_t col_d = col_desc(sbase + L::kRing);
       constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
-      // S (x = 0) or dP (1) of block n of the item (the ni-th with blocks), the t-th block
-      auto issue = [&](const int32_t* it, int n, uint32_t t, uint32_t ni, int x) {
-        const uint32_t i = 2 * t + x, s = i % SL;
-        if (x == 0 && t >= 2) ok = ok && wait(&bars->s_read[t & 1], ((t >> 1) - 1) & 1);
-        ok = ok && wait(&bars->full[s], (i / SL) & 1);
-        if (ok && n == 0) ok = wait(&bars->fix_full[x], ni & 1);
-        if (!ok) return;
-        const int live = it[qLen] - key_block(it, n) * kBlock;
-        if (a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + s * L::kTile, live);
-        fence_after();
-        const uint32_t bd = uniform(row_d + s * kStep), td = uniform(tm + (x ? kTP : 128 * (t & 1)));
-        if (elect_one()) {
-          mma_tiles<D>(td, fix_d + x * kStep, bd);
-          mma_commit(x ? &bars->dp_full : &bars->s_full[t & 1]);
-          if (x) mma_commit(&bars->empty[s]);
-          if (n + 1 == it[qN]) mma_commit(&bars->fix_empty[x]);
+      // the block whose S and dP come next
+      struct {
+        const int32_t* it;
+        int n, blocks, len;
+        uint32_t item;   // items with blocks before its own
+      } nx;
+      uint32_t items = 0;
+      auto open = [&]() {   // the first block of the next item that has any
+        nx.it = ring.take(ok);
+        while (nx.it != nullptr && nx.it[qN] == 0) {
+          ring.give_back(nx.it);
+          nx.it = ring.take(ok);
         }
-        __syncwarp();
+        if (nx.it == nullptr) return;
+        nx.n = 0;
+        nx.blocks = nx.it[qN];
+        nx.len = nx.it[qLen];
+        nx.item = items++;
       };
-      // the next item that has blocks
-      auto take = [&]() -> const int32_t* {
-        const int32_t* it = ring.take(ok);
-        while (it != nullptr && it[qN] == 0) {
-          ring.give_back(it);
-          it = ring.take(ok);
+      // K (x = 0) or V (1) of that block is in shared memory, zeros behind the length
+      auto ready = [&](int x, const RingPos<SL>& at) {
+        ok = ok && wait(&bars->full[at.slot], at.phase);
+        if (ok && nx.n == 0) ok = wait(&bars->fix_full[x], nx.item & 1);
+        if (ok && a.lengths) {
+          const int live = nx.len - key_block(nx.it, nx.n) * kBlock;
+          if (live < kBlock) zero_rows<D>(smem + L::kRing + at.slot * L::kTile, live);
         }
-        return it;
       };
-      uint32_t t = 0, ni = 0;
-      const int32_t* it = take();
-      if (it != nullptr) {
-        issue(it, 0, 0, 0, 0);
-        issue(it, 0, 0, 0, 1);
+      auto issue = [&](int x, uint32_t d, uint32_t bd, uint32_t s, uint32_t t) {   // the elected lane
+        mma_tiles<D>(d, fix_d + x * kStep, bd);
+        mma_commit(x ? &bars->dp_full : &bars->s_full[t & 1]);
+        if (x) mma_commit(&bars->empty[s]);
+        if (nx.n + 1 == nx.blocks) mma_commit(&bars->fix_empty[x]);
+      };
+      RingPos<SL> at;
+      uint32_t t = 0, sk = 0;   // slot of K of block t
+      open();
+      const int32_t* it = nx.it;
+      bool first = true, more = it != nullptr;
+      if (more) {
+        for (int x = 0; x < 2; ++x) {
+          ready(x, at);
+          const uint32_t s = at.slot, bd = uniform(row_d + s * kStep);
+          at.next();
+          if (ok && elect_one()) issue(x, tm + (x ? kTP : 0), bd, s, 0);
+          __syncwarp();
+        }
+        ++nx.n;
       }
-      while (it != nullptr && ok) {
-        const int blocks = it[qN];
-        const int32_t* nx = it;
-        for (int n = 0; n < blocks && ok; ++n, ++t) {
-          const bool end = n + 1 == blocks;
-          if (end) nx = take();
-          const int nn = end ? 0 : n + 1;
-          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 0);
-          ok = ok && wait(&bars->ds_full, t & 1);
+      while (more && ok) {
+        // block t: the next S, then dQ += dS K and the next dP
+        const bool end = nx.n == nx.blocks;
+        if (end) open();
+        more = nx.it != nullptr;
+        const uint32_t kd = uniform(col_d + sk * kStep), add = uniform(first ? 0u : 1u);
+        const uint32_t nk = at.slot, nkd = uniform(row_d + nk * kStep), td = uniform(tm + 128 * ((t + 1) & 1));
+        if (more) {
+          ready(0, at), at.next();
+          if (t >= 1) ok = ok && wait(&bars->s_read[(t + 1) & 1], (((t + 1) >> 1) - 1) & 1);
           if (!ok) break;
           fence_after();
-          const uint32_t sk = (2 * t) % SL, kd = uniform(col_d + sk * kStep);
-          const bool add = uniform(n > 0) != 0;
-          if (elect_one()) {
-            mma_packed<D>(tm + kTQ, tm + kTP, kd, add);
-            mma_commit(&bars->empty[sk]);
-            if (end) mma_commit(&bars->acc_full);
-          }
+          if (elect_one()) issue(0, td, nkd, nk, t + 1);
           __syncwarp();
-          if (nx) issue(nx, nn, t + 1, ni + (end ? 1 : 0), 1);
         }
-        ring.give_back(it);
-        it = nx;
-        ++ni;
+        const uint32_t nv = at.slot, nvd = uniform(row_d + nv * kStep);
+        if (more) ready(1, at), at.next();
+        ok = ok && wait(&bars->ds_full, t & 1);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          mma_packed<D>(tm + kTQ, tm + kTP, kd, add);
+          mma_commit(&bars->empty[sk]);
+          if (end) mma_commit(&bars->acc_full);
+          if (more) issue(1, tm + kTP, nvd, nv, t + 1);
+        }
+        __syncwarp();
+        first = end;
+        if (end) {
+          ring.give_back(it);
+          it = nx.it;
+        }
+        if (more) ++nx.n;
+        sk = nk;
+        ++t;
       }
       if (elect_one()) {
         mma_commit(&bars->drain);

@@ -381,7 +381,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   // the next item, or null behind the last one (or where a wait gave up)
   auto take = [&]() -> const Item* {
     if (!ok) return nullptr;
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[ni % kItems], (ni / kItems) & 1, a.err));
+    ok = warp_wait(&bars->item_full[ni % kItems], (ni / kItems) & 1, a.err);
     const Item* it = &bars->items[ni % kItems];
     return ok && it->order >= 0 ? it : nullptr;
   };
@@ -411,7 +411,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       bool any = false;
       for (int n = it.n0; n < it.n1; ++n) {
         if (!it.uses(st, n)) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[st], ns & 1, a.err));
+        ok = warp_wait(&bars->s_full[st], ns & 1, a.err);
         if (!ok) break;
         ++ns;
         fence_after();
@@ -486,7 +486,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       }
       if (!ok) break;
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[st], no & 1, a.err));
+        ok = warp_wait(&bars->o_full[st], no & 1, a.err);
         if (!ok) break;
         ++no;
         fence_after();
@@ -502,7 +502,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           fence_before();
           warp_arrive(&bars->x_full);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_full, nx & 1, a.err));
+          ok = warp_wait(&bars->x_full, nx & 1, a.err);
           if (!ok) break;
           fence_after();
           const float m1 = ml1[row], l1 = ml1[128 + row], mm = fmaxf(m, m1);
@@ -573,7 +573,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         if (st == 0) {
           warp_arrive(&bars->x_done);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_done, nx & 1, a.err));
+          ok = warp_wait(&bars->x_done, nx & 1, a.err);
           if (!ok) break;
         }
         ++nx;
@@ -589,7 +589,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       // the slot for the next load, free and armed
       auto acquire = [&]() -> uint32_t {
         const uint32_t s = nr % SL;
-        if (nr >= SL) ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (nr / SL - 1) & 1, a.err));
+        if (nr >= SL) ok = warp_wait(&bars->empty[s], (nr / SL - 1) & 1, a.err);
         if (ok && lane == 0) mbar_arrive_expect_tx(&bars->full[s], L::kTile);
         __syncwarp();
         if (ok) ++nr;
@@ -636,7 +636,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
         load_block(it, it.n0);
         // Q behind the first block: its slots wait for the previous item's last scores
-        if (ok && nq > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (nq - 1) & 1, a.err));
+        if (ok && nq > 0) ok = warp_wait(&bars->q_empty, (nq - 1) & 1, a.err);
         if (!ok) break;
         if (lane == 0) {
           const int tiles = it.split ? 1 : 2;
@@ -672,78 +672,80 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       const uint32_t tm = uniform(tmem);
       const uint32_t q_d = row_desc(sbase + L::kQ);
       const uint32_t k_d = row_desc(sbase + L::kRing), v_d = col_desc(sbase + L::kRing);
-      uint32_t nr = 0, nq = 0, np[2] = {0, 0};
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err));
-      };
+      uint32_t nq = 0, np[2] = {0, 0};
+      RingPos<SL> at;   // the ring slot of the next load: K of a block, then V
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, a.err); };
       while (const Item* item = take()) {
         const Item& it = *item;
-        if (it.n0 >= it.n1) {
+        const int n0 = it.n0, n1 = it.n1, len = it.len;
+        if (n0 >= n1) {
           give_back();
           continue;
         }
         const int last[2] = {it.last_use(0), it.last_use(1)};
-        int pend[2] = {-1, -1};
-        bool any[2] = {false, false};
-        const uint32_t base = nr;          // ring index of K of block n0
-        nr += 2 * (it.n1 - it.n0);
-        for (int n = it.n0; n <= it.n1 && ok; ++n) {
-          const uint32_t ik = base + 2 * (n - it.n0), iv = ik - 1;   // K of n, V of n - 1
-          if (n < it.n1) {
-            ok = wait(&bars->full[ik % SL], (ik / SL) & 1);
-            if (ok && n == it.n0) ok = wait(&bars->q_full, nq & 1);
+        const uint32_t q_of[2] = {uniform(q_d), uniform(q_d + (it.split ? 0 : kStep))};
+        bool pend[2] = {false, false};
+        uint32_t add[2] = {0, 0};
+        uint32_t sv = 0;                   // slot of V of block n - 1
+        for (int n = n0; n <= n1 && ok; ++n) {
+          // what block n needs is awaited before the softmax of block n - 1
+          const bool more = n < n1;
+          const uint32_t sk = at.slot;
+          if (more) {
+            ok = wait(&bars->full[sk], at.phase);
+            if (ok && n == n0) ok = wait(&bars->q_full, nq & 1);
+            at.next();
           }
-          if (ok && n > it.n0) {
-            ok = wait(&bars->full[iv % SL], (iv / SL) & 1);
-            const int live = it.len - it.block(n - 1) * kBlock;
+          const uint32_t kd = uniform(k_d + sk * kStep), vd = uniform(v_d + sv * kStep);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const bool use = more && it.uses(s, n);
+            if (pend[s]) {
+              ok = ok && wait(&bars->p_full[s], np[s] & 1);
+              ++np[s];
+            }
+            if (!ok) break;
+            fence_after();
+            if (elect_one()) {
+              if (pend[s]) {               // O_s (+)= P_s V of block n - 1
+#pragma unroll
+                for (int x = 0; x < kBlock; x += 16)
+                  mma_ts(tm + kTO + 128 * s, tm + 128 * s + (x >> 1), vd + x * 8, id_pv,
+                         x > 0 ? 1u : add[s]);
+                if (n - 1 == last[s]) mma_commit(&bars->o_full[s]);
+              }
+              if (use) {                   // S_s = Q_s K^T of block n
+                mma_tiles<D>(tm + 128 * s, q_of[s], kd);
+                mma_commit(&bars->s_full[s]);
+              }
+            }
+            __syncwarp();
+            if (pend[s]) add[s] = 1;
+            pend[s] = use;
+          }
+          if (!ok) break;
+          if (elect_one()) {
+            if (more) mma_commit(&bars->empty[sk]);
+            if (n > n0) mma_commit(&bars->empty[sv]);
+            if (n + 1 == n1) mma_commit(&bars->q_empty);
+          }
+          __syncwarp();
+          if (more) {                      // V of block n
+            sv = at.slot;
+            ok = wait(&bars->full[sv], at.phase);
+            at.next();
+            const int live = len - it.block(n) * kBlock;
             if (ok && live < kBlock && (PAGED || a.lengths != nullptr)) {
               // value rows behind the length: zeros
-              uint8_t* v = smem + L::kRing + (iv % SL) * L::kTile;
+              uint8_t* v = smem + L::kRing + sv * L::kTile;
               for (int r = live * 8 + lane; r < kBlock * 8; r += 32)
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                   *reinterpret_cast<uint4*>(v + c * kAtom + r * 16) = make_uint4(0, 0, 0, 0);
               fence_async_smem();
               __syncwarp();
             }
           }
-  #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (ok && pend[s] >= 0) {            // O_s (+)= P_s V of block n - 1
-              ok = wait(&bars->p_full[s], np[s] & 1);
-              ++np[s];
-              fence_after();
-              const uint32_t vd = uniform(v_d + (iv % SL) * kStep);
-              const uint32_t add = uniform(any[s]);
-              if (ok && elect_one()) {
-#pragma unroll
-                for (int x = 0; x < kBlock; x += 16)
-                  mma_ts(tm + kTO + 128 * s, tm + 128 * s + (x >> 1), vd + x * 8, id_pv,
-                         x > 0 ? 1u : add);
-                if (pend[s] == last[s]) mma_commit(&bars->o_full[s]);
-              }
-              __syncwarp();
-              any[s] = true;
-              pend[s] = -1;
-            }
-            if (ok && n < it.n1 && it.uses(s, n)) {   // S_s = Q_s K^T of block n
-              fence_after();
-              const uint32_t qd = uniform(q_d + (it.split ? 0 : s * kStep));
-              const uint32_t kd = uniform(k_d + (ik % SL) * kStep);
-              if (elect_one()) {
-                mma_tiles<D>(tm + 128 * s, qd, kd);
-                mma_commit(&bars->s_full[s]);
-              }
-              __syncwarp();
-              pend[s] = n;
-            }
-          }
-          if (ok && elect_one()) {
-            if (n < it.n1) mma_commit(&bars->empty[ik % SL]);
-            if (n > it.n0) mma_commit(&bars->empty[iv % SL]);
-            if (n + 1 == it.n1) mma_commit(&bars->q_empty);
-          }
-          __syncwarp();
         }
         ++nq;
         give_back();
