@@ -39,8 +39,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;            // 8 elementwise warps, TMA, MMA, items, one idle
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;            // 8 elementwise warps, TMA, two MMA, items
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kItemWarp = 11;
 // registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
 constexpr int kWorkRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
@@ -196,10 +196,10 @@ struct ItemRing {
   }
 };
 
-ELSAA_DEV void init_bars(Bars* b) {
+ELSAA_DEV void init_bars(Bars* b, int acc) {
   for (int i = 0; i < 8; ++i) {
     mbar_init(&b->full[i], 1);
-    mbar_init(&b->empty[i], 1);
+    mbar_init(&b->empty[i], 2);            // both MMA warps
   }
   for (int i = 0; i < 2; ++i) {
     mbar_init(&b->fix_full[i], 1);
@@ -210,12 +210,12 @@ ELSAA_DEV void init_bars(Bars* b) {
   mbar_init(&b->dp_full, 1);
   mbar_init(&b->p_full, 8);
   mbar_init(&b->ds_full, 8);
-  mbar_init(&b->acc_full, 1);
+  mbar_init(&b->acc_full, acc);            // MMA warps with an accumulator
   for (int i = 0; i < kItems; ++i) {
     mbar_init(&b->item_full[i], 1);
-    mbar_init(&b->item_empty[i], 10);   // eight elementwise warps, TMA, MMA
+    mbar_init(&b->item_empty[i], 11);   // eight elementwise warps, TMA, two MMA
   }
-  mbar_init(&b->drain, 1);
+  mbar_init(&b->drain, 2);
   fence_mbar_init();
 }
 
@@ -315,7 +315,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     if (tid == 0) raise_error(a.err, ERR_CHECK);
     return;
   }
-  if (tid == 0) init_bars(bars);
+  if (tid == 0) init_bars(bars, 2);
   if (warp == 0) {   // this CTA's run of units
     const int64_t total = all_units(a), per = run_length(total, gridDim.x), w0 = per * blockIdx.x;
     Cut c{0, 0, 0, 0};
@@ -507,112 +507,102 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           if (nf[x] > 0) mbar_wait(&bars->fix_full[x], (nf[x] - 1) & 1, a.err);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kItemWarp) {
       // ---------------------------------------------------------------- products
+      // Warp x = 0: S^T (from Q) and dV (from dY); x = 1: dP^T (from dY) and dK (from
+      // Q).  One warp's waits and bookkeeping run under the other's products.
+      const int x = warp - kMmaWarp;
       const uint32_t tm = uniform(tmem);
-      const uint32_t fix_d = row_desc(sbase + L::kFix);
-      const uint32_t row_d = row_desc(sbase + L::kRing);
-      const uint32_t col_d = col_desc(sbase + L::kRing);
+      const uint32_t fix_d = uniform(row_desc(sbase + L::kFix + x * L::kTile));
+      const uint32_t row_d = row_desc(sbase + L::kRing), col_d = col_desc(sbase + L::kRing);
       constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
-      // the block whose S^T and dP^T come next
-      struct {
-        const int32_t* it;
-        int left, q, nq, j0, len;   // blocks of the item from it on; its query block
-        bool first;
-        uint32_t item;              // items before its own
-      } nx;
+      const uint32_t t_new = uniform(tm + (x ? kTP : kTS)), t_acc = uniform(tm + (x ? kTK : kTV));
+      uint64_t* const gate = x ? &bars->ds_full : &bars->p_full;
+      uint64_t* const done = x ? &bars->dp_full : &bars->s_full[0];
+      // the block whose S^T or dP^T comes next
+      const int32_t* it = nullptr;
+      int left = 0, q = 0, nq = 1, j0 = 0, len = 0, live = 0;   // blocks of its item from it on
+      bool first = false;
       uint32_t items = 0;
       auto open = [&]() {   // the next item's first block
-        nx.it = ring.take(ok);
-        if (nx.it == nullptr) return;
-        nx.left = nx.it[kN1] - nx.it[kN0];
-        nx.nq = nx.it[kNq];
-        nx.q = nx.it[kN0] % nx.nq;
-        nx.j0 = nx.it[kKt] * kBlock;
-        nx.len = nx.it[kLen];
-        nx.first = true;
-        nx.item = items++;
+        it = ring.take(ok);
+        if (it == nullptr) return;
+        left = it[kN1] - it[kN0];
+        nq = it[kNq];
+        q = it[kN0] % nq;
+        j0 = it[kKt] * kBlock;
+        len = it[kLen];
+        first = true;
+        ++items;
       };
-      // Q (x = 0) or dY (1) of that block is in shared memory, zeros behind the length
-      auto ready = [&](int x, const RingPos<SL>& at) {
+      // a tile is in shared memory, zeros behind the length
+      auto ready = [&](const RingPos<SL>& at, int rows) {
         ok = ok && wait(&bars->full[at.slot], at.phase);
-        if (ok && nx.first) ok = wait(&bars->fix_full[x], nx.item & 1);
-        const int live = nx.len - nx.j0 - nx.q * kBlock;
-        if (ok && a.lengths && live < kBlock) zero_rows<D>(smem + L::kRing + at.slot * L::kTile, live);
+        if (ok && a.lengths && rows < kBlock) zero_rows<D>(smem + L::kRing + at.slot * L::kTile, rows);
       };
-      // its product (the elected lane)
-      auto issue = [&](int x, uint32_t d, uint32_t bd) {
-        mma_tiles<D>(d, fix_d + x * kStep, bd);
-        mma_commit(x ? &bars->dp_full : &bars->s_full[0]);
-        if (nx.left == 1) mma_commit(&bars->fix_empty[x]);
+      RingPos<SL> own, other;   // Q, dY (x = 0) or dY, Q (1)
+      if (x) own.next(); else other.next();
+      // the next block's operand, awaited before the elementwise work
+      auto prepare = [&]() {
+        live = len - j0 - q * kBlock;
+        ready(own, live);
+        if (ok && first) ok = wait(&bars->fix_full[x], (items - 1) & 1);
+      };
+      auto issue = [&](uint32_t d) {   // its product (the elected lane)
+        mma_tiles<D>(t_new, fix_d, d);
+        mma_commit(done);
+        mma_commit(&bars->empty[own.slot]);
+        if (left == 1) mma_commit(&bars->fix_empty[x]);
       };
       auto advance = [&]() {
-        if (++nx.q == nx.nq) nx.q = 0;
-        --nx.left;
-        nx.first = false;
+        own.next(), own.next();
+        if (++q == nq) q = 0;
+        --left;
+        first = false;
       };
-      RingPos<SL> at;   // the ring slot to wait for next
-      uint32_t t = 0;
       open();
-      uint32_t sq = 0, sg = 0;   // slots of Q and dY of block t
-      const int32_t* it = nx.it;
-      bool first = true, more = it != nullptr;
-      if (more) {
-        for (int x = 0; x < 2; ++x) {
-          ready(x, at);
-          (x ? sg : sq) = at.slot;
-          const uint32_t bd = uniform(row_d + at.slot * kStep);
-          at.next();
-          if (ok && elect_one()) issue(x, tm + (x ? kTP : kTS), bd);
-          __syncwarp();
-        }
+      if (it != nullptr) {
+        prepare();
+        const uint32_t d = uniform(row_d + own.slot * kStep);
+        fence_after();
+        if (ok && elect_one()) issue(d);
+        __syncwarp();
         advance();
       }
-      while (more && ok) {
-        // block t: dV += P^T dY and the next S^T, then dK += dS^T Q and the next dP^T
-        const bool end = nx.left == 0;
-        if (end) open();
-        more = nx.it != nullptr;
-        const uint32_t gd = uniform(col_d + sg * kStep), qd = uniform(col_d + sq * kStep);
-        const uint32_t add = uniform(first ? 0u : 1u);
-        const uint32_t nq = at.slot, nqd = uniform(row_d + nq * kStep);
-        if (more) ready(0, at), at.next();
-        ok = ok && wait(&bars->p_full, t & 1);
-        if (!ok) break;
-        fence_after();
-        if (elect_one()) {
-          mma_packed<D>(tm + kTV, tm + kTS, gd, add);
-          mma_commit(&bars->empty[sg]);
-          if (more) issue(0, tm + kTS, nqd);
-        }
-        __syncwarp();
-        const uint32_t ng = at.slot, ngd = uniform(row_d + ng * kStep);
-        if (more) ready(1, at), at.next();
-        ok = ok && wait(&bars->ds_full, t & 1);
-        if (!ok) break;
-        fence_after();
-        if (elect_one()) {
-          mma_packed<D>(tm + kTK, tm + kTP, qd, add);
-          mma_commit(&bars->empty[sq]);
-          if (end) mma_commit(&bars->acc_full);
-          if (more) issue(1, tm + kTP, ngd);
-        }
-        __syncwarp();
-        first = end;
+      uint32_t add = 0;
+      for (uint32_t t = 0; it != nullptr && ok; ++t) {   // block t's accumulation and the next product
+        const int rows = live;
+        const bool end = left == 0;
         if (end) {
-          ring.give_back(it);
-          it = nx.it;
+          const int32_t* was = it;
+          open();
+          ring.give_back(was);
         }
+        const bool more = it != nullptr;
+        if (more) prepare();
+        ready(other, rows);
+        const uint32_t d = uniform(row_d + own.slot * kStep), od = uniform(col_d + other.slot * kStep);
+        const uint32_t acc = uniform(add);
+        ok = ok && wait(gate, t & 1);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          mma_packed<D>(t_acc, t_new, od, acc);
+          mma_commit(&bars->empty[other.slot]);
+          if (end) mma_commit(&bars->acc_full);
+          if (more) issue(d);
+        }
+        __syncwarp();
+        add = end ? 0 : 1;
+        other.next(), other.next();
         if (more) advance();
-        sq = nq, sg = ng;
-        ++t;
       }
       if (elect_one()) {
         mma_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, a.err);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp + 1 && lane == 0) {
+    } else if (lane == 0) {
       // ---------------------------------------------------------------- items
       int b = bars->cut[0], hk = bars->cut[1], kt = bars->cut[2], off = bars->cut[3], left = bars->cut[4];
       int order = 0;
@@ -728,7 +718,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
     if (tid == 0) raise_error(a.err, ERR_CHECK);
     return;
   }
-  if (tid == 0) init_bars(bars);
+  if (tid == 0) init_bars(bars, 1);
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem, kTmemCols);
     tmem_relinquish();
@@ -885,104 +875,116 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
           if (nf[x] > 0) mbar_wait(&bars->fix_full[x], (nf[x] - 1) & 1, a.err);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kItemWarp) {
       // ---------------------------------------------------------------- products
+      // Warp x = 0: S (from K); x = 1: dP (from V) and dQ (from K).
+      const int x = warp - kMmaWarp;
       const uint32_t tm = uniform(tmem);
-      const uint32_t fix_d = row_desc(sbase + L::kFix);
-      const uint32_t row_d = row_desc(sbase + L::kRing);
-      const uint32_t col_d = col_desc(sbase + L::kRing);
+      const uint32_t fix_d = uniform(row_desc(sbase + L::kFix + x * L::kTile));
+      const uint32_t row_d = row_desc(sbase + L::kRing), col_d = col_desc(sbase + L::kRing);
       constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
-      // the block whose S and dP come next
-      struct {
-        const int32_t* it;
-        int n, blocks, len;
-        uint32_t item;   // items with blocks before its own
-      } nx;
+      const int32_t* it = nullptr;
+      int n = 0, blocks = 0, len = 0;
       uint32_t items = 0;
       auto open = [&]() {   // the first block of the next item that has any
-        nx.it = ring.take(ok);
-        while (nx.it != nullptr && nx.it[qN] == 0) {
-          ring.give_back(nx.it);
-          nx.it = ring.take(ok);
+        it = ring.take(ok);
+        while (it != nullptr && it[qN] == 0) {
+          ring.give_back(it);
+          it = ring.take(ok);
         }
-        if (nx.it == nullptr) return;
-        nx.n = 0;
-        nx.blocks = nx.it[qN];
-        nx.len = nx.it[qLen];
-        nx.item = items++;
+        if (it == nullptr) return;
+        n = 0;
+        blocks = it[qN];
+        len = it[qLen];
+        ++items;
       };
-      // K (x = 0) or V (1) of that block is in shared memory, zeros behind the length
-      auto ready = [&](int x, const RingPos<SL>& at) {
-        ok = ok && wait(&bars->full[at.slot], at.phase);
-        if (ok && nx.n == 0) ok = wait(&bars->fix_full[x], nx.item & 1);
+      RingPos<SL> own, other;   // K, V (x = 0) or V, K (1)
+      if (x) own.next(); else other.next();
+      // the next block's operand is in shared memory, zeros behind the length
+      auto prepare = [&]() {
+        ok = ok && wait(&bars->full[own.slot], own.phase);
+        if (ok && n == 0) ok = wait(&bars->fix_full[x], (items - 1) & 1);
         if (ok && a.lengths) {
-          const int live = nx.len - key_block(nx.it, nx.n) * kBlock;
-          if (live < kBlock) zero_rows<D>(smem + L::kRing + at.slot * L::kTile, live);
+          const int live = len - key_block(it, n) * kBlock;
+          if (live < kBlock) zero_rows<D>(smem + L::kRing + own.slot * L::kTile, live);
         }
       };
-      auto issue = [&](int x, uint32_t d, uint32_t bd, uint32_t s, uint32_t t) {   // the elected lane
-        mma_tiles<D>(d, fix_d + x * kStep, bd);
-        mma_commit(x ? &bars->dp_full : &bars->s_full[t & 1]);
-        if (x) mma_commit(&bars->empty[s]);
-        if (nx.n + 1 == nx.blocks) mma_commit(&bars->fix_empty[x]);
+      auto advance = [&]() {
+        own.next(), own.next();
+        ++n;
       };
-      RingPos<SL> at;
-      uint32_t t = 0, sk = 0;   // slot of K of block t
       open();
-      const int32_t* it = nx.it;
-      bool first = true, more = it != nullptr;
-      if (more) {
-        for (int x = 0; x < 2; ++x) {
-          ready(x, at);
-          const uint32_t s = at.slot, bd = uniform(row_d + s * kStep);
-          at.next();
-          if (ok && elect_one()) issue(x, tm + (x ? kTP : 0), bd, s, 0);
-          __syncwarp();
-        }
-        ++nx.n;
-      }
-      while (more && ok) {
-        // block t: the next S, then dQ += dS K and the next dP
-        const bool end = nx.n == nx.blocks;
-        if (end) open();
-        more = nx.it != nullptr;
-        const uint32_t kd = uniform(col_d + sk * kStep), add = uniform(first ? 0u : 1u);
-        const uint32_t nk = at.slot, nkd = uniform(row_d + nk * kStep), td = uniform(tm + 128 * ((t + 1) & 1));
-        if (more) {
-          ready(0, at), at.next();
-          if (t >= 1) ok = ok && wait(&bars->s_read[(t + 1) & 1], (((t + 1) >> 1) - 1) & 1);
+      if (x == 0) {
+        for (uint32_t t = 0; it != nullptr && ok; ++t) {   // S of block t
+          prepare();
+          const uint32_t d = uniform(row_d + own.slot * kStep), td = uniform(tm + 128 * (t & 1));
+          if (t >= 2) ok = ok && wait(&bars->s_read[t & 1], ((t >> 1) - 1) & 1);
           if (!ok) break;
           fence_after();
-          if (elect_one()) issue(0, td, nkd, nk, t + 1);
+          const bool end = n + 1 == blocks;
+          if (elect_one()) {
+            mma_tiles<D>(td, fix_d, d);
+            mma_commit(&bars->s_full[t & 1]);
+            mma_commit(&bars->empty[own.slot]);
+            if (end) mma_commit(&bars->fix_empty[0]);
+          }
           __syncwarp();
+          advance();
+          if (end) {
+            const int32_t* was = it;
+            open();
+            ring.give_back(was);
+          }
         }
-        const uint32_t nv = at.slot, nvd = uniform(row_d + nv * kStep);
-        if (more) ready(1, at), at.next();
-        ok = ok && wait(&bars->ds_full, t & 1);
-        if (!ok) break;
-        fence_after();
-        if (elect_one()) {
-          mma_packed<D>(tm + kTQ, tm + kTP, kd, add);
-          mma_commit(&bars->empty[sk]);
-          if (end) mma_commit(&bars->acc_full);
-          if (more) issue(1, tm + kTP, nvd, nv, t + 1);
+      } else {
+        auto issue = [&](uint32_t d) {   // dP (the elected lane; V is this warp's alone)
+          mma_tiles<D>(tm + kTP, fix_d, d);
+          mma_commit(&bars->dp_full);
+          mma_commit(&bars->empty[own.slot]);
+          mma_commit(&bars->empty[own.slot]);
+          if (n + 1 == blocks) mma_commit(&bars->fix_empty[1]);
+        };
+        if (it != nullptr) {
+          prepare();
+          const uint32_t d = uniform(row_d + own.slot * kStep);
+          fence_after();
+          if (ok && elect_one()) issue(d);
+          __syncwarp();
+          advance();
         }
-        __syncwarp();
-        first = end;
-        if (end) {
-          ring.give_back(it);
-          it = nx.it;
+        uint32_t add = 0;
+        for (uint32_t t = 0; it != nullptr && ok; ++t) {   // dQ of block t and the next dP
+          const bool end = n == blocks;
+          if (end) {
+            const int32_t* was = it;
+            open();
+            ring.give_back(was);
+          }
+          const bool more = it != nullptr;
+          if (more) prepare();
+          const uint32_t d = uniform(row_d + own.slot * kStep), kd = uniform(col_d + other.slot * kStep);
+          const uint32_t acc = uniform(add);
+          ok = ok && wait(&bars->ds_full, t & 1);
+          if (!ok) break;
+          fence_after();
+          if (elect_one()) {
+            mma_packed<D>(tm + kTQ, tm + kTP, kd, acc);
+            mma_commit(&bars->empty[other.slot]);
+            if (end) mma_commit(&bars->acc_full);
+            if (more) issue(d);
+          }
+          __syncwarp();
+          add = end ? 0 : 1;
+          other.next(), other.next();
+          if (more) advance();
         }
-        if (more) ++nx.n;
-        sk = nk;
-        ++t;
       }
       if (elect_one()) {
         mma_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, a.err);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp + 1 && lane == 0) {
+    } else if (lane == 0) {
       // ---------------------------------------------------------------- items
       const int64_t bh = (int64_t)a.B * a.H, items = bh * tiles;
       int64_t x = blockIdx.x;

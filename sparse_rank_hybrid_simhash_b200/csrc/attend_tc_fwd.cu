@@ -23,11 +23,11 @@
 // partial rows in the workspace, which attend_combine_kernel adds up in order.
 //
 // Roles (384 threads, one CTA per SM): warps 0..3 and 4..7 softmax and output of
-// the two streams, warp 8 TMA, warp 9 MMA issue and TMEM, warp 10 hands out the
-// items through a ring in shared memory (registers move between whole warpgroups:
+// the two streams, warp 8 TMA, warps 9 and 10 the streams' products, warp 11 hands
+// out the items through a ring in shared memory (registers move between whole warpgroups:
 // a softmax thread holds its row of S).  K and V blocks pass
 // through one ring of slots (K0 V0 K1 V1 ...).  Keys behind a length may hold
-// anything: their scores are replaced, and the MMA warp zeroes their value rows
+// anything: their scores are replaced, and the MMA warps zero their value rows
 // in shared memory (0 times a stray infinity is not 0).
 //
 // Bound: at d = 128 a block costs 1024 cycles of products and 1024 of
@@ -49,7 +49,7 @@ using namespace tc;
 constexpr int kThreads = 384;
 // registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kItemWarp = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTO = 256;            // O of stream s at kTO + 128 s; S (and P) at 128 s
 constexpr float kGrow = 8.0f;            // log2 of the growth that rescales O
@@ -335,10 +335,10 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   if (tid == 0) {
     for (int i = 0; i < SL; ++i) {
       mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 1);
+      mbar_init(&bars->empty[i], 2);       // both MMA warps
     }
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], 4);   // a stream's warps
@@ -348,9 +348,9 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     mbar_init(&bars->x_done, 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 10);   // eight softmax warps, TMA, MMA
+      mbar_init(&bars->item_empty[i], 11);   // eight softmax warps, TMA, two MMA
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     fence_mbar_init();
   }
   if (PAGED && warp == 0) {   // this CTA's run of units
@@ -665,14 +665,16 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       }
       __syncwarp();
 
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kItemWarp) {
       // ------------------------------------------------------------------ products
+      // a warp a stream: one's waits and bookkeeping run under the other's products
       constexpr uint32_t id_pv = idesc_bf16(128, D, false, true);
       constexpr uint32_t kStep = L::kTile >> 4;   // a slot further, in descriptor units
-      const uint32_t tm = uniform(tmem);
+      const int st = warp - kMmaWarp;
+      const uint32_t tS = uniform(tmem + 128 * st), tO = uniform(tmem + kTO + 128 * st);
       const uint32_t q_d = row_desc(sbase + L::kQ);
       const uint32_t k_d = row_desc(sbase + L::kRing), v_d = col_desc(sbase + L::kRing);
-      uint32_t nq = 0, np[2] = {0, 0};
+      uint32_t nq = 0, np = 0;
       RingPos<SL> at;   // the ring slot of the next load: K of a block, then V
       auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, a.err); };
       while (const Item* item = take()) {
@@ -682,14 +684,13 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           give_back();
           continue;
         }
-        const int last[2] = {it.last_use(0), it.last_use(1)};
-        const uint32_t q_of[2] = {uniform(q_d), uniform(q_d + (it.split ? 0 : kStep))};
-        bool pend[2] = {false, false};
-        uint32_t add[2] = {0, 0};
-        uint32_t sv = 0;                   // slot of V of block n - 1
+        const int last = it.last_use(st);
+        const uint32_t qd = uniform(q_d + (it.split || st == 0 ? 0 : kStep));
+        bool pend = false;
+        uint32_t add = 0, sv = 0;          // slot of V of block n - 1
         for (int n = n0; n <= n1 && ok; ++n) {
           // what block n needs is awaited before the softmax of block n - 1
-          const bool more = n < n1;
+          const bool more = n < n1, use = more && it.uses(st, n);
           const uint32_t sk = at.slot;
           if (more) {
             ok = wait(&bars->full[sk], at.phase);
@@ -697,46 +698,38 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             at.next();
           }
           const uint32_t kd = uniform(k_d + sk * kStep), vd = uniform(v_d + sv * kStep);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const bool use = more && it.uses(s, n);
-            if (pend[s]) {
-              ok = ok && wait(&bars->p_full[s], np[s] & 1);
-              ++np[s];
-            }
-            if (!ok) break;
-            fence_after();
-            if (elect_one()) {
-              if (pend[s]) {               // O_s (+)= P_s V of block n - 1
-#pragma unroll
-                for (int x = 0; x < kBlock; x += 16)
-                  mma_ts(tm + kTO + 128 * s, tm + 128 * s + (x >> 1), vd + x * 8, id_pv,
-                         x > 0 ? 1u : add[s]);
-                if (n - 1 == last[s]) mma_commit(&bars->o_full[s]);
-              }
-              if (use) {                   // S_s = Q_s K^T of block n
-                mma_tiles<D>(tm + 128 * s, q_of[s], kd);
-                mma_commit(&bars->s_full[s]);
-              }
-            }
-            __syncwarp();
-            if (pend[s]) add[s] = 1;
-            pend[s] = use;
+          const uint32_t acc = uniform(add);
+          if (pend) {
+            ok = ok && wait(&bars->p_full[st], np & 1);
+            ++np;
           }
           if (!ok) break;
+          fence_after();
           if (elect_one()) {
-            if (more) mma_commit(&bars->empty[sk]);
+            if (pend) {                    // O (+)= P V of block n - 1
+#pragma unroll
+              for (int x = 0; x < kBlock; x += 16)
+                mma_ts(tO, tS + (x >> 1), vd + x * 8, id_pv, x > 0 ? 1u : acc);
+              if (n - 1 == last) mma_commit(&bars->o_full[st]);
+            }
             if (n > n0) mma_commit(&bars->empty[sv]);
+            if (use) {                     // S = Q K^T of block n
+              mma_tiles<D>(tS, qd, kd);
+              mma_commit(&bars->s_full[st]);
+            }
+            if (more) mma_commit(&bars->empty[sk]);
             if (n + 1 == n1) mma_commit(&bars->q_empty);
           }
           __syncwarp();
+          if (pend) add = 1;
+          pend = use;
           if (more) {                      // V of block n
             sv = at.slot;
             ok = wait(&bars->full[sv], at.phase);
             at.next();
             const int live = len - it.block(n) * kBlock;
-            if (ok && live < kBlock && (PAGED || a.lengths != nullptr)) {
-              // value rows behind the length: zeros
+            if (ok && use && live < kBlock && (PAGED || a.lengths != nullptr)) {
+              // value rows behind the length: zeros (both warps may write them)
               uint8_t* v = smem + L::kRing + sv * L::kTile;
               for (int r = live * 8 + lane; r < kBlock * 8; r += 32)
 #pragma unroll
@@ -756,7 +749,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       }
       __syncwarp();
 
-    } else if (warp == kMmaWarp + 1) {
+    } else {
       // ------------------------------------------------------------------ items
       if (lane == 0) {
         Walk<PAGED> walk(a, sh, items, bars->cut);
