@@ -409,20 +409,25 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m = -INFINITY, l = 0.f;
       bool any = false;
-      for (int n = it.n0; n < it.n1; ++n) {
-        if (!it.uses(st, n)) continue;
+      const int n1 = it.n1, sink_blocks = it.sink_blocks, shift = it.first - sink_blocks;
+      const int p_first = pick(it.p_first, st), edge = pick(it.p_last, st) - a.window;
+      const int k_first = pick(it.k_first, st), k_last = pick(it.k_last, st), sink_top = it.sink_top;
+      const bool split = it.split;
+      for (int n = it.n0; n < n1; ++n) {
+        const int kb = n < sink_blocks ? n : n + shift;
+        if (split ? (n & 1) != st : kb > k_last || (kb < k_first && kb >= sink_top)) continue;
         ok = warp_wait(&bars->s_full[st], ns & 1, a.err);
         if (!ok) break;
         ++ns;
         fence_after();
         if (warp_live) {
-          const int j0 = it.block(n) * kBlock;
+          const int j0 = kb * kBlock;
           float sv[128];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sv + 32 * c);
           tmem_ld_wait();
-          if (j0 + kBlock - 1 > pick(it.p_first, st) ||
-              (int64_t)j0 <= (int64_t)pick(it.p_last, st) - a.window) {
+          // some row of the tile does not see all of the block
+          if (j0 + kBlock - 1 > p_first || j0 <= edge) {
             const int hi = pos - j0, lo = pos - a.window + 1 - j0;
             const int sk = (int)min((int64_t)a.sinks - j0, (int64_t)kBlock);
 #pragma unroll
