@@ -336,8 +336,10 @@ int32_t elsaa_path_flags(const elsaa_params* p);
  *     dense [B, heads, N, d].  d is contiguous.  Every stride times the element
  *     size is a multiple of 16 bytes and positive where the dimension is
  *     larger than one (a broadcast input is materialised by the caller).
- *   - The workspace's error word is only ever set by these calls: the caller
- *     zeroes its first 256 bytes once, and elsaa_check() reads and clears it.
+ *   - The caller zeroes the first 8192 bytes of a workspace once.  They hold
+ *     the error word, which these calls only ever set and elsaa_check() reads
+ *     and clears, and counters that every call leaves at zero (zero them anew
+ *     after ELSAA_ERR_DEVICE_TIMEOUT).
  *   - Two calls that may run at the same time (two streams, two captured
  *     graphs) need a workspace each. */
 

@@ -17,7 +17,9 @@
 // window_dkv_kernel's work is one list of (key tile, query head, query block) units
 // cut into equal runs, one per CTA: a tile of sinks is seen by every query behind
 // it, an order of magnitude more than the others.  A tile cut between CTAs leaves
-// fp32 partials that dkv_combine_kernel adds up in the CTAs' order.
+// fp32 partials, and the last CTA to get there adds them up, in the CTAs' order
+// whichever it is (a counter a warp: a row's partials come from the same warp of
+// every CTA).
 //
 // Elementwise work of a block: 256 threads, each one lane and 64 of the 128
 // columns.  The products of one block run under the elementwise work of the
@@ -44,7 +46,7 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9, kItemWarp = 11;
 // registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
 constexpr int kWorkRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kItems = 4;
+constexpr int kItems = 3;
 constexpr int kMinUnits = 2;
 
 template <int D>
@@ -78,6 +80,7 @@ struct Bars {
   uint64_t drain;
   uint32_t tmem;
   int32_t cut[5];
+  int64_t per;
   int32_t items[kItems][12];
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
@@ -93,7 +96,7 @@ ELSAA_DEV int length_of(const AttendArgs& a, int b) {
   return a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
 }
 
-// ---- row statistics ------------------------------------------------------------
+// ---- row statistics (and the zeros of empty tiles) ------------------------------------------------------------
 
 template <int D>
 __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const Stats st) {
@@ -123,6 +126,19 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
   if (in && c == 0) {
     st.nl[x] = nl;
     st.nd[x] = -s;
+  }
+  if (in && n < a.N && n / kBlock * kBlock >= length_of(a, b)) {
+    // a tile behind the length is no item of the kernels below: its zeros
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dq) + b * a.sdq.b + h * a.sdq.h +
+                              n * a.sdq.n + c) = z;
+    if (h % a.g == 0) {
+      const int hk = h / a.g;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk) + b * a.sdk.b + hk * a.sdk.h +
+                                n * a.sdk.n + c) = z;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv) + b * a.sdv.b + hk * a.sdv.h +
+                                n * a.sdv.n + c) = z;
+    }
   }
 }
 
@@ -222,7 +238,7 @@ ELSAA_DEV void init_bars(Bars* b, int acc) {
 // ---- dk, dv ----------------------------------------------------------------------
 
 // Fields of a key tile's item; [0] < 0: no more items.
-enum { kB, kHk, kLen, kKt, kNb, kNq, kN0, kN1, kOrder };
+enum { kB, kHk, kLen, kKt, kNb, kNq, kN0, kN1, kOrder, kCta0, kCta1, kSlot0 };
 
 // Query blocks (of one head) that see key tile kt.
 ELSAA_DEV int query_blocks(const AttendArgs& a, int len, int kt) {
@@ -301,6 +317,49 @@ ELSAA_DEV float* partial(const AttendArgs& a, int d, int slot, int which, int ro
   return reinterpret_cast<float*>(a.scratch) + (((int64_t)slot * 2 + which) * kBlock + row) * d;
 }
 
+// 32 rows of a cut tile's dV (which = 0) or dK (1) from the partials of all its CTAs,
+// in their order; lanes over the columns, eight rows at a time.
+template <int D>
+ELSAA_DEV void merge_rows(const AttendArgs& a, const int32_t* it, int which, int warp_row) {
+  constexpr int V = D / 32, R = 8;   // values of a lane, rows at a time
+  const int lane = threadIdx.x & 31, cta0 = it[kCta0], cta1 = it[kCta1], slot0 = it[kSlot0];
+  const int j0 = it[kKt] * kBlock, len = it[kLen];
+  const float f = which ? a.scale : 1.f;
+  const Strides so = which ? a.sdk : a.sdv;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(which ? a.dk : a.dv) + it[kB] * so.b +
+                       it[kHk] * so.h + lane * V;
+  for (int x0 = warp_row; x0 < warp_row + 32; x0 += R) {
+    float o[R][V];
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[x][e] = 0.f;
+#pragma unroll 2
+    for (int i = cta0; i <= cta1; ++i) {
+      const float* p = partial(a, D, i * 2 + (i == cta0 ? slot0 : 0), which, x0) + lane * V;
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        if (V == 4) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(p + x * D));
+          o[x][0] += u.x, o[x][1] += u.y, o[x][2 % V] += u.z, o[x][3 % V] += u.w;
+        } else {
+          const float2 u = __ldcg(reinterpret_cast<const float2*>(p + x * D));
+          o[x][0] += u.x, o[x][1] += u.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const int j = j0 + x0 + x;
+      if (j >= a.N) break;
+#pragma unroll
+      for (int e = 0; e < V; e += 2)   // rows behind the length: zeros
+        *reinterpret_cast<__nv_bfloat162*>(out + (int64_t)j * so.n + e) =
+            __floats2bfloat162_rn(j < len ? o[x][e] * f : 0.f, j < len ? o[x][(e + 1) % V] * f : 0.f);
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const Stats stats) {
@@ -327,6 +386,7 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     if (lane == 0) {
       bars->cut[0] = c.b, bars->cut[1] = c.hk, bars->cut[2] = c.kt, bars->cut[3] = c.off;
       bars->cut[4] = units;
+      bars->per = per;
     }
   }
   __syncthreads();
@@ -444,6 +504,20 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           for (int q = 0; q < 8; ++q)
             *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
                 make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      }
+      if (!whole) {
+        // the last of the tile's CTAs to come here with this warp's rows adds them up
+        uint32_t* counter = a.counters + it[kCta0] * 8 + warp;
+        uint32_t before = 0;
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) before = atomicAdd(counter, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == (uint32_t)(it[kCta1] - it[kCta0])) {
+          __threadfence();
+          merge_rows<D>(a, it, half, 32 * (warp & 3));
+          if (lane == 0) *counter = 0;
         }
       }
       fence_before();
@@ -574,9 +648,8 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         const int rows = live;
         const bool end = left == 0;
         if (end) {
-          const int32_t* was = it;
+          ring.give_back(it);   // (before the next is asked for: its place may be needed)
           open();
-          ring.give_back(was);
         }
         const bool more = it != nullptr;
         if (more) prepare();
@@ -606,6 +679,8 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       // ---------------------------------------------------------------- items
       int b = bars->cut[0], hk = bars->cut[1], kt = bars->cut[2], off = bars->cut[3], left = bars->cut[4];
       int order = 0;
+      const int64_t per = bars->per;
+      int64_t at = per * blockIdx.x;   // the next unit
       for (uint32_t n = 0;; ++n) {
         if (n >= kItems && !mbar_wait(&bars->item_empty[n % kItems], (n / kItems - 1) & 1, a.err)) break;
         int32_t* it = bars->items[n % kItems];
@@ -625,6 +700,13 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           it[kN0] = off;
           it[kN1] = min(nb, off + left);
           it[kOrder] = order++;
+          if (it[kN1] - off < nb) {   // cut: its CTAs, and its slot in the first one's run
+            const int64_t begin = at - off;
+            it[kCta0] = (int)(begin / per);
+            it[kCta1] = (int)((begin + nb - 1) / per);
+            it[kSlot0] = begin == it[kCta0] * per ? 0 : 1;
+          }
+          at += it[kN1] - off;
           left -= it[kN1] - off;
           off = 0;
           ++kt;
@@ -642,57 +724,6 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   if (warp == kMmaWarp) {
     fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// Key tiles cut between CTAs: their partials added up in the CTAs' order.  Block
-// x = 1 .. CTAs - 1 takes the tile that CTA x begins inside of, if x is its second
-// CTA.
-template <int D>
-__global__ void __launch_bounds__(256) dkv_combine_kernel(const AttendArgs a, int ctas) {
-  __shared__ int64_t found[2];
-  __shared__ Cut cut;
-  const int c = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    const int64_t total = all_units(a), per = run_length(total, ctas), w0 = per * c;
-    Cut f{0, 0, 0, 0};
-    if (w0 < total) f = find_unit(a, w0);
-    if (threadIdx.x == 0) {
-      cut = f;
-      found[0] = per;
-      found[1] = w0;
-    }
-  }
-  __syncthreads();
-  if (cut.off == 0) return;
-  const int64_t per = found[0], begin = found[1] - cut.off;
-  const int first = (int)(begin / per);
-  if (first != c - 1) return;
-  const int len = length_of(a, cut.b);
-  const int nb = query_blocks(a, len, cut.kt) * a.g;
-  const int last = (int)((begin + nb - 1) / per);
-  const int first_slot = begin == first * per ? 0 : 1;   // the tile is that run's first item, or its last
-  for (int x = blockIdx.y * 256 + threadIdx.x; x < 2 * kBlock * (D / 4); x += 256 * gridDim.y) {
-    const int which = x / (kBlock * (D / 4)), row = x / (D / 4) % kBlock, col = x % (D / 4) * 4;
-    const int j = cut.kt * kBlock + row;
-    if (j >= a.N) continue;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < len) {
-#pragma unroll 4
-      for (int i = first; i <= last; ++i) {
-        const float4 p = *reinterpret_cast<const float4*>(
-            partial(a, D, i * 2 + (i == first ? first_slot : 0), which, row) + col);
-        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-      }
-    }
-    const float f = which ? a.scale : 1.f;
-    const Strides so = which ? a.sdk : a.sdv;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(which ? a.dk : a.dv) + cut.b * so.b + cut.hk * so.h +
-                       (int64_t)j * so.n + col;
-    const __nv_bfloat162 u = __floats2bfloat162_rn(s.x * f, s.y * f);
-    const __nv_bfloat162 w = __floats2bfloat162_rn(s.z * f, s.w * f);
-    *reinterpret_cast<uint2*>(o) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
   }
 }
 
@@ -796,32 +827,20 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         warp_arrive(&bars->ds_full);
       }
       if (!ok) break;
-      if (blocks > 0) {
-        ok = wait(&bars->acc_full, ni & 1);
-        if (!ok) break;
-        ++ni;
-        fence_after();
-      }
+      ok = wait(&bars->acc_full, ni & 1);
+      if (!ok) break;
+      ++ni;
+      fence_after();
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.dq) + it[qB] * a.sdq.b + it[qH] * a.sdq.h +
                             (int64_t)r * a.sdq.n + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         float v[32];
-        if (blocks > 0) {
-          tmem_ld32(tmem + kTQ + half * (D / 2) + 32 * c + lane_off, v);
-          tmem_ld_wait();
-        }
+        tmem_ld32(tmem + kTQ + half * (D / 2) + 32 * c + lane_off, v);
+        tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = blocks > 0 && r < len ? v[e] * a.scale : 0.f;
+        for (int e = 0; e < 32; ++e) v[e] = r < len ? v[e] * a.scale : 0.f;
         if (r < a.N) store32(orow + 32 * c, v);
-        // a tile behind the length has no key tile either: its zeros
-        if (blocks == 0 && it[qH] % a.g == 0 && r < a.N) {
-          const int hk = it[qH] / a.g;
-          store32(static_cast<__nv_bfloat16*>(a.dk) + it[qB] * a.sdk.b + hk * a.sdk.h +
-                      (int64_t)r * a.sdk.n + half * (D / 2) + 32 * c, v);
-          store32(static_cast<__nv_bfloat16*>(a.dv) + it[qB] * a.sdv.b + hk * a.sdv.h +
-                      (int64_t)r * a.sdv.n + half * (D / 2) + 32 * c, v);
-        }
       }
       fence_before();
       ring.give_back(it);
@@ -856,15 +875,13 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
       };
       while (const int32_t* it = ring.take(ok)) {
         const int blocks = it[qN];
-        if (blocks > 0) {
-          load_fix(it, 0);
-          load_block(it, 0, 0);
-          load_fix(it, 1);
-          load_block(it, 0, 1);
-          for (int n = 1; n < blocks && ok; ++n) {
-            load_block(it, n, 0);
-            load_block(it, n, 1);
-          }
+        load_fix(it, 0);
+        load_block(it, 0, 0);
+        load_fix(it, 1);
+        load_block(it, 0, 1);
+        for (int n = 1; n < blocks && ok; ++n) {
+          load_block(it, n, 0);
+          load_block(it, n, 1);
         }
         ring.give_back(it);
       }
@@ -886,12 +903,8 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
       const int32_t* it = nullptr;
       int n = 0, blocks = 0, len = 0;
       uint32_t items = 0;
-      auto open = [&]() {   // the first block of the next item that has any
+      auto open = [&]() {   // the next item's first block
         it = ring.take(ok);
-        while (it != nullptr && it[qN] == 0) {
-          ring.give_back(it);
-          it = ring.take(ok);
-        }
         if (it == nullptr) return;
         n = 0;
         blocks = it[qN];
@@ -931,9 +944,8 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
           __syncwarp();
           advance();
           if (end) {
-            const int32_t* was = it;
+            ring.give_back(it);   // (before the next is asked for: its place may be needed)
             open();
-            ring.give_back(was);
           }
         }
       } else {
@@ -956,9 +968,8 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         for (uint32_t t = 0; it != nullptr && ok; ++t) {   // dQ of block t and the next dP
           const bool end = n == blocks;
           if (end) {
-            const int32_t* was = it;
+            ring.give_back(it);   // (before the next is asked for: its place may be needed)
             open();
-            ring.give_back(was);
           }
           const bool more = it != nullptr;
           if (more) prepare();
@@ -988,19 +999,23 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
       // ---------------------------------------------------------------- items
       const int64_t bh = (int64_t)a.B * a.H, items = bh * tiles;
       int64_t x = blockIdx.x;
-      for (uint32_t n = 0;; ++n, x += gridDim.x) {
+      // Every item has blocks: a product warp asks for the next one before it ends the
+      // last, and must not wait there for items in between to pass.
+      for (uint32_t n = 0;; ++n) {
         if (n >= kItems && !mbar_wait(&bars->item_empty[n % kItems], (n / kItems - 1) & 1, a.err)) break;
         int32_t* it = bars->items[n % kItems];
-        const bool more = x < items;
-        if (more) {   // the longest (last) tiles first, heads and batches inside
+        it[qB] = -1;
+        for (; x < items && it[qB] < 0; x += gridDim.x) {
+          // the longest (last) tiles first, heads and batches inside
           const int t = tiles - 1 - (int)(x / bh), b = (int)(x % bh / a.H), h = (int)(x % a.H);
           const int len = length_of(a, b);
           const KeyBlocks k = key_blocks(t * kBlock, min(len, (t + 1) * kBlock) - 1, a.window, a.sinks, kBlock);
-          it[qB] = b, it[qH] = h, it[qLen] = len, it[qT] = t;
+          if (k.count() == 0) continue;
+          it[qH] = h, it[qLen] = len, it[qT] = t;
           it[qSink] = k.sink_blocks, it[qFirst] = k.first, it[qN] = k.count();
-        } else {
-          it[qB] = -1;
+          it[qB] = b;
         }
+        const bool more = it[qB] >= 0;
         mbar_arrive(&bars->item_full[n % kItems]);
         if (!more) break;
       }
@@ -1051,10 +1066,6 @@ cudaError_t backward(const AttendArgs& args, cudaStream_t s) {
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   window_dkv_kernel<D><<<ctas, kThreads, smem, s>>>(maps, a, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (ctas > 1) {
-    dkv_combine_kernel<D><<<dim3(ctas - 1, 8), 256, 0, s>>>(a, ctas);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   const int64_t items = (int64_t)a.B * a.H * tiles;
   window_dq_kernel<D><<<(int)(items < sms ? items : sms), kThreads, smem, s>>>(maps, a, st, tiles);
   return cudaGetLastError();

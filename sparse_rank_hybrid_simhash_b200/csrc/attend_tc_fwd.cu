@@ -20,7 +20,9 @@
 // Paged work is one list of (tile pair, key head, key block) units cut into equal
 // runs, one per CTA (the cuts are found from the lengths on the device, so a
 // captured launch follows them); an item cut between CTAs leaves unnormalised
-// partial rows in the workspace, which attend_combine_kernel adds up in order.
+// partial rows in the workspace, and the last CTA to get there adds them up, in the
+// CTAs' order whichever it is (a counter a warp: a row's partials come from the same
+// warp of every CTA).  A second kernel for that cost 12 us a call.
 //
 // Roles (384 threads, one CTA per SM): warps 0..3 and 4..7 softmax and output of
 // the two streams, warp 8 TMA, warps 9 and 10 the streams' products, warp 11 hands
@@ -91,6 +93,7 @@ struct Item {
   int sink_blocks, first, nblk, n0, n1;
   int k_first[2], k_last[2], sink_top;
   int order;                // the CTA's items before it; -1: there are no more
+  int cta0, cta1, slot0;    // a cut item: its CTAs, and whether it is not the first of cta0's
   ELSAA_DEV int block(int n) const { return n < sink_blocks ? n : first + n - sink_blocks; }
   ELSAA_DEV bool uses(int s, int n) const {
     if (split) return (n & 1) == s;
@@ -134,7 +137,8 @@ struct Bars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
   uint32_t tmem;
-  int32_t cut[6];               // a paged CTA's first item (Cut)
+  int32_t cut[5];               // a paged CTA's first item (Cut)
+  int64_t per;                  // units of a run
   Item items[kItems];
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
@@ -199,7 +203,6 @@ ELSAA_DEV Item paged_item(const AttendArgs& a, const Shape& sh, int b, int pair,
 struct Cut {
   int b, pair, hk, off;   // where a run begins: its item and block
   int units;              // its length
-  int fresh;              // it begins an item
 };
 
 // Units (tile pair, key head, block) of sequence b.
@@ -217,21 +220,21 @@ ELSAA_DEV int64_t run_length(int64_t total, int ctas) {
   return per > kMinUnits ? per : kMinUnits;
 }
 
-ELSAA_DEV int64_t all_units(const AttendArgs& a, const Shape& sh, bool lead) {
+// The run of CTA `cta` of `ctas`, by one warp; units 0: nothing is left for it.
+// *per: units of a run.
+ELSAA_DEV Cut find_run(const AttendArgs& a, const Shape& sh, int cta, int ctas, int64_t* per) {
   const int lane = threadIdx.x & 31;
-  int64_t u = 0;
-  for (int b = lane; b < a.seqs; b += 32) u += seq_units(a, sh, b, lead);
+  Cut c{0, 0, 0, 0, 0};
+  int64_t total = 0, mine = 0;
+  for (int b = lane; b < a.seqs; b += 32) total += mine = seq_units(a, sh, b, cta == 0);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-  return u;
-}
-
-// The item and block of unit w (0 <= w < total), by one warp.
-ELSAA_DEV Cut find_unit(const AttendArgs& a, const Shape& sh, int64_t w) {
-  const int lane = threadIdx.x & 31;
-  Cut c{0, 0, 0, 0, 0, 0};
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  *per = run_length(total, ctas);
+  int64_t w = *per * cta;
+  if (w >= total) return c;
+  c.units = (int)(*per < total - w ? *per : total - w);
   for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-    const int64_t mine = b0 + lane < a.seqs ? seq_units(a, sh, b0 + lane, false) : 0;
+    if (a.seqs > 32) mine = b0 + lane < a.seqs ? seq_units(a, sh, b0 + lane, false) : 0;
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -255,7 +258,6 @@ ELSAA_DEV Cut find_unit(const AttendArgs& a, const Shape& sh, int64_t w) {
         }
         rest -= blk * a.Hkv;
       }
-      c.fresh = c.off == 0;
       return c;
     }
     w -= __shfl_sync(0xffffffffu, upto, 31);
@@ -271,9 +273,11 @@ struct Walk {
   int64_t x, items;                          // window
   int b, pair, hk, off, left, start, tokens, len;   // pages
   int order;                                 // items so far
-  ELSAA_DEV Walk(const AttendArgs& a_, const Shape& sh_, int64_t items_, const int32_t* cut)
-      : a(a_), sh(sh_), x(blockIdx.x), items(items_), order(0) {
+  int64_t per, at;                           // pages: units of a run, and the next unit
+  ELSAA_DEV Walk(const AttendArgs& a_, const Shape& sh_, int64_t items_, const int32_t* cut, int64_t per_)
+      : a(a_), sh(sh_), x(blockIdx.x), items(items_), order(0), per(per_) {
     if (PAGED) {
+      at = per * blockIdx.x;
       b = cut[0], pair = cut[1], hk = cut[2], off = cut[3], left = cut[4];
       start = tokens = len = 0;
       if (left > 0) tokens = new_tokens(a, b, &start, &len, false);
@@ -296,7 +300,15 @@ struct Walk {
     it = paged_item(a, sh, b, pair, hk, start, tokens, len);
     it.n0 = off;
     it.n1 = min(it.nblk, off + left);
+    it.cta0 = it.cta1 = it.slot0 = 0;
+    if (it.n1 - it.n0 < it.nblk) {
+      const int64_t begin = at - off;
+      it.cta0 = (int)(begin / per);
+      it.cta1 = (int)((begin + it.nblk - 1) / per);
+      it.slot0 = begin == it.cta0 * per ? 0 : 1;
+    }
     left -= it.n1 - it.n0;
+    at += it.n1 - it.n0;
     off = 0;
     if (++hk == a.Hkv) hk = 0, ++pair;
     it.order = order++;
@@ -316,6 +328,68 @@ ELSAA_DEV Partial partial_row(const AttendArgs& a, const Shape& sh, int d, int s
   const int64_t slots = (int64_t)kMaxCtas * 4, at = (int64_t)slot * sh.slot_rows + row;
   float* o = reinterpret_cast<float*>(a.scratch);
   return {o + at * d, reinterpret_cast<float2*>(o + slots * sh.slot_rows * d) + at};
+}
+
+// The rows of one warp of a cut item from the partials of all its CTAs, in their
+// order: m = max m_i, y = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.  Lanes over the
+// columns, four rows at a time.
+template <int D>
+ELSAA_DEV void merge_rows(const AttendArgs& a, const Shape& sh, const Item& it, int st, int warp_row) {
+  constexpr int V = D / 32;   // values of a lane
+  const int lane = threadIdx.x & 31, cta0 = it.cta0, cta1 = it.cta1, slot0 = it.slot0;
+  auto part = [&](int cta, int row) {
+    return partial_row(a, sh, D, (cta * 2 + (cta == cta0 ? slot0 : 0)) * 2 + st, row);
+  };
+  const int tt = sh.tt, g = a.g, tokens = it.tokens, r0 = pick(it.r0, st);
+  for (int x0 = warp_row; x0 < warp_row + 32; x0 += 4) {
+    if (x0 / g >= tt || r0 + x0 / g >= tokens) break;   // (rows end with the tokens)
+    int row[4];                                         // (a row past the end: the first again)
+    float m[4], l[4], o[4][V];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int tok = (x0 + x) / g;
+      row[x] = tok < tt && r0 + tok < tokens ? x0 + x : x0;
+      float top = -INFINITY;
+      for (int i = cta0 + lane; i <= cta1; i += 32) top = fmaxf(top, __ldcg(part(i, row[x]).ml).x);
+      m[x] = top;
+      l[x] = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[x][e] = 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m[x] = warp_max(m[x]);
+#pragma unroll 4
+    for (int i = cta0; i <= cta1; ++i) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const Partial p = part(i, row[x]);
+        const float2 ml = __ldcg(p.ml);
+        float v[V];
+        if (V == 4) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(p.o) + lane);
+          v[0] = u.x, v[1] = u.y, v[2 % V] = u.z, v[3 % V] = u.w;
+        } else {
+          const float2 u = __ldcg(reinterpret_cast<const float2*>(p.o) + lane);
+          v[0] = u.x, v[1] = u.y;
+        }
+        const float w = ml.x > -INFINITY ? ex2(ml.x - m[x]) : 0.f;   // (no blocks of the stream there)
+        l[x] += ml.y * w;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[x][e] += v[e] * w;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float inv = l[x] > 0.f ? 1.0f / l[x] : 0.f;
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
+                         (int64_t)(it.start + r0 + row[x] / g) * a.sy.n +
+                         (int64_t)(it.hk * g + row[x] % g) * a.sy.h + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<__nv_bfloat162*>(y + e) =
+            __floats2bfloat162_rn(o[x][e] * inv, o[x][(e + 1) % V] * inv);
+    }
+  }
 }
 
 template <int D, bool PAGED>
@@ -354,16 +428,12 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     fence_mbar_init();
   }
   if (PAGED && warp == 0) {   // this CTA's run of units
-    const int64_t total = all_units(a, sh, blockIdx.x == 0);
-    const int64_t per = run_length(total, gridDim.x), w0 = per * blockIdx.x;
-    Cut c{0, 0, 0, 0, 0, 0};
-    if (w0 < total) {
-      c = find_unit(a, sh, w0);
-      c.units = (int)(per < total - w0 ? per : total - w0);
-    }
+    int64_t per;
+    const Cut c = find_run(a, sh, blockIdx.x, gridDim.x, &per);
     if (lane == 0) {
       bars->cut[0] = c.b, bars->cut[1] = c.pair, bars->cut[2] = c.hk;
-      bars->cut[3] = c.off, bars->cut[4] = c.units, bars->cut[5] = c.fresh;
+      bars->cut[3] = c.off, bars->cut[4] = c.units;
+      bars->per = per;
     }
   }
   __syncthreads();
@@ -549,6 +619,20 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
                   make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+        if (!whole) {
+          // the last of the item's CTAs to come here with this warp's rows adds them up
+          uint32_t* counter = a.counters + it.cta0 * 8 + warp;
+          uint32_t before = 0;
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) before = atomicAdd(counter, 1u);
+          before = __shfl_sync(0xffffffffu, before, 0);
+          if (before == (uint32_t)(it.cta1 - it.cta0)) {
+            __threadfence();
+            merge_rows<D>(a, sh, it, st, 32 * (warp & 3));
+            if (lane == 0) *counter = 0;
           }
         }
       }
@@ -757,7 +841,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     } else {
       // ------------------------------------------------------------------ items
       if (lane == 0) {
-        Walk<PAGED> walk(a, sh, items, bars->cut);
+        Walk<PAGED> walk(a, sh, items, bars->cut, bars->per);
         for (bool more = true; more; ++ni) {
           if (ni >= kItems &&
               !mbar_wait(&bars->item_empty[ni % kItems], (ni / kItems - 1) & 1, a.err))
@@ -777,67 +861,6 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   if (warp == kMmaWarp) {
     fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// Items cut between CTAs: their partial rows added up in the CTAs' order.  Block
-// x = 1 .. CTAs - 1 takes the item that CTA x begins inside of, if x is its second
-// CTA; a warp a row.
-template <int D>
-__global__ void __launch_bounds__(256)
-attend_combine_kernel(const AttendArgs a, const Shape sh, int ctas) {
-  __shared__ int64_t found[4];
-  __shared__ Cut cut;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x + 1;
-  if (warp == 0) {
-    const int64_t total = all_units(a, sh, false), per = run_length(total, ctas);
-    const int64_t w0 = per * c;
-    Cut f{0, 0, 0, 0, 0, 1};
-    if (w0 < total) f = find_unit(a, sh, w0);
-    if (lane == 0) {
-      cut = f;
-      found[0] = per;
-      found[1] = w0;
-    }
-  }
-  __syncthreads();
-  if (cut.fresh) return;
-  const int64_t per = found[0], begin = found[1] - cut.off;
-  const int first = (int)(begin / per);
-  if (first != c - 1) return;
-  int start, len;
-  const int n = new_tokens(a, cut.b, &start, &len, false);
-  const Item it = paged_item(a, sh, cut.b, cut.pair, cut.hk, start, n, len);
-  const int last = (int)((begin + it.nblk - 1) / per);
-  const int first_slot = begin == first * per ? 0 : 1;   // the item is that run's first, or its last
-  const int per_stream = sh.tt * a.g;
-  for (int x = blockIdx.y * 8 + warp; x < per_stream * (it.split ? 1 : 2); x += 8 * gridDim.y) {
-    const int st = x / per_stream, row = x % per_stream, r = it.r0[st] + row / a.g;
-    if (r >= n) continue;
-    auto part = [&](int cta) {
-      return partial_row(a, sh, D, (cta * 2 + (cta == first ? first_slot : 0)) * 2 + st, row);
-    };
-    float m = -INFINITY;
-    for (int i = first + lane; i <= last; i += 32) m = fmaxf(m, part(i).ml->x);
-    m = warp_max(m);
-    float l = 0.f, o[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int i = first; i <= last; ++i) {
-      const Partial p = part(i);
-      const float2 ml = *p.ml;
-      if (ml.x == -INFINITY) continue;   // (a stream without blocks in that run)
-      const float w = exp2f(ml.x - m);
-      l += ml.y * w;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] += p.o[lane + 32 * e] * w;
-    }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + (int64_t)(start + r) * a.sy.n +
-                       (int64_t)(cut.hk * a.g + row % a.g) * a.sy.h;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
   }
 }
 
@@ -902,9 +925,6 @@ cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int sms = sm_count(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
   attend_fwd_kernel<D, true><<<ctas, kThreads, Lay<D>::kDyn, s>>>(maps, a, sh, 0);
-  if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
-  const int rows = 2 * sh.slot_rows;
-  attend_combine_kernel<D><<<dim3(ctas - 1, rows < 64 ? (rows + 7) / 8 : 8), 256, 0, s>>>(a, sh, ctas);
   return cudaGetLastError();
 }
 

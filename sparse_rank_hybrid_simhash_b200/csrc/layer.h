@@ -18,6 +18,11 @@ struct Strides {
   int64_t b, h, n;
 };
 
+// Head of every workspace, zeroed once by the caller: the error word, and the
+// arrival counters of work cut between CTAs (which the calls leave at zero).
+constexpr size_t kHeadBytes = 8192;
+constexpr size_t kCounters = 256;   // byte offset of the counters
+
 // ---- norm and rotation -------------------------------------------------------
 
 // Most blocks that leave a partial sum of a weight's gradient (queries' and
@@ -68,6 +73,7 @@ struct AttendArgs {
   int sinks;
   float scale;
   uint32_t* err;
+  uint32_t* counters;         // [CTAs][8 warps]
   float* delta;               // [B, H, N]: rowsum(y dy) (backward)
   // pages
   const int32_t *page_table, *starts;

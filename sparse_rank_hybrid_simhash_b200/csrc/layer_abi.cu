@@ -11,8 +11,6 @@ using namespace elsaa;
 
 namespace {
 
-constexpr size_t kErrBytes = 256;
-
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 bool head_dim(int d, elsaa_status* why) {
@@ -106,7 +104,7 @@ elsaa_status elsaa_rotary_validate(const elsaa_rotary_params* p) { return check(
 
 size_t elsaa_rotary_workspace_bytes(const elsaa_rotary_params* p) {
   if (check(p) != ELSAA_OK) return 0;
-  return kErrBytes + (size_t)kRotaryPartials * p->d * sizeof(float);
+  return kHeadBytes + (size_t)kRotaryPartials * p->d * sizeof(float);
 }
 
 static elsaa_status rotary_args(const elsaa_rotary_params* p, const float* table, const float* wq,
@@ -120,7 +118,7 @@ static elsaa_status rotary_args(const elsaa_rotary_params* p, const float* table
   a->wq = p->norm ? wq : nullptr;
   a->wk = p->norm ? wk : nullptr;
   a->err = (uint32_t*)ws;
-  a->partials = (float*)((char*)ws + kErrBytes);
+  a->partials = (float*)((char*)ws + kHeadBytes);
   a->B = p->B;
   a->H = p->H;
   a->Hkv = p->Hkv;
@@ -201,8 +199,8 @@ elsaa_status elsaa_window_validate(const elsaa_window_params* p) { return check(
 
 size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backward) {
   if (check(p) != ELSAA_OK) return 0;
-  if (!backward) return kErrBytes;
-  return kErrBytes + window_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->B, p->H, p->N);
+  if (!backward) return kHeadBytes;
+  return kHeadBytes + window_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->B, p->H, p->N);
 }
 
 static elsaa_status window_args(const elsaa_window_params* p, const void* const* tensors,
@@ -235,7 +233,8 @@ static elsaa_status window_args(const elsaa_window_params* p, const void* const*
   a->sinks = p->sinks;
   a->scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->d);
   a->err = (uint32_t*)ws;
-  a->delta = (float*)((char*)ws + kErrBytes);
+  a->counters = (uint32_t*)((char*)ws + kCounters);
+  a->delta = (float*)((char*)ws + kHeadBytes);
   return ELSAA_OK;
 }
 
@@ -281,7 +280,7 @@ elsaa_status elsaa_paged_validate(const elsaa_paged_params* p) { return check(p)
 
 size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p) {
   if (check(p) != ELSAA_OK) return 0;
-  return kErrBytes + paged_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->rows, p->H / p->Hkv);
+  return kHeadBytes + paged_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->rows, p->H / p->Hkv);
 }
 
 static bool page_strides_of(const elsaa_paged_params* p, const int64_t* given, Strides* kp,
@@ -313,7 +312,7 @@ elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_p
     return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_pages, (const void*)v_pages})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
-  if (ws_bytes < kErrBytes) return ELSAA_ERR_WORKSPACE;
+  if (ws_bytes < kHeadBytes) return ELSAA_ERR_WORKSPACE;
   const int e = esize(p->dtype);
   auto take = [&](int i, int h, Strides* to) {
     return take_row_strides(strides ? strides + 2 * i : nullptr, p->rows, h, p->d, e, to);
@@ -374,7 +373,8 @@ elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
   a.sinks = p->sinks;
   a.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->d);
   a.err = (uint32_t*)ws;
-  a.scratch = (char*)ws + kErrBytes;
+  a.counters = (uint32_t*)((char*)ws + kCounters);
+  a.scratch = (char*)ws + kHeadBytes;
   a.seqs = p->seqs;
   a.rows = p->rows;
   a.page_size = p->page_size;

@@ -28,11 +28,11 @@ def torch_dtype(code: int) -> torch.dtype:
 
 
 def alloc_workspace(nbytes: int, device) -> torch.Tensor:
-    """A workspace whose error word is clear (later calls only ever set it)."""
+    """A workspace with its head cleared (the error word and the counters)."""
     if nbytes == 0:
         raise ValueError("not a valid problem")
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+    ws[:8192].zero_()
     return ws
 
 

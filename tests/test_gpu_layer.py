@@ -142,6 +142,9 @@ WINDOW = [
     (2, 2, 2, 515, 64, "bf16", 200, 300, (515, 400), False),
     (1, 2, 2, 1100, 128, "bf16", 130, 4, None, True),
     (1, 8, 1, 1030, 64, "bf16", 2000, 5, None, False),
+    # several tiles a CTA, many of them empty in a row
+    (4, 16, 4, 1100, 64, "bf16", 300, 3, (1100, 0, 100, 1), False),
+    (5, 12, 12, 900, 128, "bf16", 0, 0, (0, 0, 1, 900, 0), False),
     (2, 4, 2, 200, 32, "f32", 48, 4, None, False),
     (1, 2, 1, 131, 64, "f32", 0, 0, (100,), True),
     (2, 3, 3, 190, 128, "f32", 1, 0, (65, 190), False),
