@@ -330,65 +330,74 @@ ELSAA_DEV Partial partial_row(const AttendArgs& a, const Shape& sh, int d, int s
   return {o + at * d, reinterpret_cast<float2*>(o + slots * sh.slot_rows * d) + at};
 }
 
-// The rows of one warp of a cut item from the partials of all its CTAs, in their
-// order: m = max m_i, y = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.  Lanes over the
-// columns, four rows at a time.
-template <int D>
-ELSAA_DEV void merge_rows(const AttendArgs& a, const Shape& sh, const Item& it, int st, int warp_row) {
+// R of them at a time; lanes over the columns.  w: the lane's row's weight of a CTA.
+template <int D, int R>
+ELSAA_DEV void merge_group(const AttendArgs& a, const Shape& sh, const Item& it, int st, int row0,
+                           int x0, int rows, float m) {
   constexpr int V = D / 32;   // values of a lane
   const int lane = threadIdx.x & 31, cta0 = it.cta0, cta1 = it.cta1, slot0 = it.slot0;
-  auto part = [&](int cta, int row) {
-    return partial_row(a, sh, D, (cta * 2 + (cta == cta0 ? slot0 : 0)) * 2 + st, row);
-  };
-  const int tt = sh.tt, g = a.g, tokens = it.tokens, r0 = pick(it.r0, st);
-  for (int x0 = warp_row; x0 < warp_row + 32; x0 += 4) {
-    if (x0 / g >= tt || r0 + x0 / g >= tokens) break;   // (rows end with the tokens)
-    int row[4];                                         // (a row past the end: the first again)
-    float m[4], l[4], o[4][V];
+  float o[R][V], l = 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int tok = (x0 + x) / g;
-      row[x] = tok < tt && r0 + tok < tokens ? x0 + x : x0;
-      float top = -INFINITY;
-      for (int i = cta0 + lane; i <= cta1; i += 32) top = fmaxf(top, __ldcg(part(i, row[x]).ml).x);
-      m[x] = top;
-      l[x] = 0.f;
+  for (int x = 0; x < R; ++x)
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[x][e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) o[x][e] = 0.f;
+#pragma unroll(16 / R)
+  for (int i = cta0; i <= cta1; ++i) {
+    const int slot = (i * 2 + (i == cta0 ? slot0 : 0)) * 2 + st;
+    const float2 ml = __ldcg(partial_row(a, sh, D, slot, row0 + min(lane, rows - 1)).ml);
+    const float* p = partial_row(a, sh, D, slot, row0).o + lane * V;
+    float v[R][V];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) m[x] = warp_max(m[x]);
-#pragma unroll 4
-    for (int i = cta0; i <= cta1; ++i) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const Partial p = part(i, row[x]);
-        const float2 ml = __ldcg(p.ml);
-        float v[V];
-        if (V == 4) {
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(p.o) + lane);
-          v[0] = u.x, v[1] = u.y, v[2 % V] = u.z, v[3 % V] = u.w;
-        } else {
-          const float2 u = __ldcg(reinterpret_cast<const float2*>(p.o) + lane);
-          v[0] = u.x, v[1] = u.y;
-        }
-        const float w = ml.x > -INFINITY ? ex2(ml.x - m[x]) : 0.f;   // (no blocks of the stream there)
-        l[x] += ml.y * w;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[x][e] += v[e] * w;
+    for (int x = 0; x < R; ++x) {   // (past the last row: that one again)
+      const float* q = p + (int64_t)min(x0 + x, rows - 1) * D;
+      if (V == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(q));
+        v[x][0] = u.x, v[x][1] = u.y, v[x][2 % V] = u.z, v[x][3 % V] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(q));
+        v[x][0] = u.x, v[x][1] = u.y;
       }
     }
+    const float w = ml.x > -INFINITY ? ex2(ml.x - m) : 0.f;   // (no blocks of the stream there)
+    l += ml.y * w;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float inv = l[x] > 0.f ? 1.0f / l[x] : 0.f;
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
-                         (int64_t)(it.start + r0 + row[x] / g) * a.sy.n +
-                         (int64_t)(it.hk * g + row[x] % g) * a.sy.h + lane * V;
+    for (int x = 0; x < R; ++x) {
+      const float wx = __shfl_sync(0xffffffffu, w, min(x0 + x, rows - 1));
 #pragma unroll
-      for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<__nv_bfloat162*>(y + e) =
-            __floats2bfloat162_rn(o[x][e] * inv, o[x][(e + 1) % V] * inv);
+      for (int e = 0; e < V; ++e) o[x][e] += v[x][e] * wx;
     }
+  }
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll
+  for (int x = 0; x < R; ++x) {
+    const float f = __shfl_sync(0xffffffffu, inv, min(x0 + x, rows - 1));
+    if (x0 + x >= rows) break;
+    const int row = row0 + x0 + x;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
+                       (int64_t)(it.start + pick(it.r0, st) + row / a.g) * a.sy.n +
+                       (int64_t)(it.hk * a.g + row % a.g) * a.sy.h + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(y + e) =
+          __floats2bfloat162_rn(o[x][e] * f, o[x][(e + 1) % V] * f);
+  }
+}
+
+// The rows of one warp of a cut item from the partials of all its CTAs, in their
+// order: m = max m_i, y = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
+template <int D>
+ELSAA_DEV void merge_rows(const AttendArgs& a, const Shape& sh, const Item& it, int st, int row0) {
+  const int lane = threadIdx.x & 31, cta0 = it.cta0, cta1 = it.cta1, slot0 = it.slot0;
+  const int rows = min(min(sh.tt, it.tokens - pick(it.r0, st)) * a.g - row0, 32);   // (at least 1)
+  float m = -INFINITY;   // of row `lane`
+#pragma unroll 8
+  for (int i = cta0; i <= cta1; ++i)
+    m = fmaxf(m, __ldcg(partial_row(a, sh, D, (i * 2 + (i == cta0 ? slot0 : 0)) * 2 + st,
+                                    row0 + min(lane, rows - 1)).ml).x);
+  if (rows <= 4) {
+    merge_group<D, 4>(a, sh, it, st, row0, 0, rows, m);
+  } else {
+    for (int x0 = 0; x0 < rows; x0 += 8) merge_group<D, 8>(a, sh, it, st, row0, x0, rows, m);
   }
 }
 

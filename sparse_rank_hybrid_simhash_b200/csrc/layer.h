@@ -27,7 +27,7 @@ constexpr size_t kCounters = 256;   // byte offset of the counters
 
 // Most blocks that leave a partial sum of a weight's gradient (queries' and
 // keys' together): a fixed number, so the summation order is fixed.
-constexpr int kRotaryPartials = 1184;
+constexpr int kRotaryPartials = 444;   // 3 x 148: all resident
 
 struct RotaryArgs {
   const void *q, *k;

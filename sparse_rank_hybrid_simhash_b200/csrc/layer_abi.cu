@@ -26,8 +26,8 @@ bool shape_ok(int B, int H, int Hkv, int N, int d, int dtype, elsaa_status* why)
   *why = ELSAA_ERR_INVALID_ARG;
   if (B <= 0 || H <= 0 || Hkv <= 0 || N <= 0 || H > 16384 || H % Hkv != 0) return false;
   if (dtype != ELSAA_BF16 && dtype != ELSAA_F32) return false;
-  // rows are numbered in 32 bits (elements and bytes in 64)
-  if ((int64_t)B * H > INT32_MAX || (int64_t)B * H * N > INT32_MAX) return false;
+  // rows are numbered in 32 bits, with room for the last tile (elements and bytes in 64)
+  if ((int64_t)B * H > INT32_MAX || (int64_t)B * H * N > INT32_MAX - 4096) return false;
   return head_dim(d, why);
 }
 

@@ -14,7 +14,9 @@
 // halves a lane's partner values sit rot / (2 V) lanes away.  A group keeps its
 // token's cos and sin in registers and walks several heads of that token,
 // so the table (8 rot / 2 bytes a token, more than a bf16 row) is read once per
-// head chunk, not per head.
+// head chunk, not per head; four heads' rows are in flight at a time (an output may
+// be its input, so the compiler must keep a later row's load behind an earlier
+// row's store: text-32k queries and keys 102 us without the batches).
 #include "common.cuh"
 #include "internal.h"
 #include "layer.h"
@@ -23,6 +25,7 @@ namespace elsaa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;       // heads whose rows are in flight
 constexpr int kStarts = 2048;   // sequence starts kept in shared memory
 
 template <typename T>
@@ -30,12 +33,16 @@ struct Vec {
   static constexpr int V = 16 / sizeof(T);
 };
 
-ELSAA_DEV void load_row(const float* p, float* x) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+// A lane's 16 bytes of a row as fp32.
+template <typename T>
+ELSAA_DEV void unpack(const uint4& v, float* x);
+template <>
+ELSAA_DEV void unpack<float>(const uint4& v, float* x) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
 }
-ELSAA_DEV void load_row(const __nv_bfloat16* p, float* x) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+template <>
+ELSAA_DEV void unpack<__nv_bfloat16>(const uint4& v, float* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -151,13 +158,13 @@ ELSAA_DEV const float* table_row(const RotaryArgs& a, int pos, bool lead) {
 
 // blockIdx.y: chunks of HP query heads, then of HP key heads.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
   constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
   const int col = (threadIdx.x % LANES) * V;
-  const int64_t tok = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
-  const bool live = tok < (int64_t)a.B * a.N;
-  const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok % a.N) : 0;
+  const int tok = blockIdx.x * ROWS + threadIdx.x / LANES;   // (B N < 2^31 / H)
+  const bool live = tok < a.B * a.N;
+  const int b = live ? tok / a.N : 0, n = live ? tok - b * a.N : 0;
   const bool is_q = (int)blockIdx.y < q_chunks;
   const int h0 = (is_q ? blockIdx.y : blockIdx.y - q_chunks) * hp;
   const int h1 = min(h0 + hp, is_q ? a.H : a.Hkv);
@@ -170,17 +177,24 @@ norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
   Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
   float w[V];
   load_weight<V>(is_q ? a.wq : a.wk, col, w);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    float x[V];
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.f;
-    if (live) load_row(in + h * si.h, x);
-    row_forward<D, V, IL>(x, w, ang, col, a);
-    if (!ok)
+    for (int u = 0; u < kBatch; ++u) {
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (live && h + u < h1) raw[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
+    }
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = 0.f;
-    if (live) store_row(out + h * so.h, x);
+    for (int u = 0; u < kBatch; ++u) {
+      if (h + u >= h1) break;
+      float x[V];
+      unpack<T>(raw[u], x);
+      row_forward<D, V, IL>(x, w, ang, col, a);
+      if (!ok)
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 0.f;
+      if (live) store_row(out + (h + u) * so.h, x);
+    }
   }
 }
 
@@ -188,15 +202,15 @@ norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
 // queries, the rest those of the keys; each block leaves one partial sum of
 // its weight's gradient.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
   const int col = (threadIdx.x % LANES) * V;
   const bool is_q = (int)blockIdx.x < q_blocks;
   const int heads = is_q ? a.H : a.Hkv;
   const int chunks = (heads + hp - 1) / hp;
-  const int64_t groups = ((int64_t)a.B * a.N + ROWS - 1) / ROWS;
-  const int64_t items = groups * chunks;
+  const int tokens = a.B * a.N;   // (tokens and items: below 2^31)
+  const int items = (tokens + ROWS - 1) / ROWS * chunks;
   const int first = is_q ? blockIdx.x : blockIdx.x - q_blocks;
   const int step = is_q ? q_blocks : gridDim.x - q_blocks;
   const Strides si = is_q ? a.sq : a.sk, sg = is_q ? a.sdqo : a.sdko, so = is_q ? a.sqo : a.sko;
@@ -204,11 +218,11 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   load_weight<V>(is_q ? a.wq : a.wk, col, w);
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = 0.f;
-  for (int64_t it = first; it < items; it += step) {
-    const int64_t tok = it / chunks * ROWS + threadIdx.x / LANES;
-    const int h0 = (int)(it % chunks) * hp, h1 = min(h0 + hp, heads);
-    const bool live = tok < (int64_t)a.B * a.N;
-    const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok % a.N) : 0;
+  for (int it = first; it < items; it += step) {
+    const int group = it / chunks, tok = group * ROWS + threadIdx.x / LANES;
+    const int h0 = (it - group * chunks) * hp, h1 = min(h0 + hp, heads);
+    const bool live = tok < tokens;
+    const int b = live ? tok / a.N : 0, n = live ? tok - b * a.N : 0;
     const T* in = static_cast<const T*>(is_q ? a.q : a.k) + b * si.b + n * si.n + col;
     const T* dy = static_cast<const T*>(is_q ? a.dqo : a.dko) + b * sg.b + n * sg.n + col;
     T* out = static_cast<T*>(is_q ? a.qo : a.ko) + b * so.b + n * so.n + col;
@@ -216,35 +230,43 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
     const float* tab = table_row(a, pos, live && col == 0);
     const bool ok = a.rot == 0 || tab != nullptr;
     const Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-      float x[V], g[V];
+    for (int h = h0; h < h1; h += 2) {
+      uint4 rx[2], rg[2];
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = g[i] = 0.f;
-      if (live && ok) {   // (a row without a position was written as zeros: no gradient)
-        load_row(in + h * si.h, x);
-        load_row(dy + h * sg.h, g);
-      }
-      rotate<V, IL, true, LANES>(g, ang, col, a.rot);
-      if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) ss += x[i] * x[i];
-        ss = group_sum<LANES>(ss);
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          x[i] *= r;
-          if (ok) dw[i] += g[i] * x[i];
-          g[i] *= w[i];
-          dot += g[i] * x[i];
+      for (int u = 0; u < 2; ++u) {
+        rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
+        if (live && ok && h + u < h1) {   // (a row without a position was written as zeros: no gradient)
+          rx[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
+          rg[u] = *reinterpret_cast<const uint4*>(dy + (h + u) * sg.h);
         }
-        dot = group_sum<LANES>(dot) * (1.0f / D);
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = ok ? r * (g[i] - x[i] * dot) : 0.f;
       }
-      if (live) store_row(out + h * so.h, g);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (h + u >= h1) break;
+        float x[V], g[V];
+        unpack<T>(rx[u], x);
+        unpack<T>(rg[u], g);
+        rotate<V, IL, true, LANES>(g, ang, col, a.rot);
+        if (a.norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) ss += x[i] * x[i];
+          ss = group_sum<LANES>(ss);
+          const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            x[i] *= r;
+            if (ok) dw[i] += g[i] * x[i];
+            g[i] *= w[i];
+            dot += g[i] * x[i];
+          }
+          dot = group_sum<LANES>(dot) * (1.0f / D);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] = ok ? r * (g[i] - x[i] * dot) : 0.f;
+        }
+        if (live) store_row(out + (h + u) * so.h, g);
+      }
     }
   }
   if ((is_q ? a.dwq : a.dwk) == nullptr) return;
@@ -260,9 +282,9 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   }
 }
 
-// dw of the queries (block y = 0) and keys (1): 32 columns a block, warps over
+// dw of the queries (block y = 0) and keys (1): 32 columns a block, 32 warps over
 // the partials in a fixed order, in 64 bits.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(1024)
 weight_reduce_kernel(const RotaryArgs a, int d, int q_blocks, int blocks) {
   const bool is_q = blockIdx.y == 0;
   float* to = is_q ? a.dwq : a.dwk;
@@ -271,14 +293,16 @@ weight_reduce_kernel(const RotaryArgs a, int d, int q_blocks, int blocks) {
   const int c = blockIdx.x * 32 + lane;
   const int lo = is_q ? 0 : q_blocks, hi = is_q ? q_blocks : blocks;
   double s = 0.0;
-  for (int r = lo + warp; r < hi; r += kThreads / 32) s += (double)a.partials[(int64_t)r * d + c];
-  __shared__ double part[kThreads / 32][32];
-  part[warp][lane] = s;
+#pragma unroll 8
+  for (int r = lo + warp; r < hi; r += 32) s += (double)a.partials[(int64_t)r * d + c];
+  __shared__ double part[32][33];
+  part[lane][warp] = s;
   __syncthreads();
-  if (warp == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) s += part[i][lane];
-    to[c] = (float)s;
-  }
+  // warp x adds column x up
+  double v = part[warp][lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) to[blockIdx.x * 32 + warp] = (float)v;
 }
 
 // The write into the cache: blockIdx.y walks chunks of hp query heads, key
@@ -323,10 +347,15 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
     const T* in = static_cast<const T*>(a.v) + row * a.sv.n + col;
     T* out = static_cast<T*>(a.v_pages) + page * a.svp.b + slot * a.svp.n + col;
     if (ok)
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h)
-        *reinterpret_cast<uint4*>(out + h * a.svp.h) =
-            *reinterpret_cast<const uint4*>(in + h * a.sv.h);
+      for (int h = h0; h < h1; h += kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (h + u < h1) raw[u] = *reinterpret_cast<const uint4*>(in + (h + u) * a.sv.h);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (h + u < h1) *reinterpret_cast<uint4*>(out + (h + u) * a.svp.h) = raw[u];
+      }
     return;
   }
   const Strides si = kind == 0 ? a.sq : a.sk;
@@ -339,18 +368,25 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
   const Angles<V, IL> ang = load_angles<V, IL>(tab, pos_ok ? col : D, pos_ok ? a.rot : 0);
   float w[V];
   load_weight<V>(kind == 0 ? a.wq : a.wk, col, w);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    float x[V];
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.f;
-    if (pos_ok) load_row(in + h * si.h, x);
-    row_forward<D, V, IL>(x, w, ang, col, a);
-    if (!pos_ok)
+    for (int u = 0; u < kBatch; ++u) {
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (pos_ok && h + u < h1) raw[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
+    }
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = 0.f;
-    // a query row without a position is zeros; a key row is written with a page only
-    if (kind == 0 ? live : ok) store_row(out + h * oh, x);
+    for (int u = 0; u < kBatch; ++u) {
+      if (h + u >= h1) break;
+      float x[V];
+      unpack<T>(raw[u], x);
+      row_forward<D, V, IL>(x, w, ang, col, a);
+      if (!pos_ok)
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 0.f;
+      // a query row without a position is zeros; a key row is written with a page only
+      if (kind == 0 ? live : ok) store_row(out + (h + u) * oh, x);
+    }
   }
 }
 
@@ -401,7 +437,7 @@ struct Backward {
     const int64_t tokens = (int64_t)a.B * a.N, groups = (tokens + ROWS - 1) / ROWS;
     const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
     const int64_t qi = groups * ((a.H + hp - 1) / hp), ki = groups * ((a.Hkv + hp - 1) / hp);
-    // blocks by the share of the items, all resident at once (4 x 148, at most two waves)
+    // blocks by the share of the items, all resident at once
     const int64_t cap = kRotaryPartials;
     int64_t qb = qi, kb = ki;
     if (qi + ki > cap) {
@@ -413,7 +449,7 @@ struct Backward {
     norm_rotate_back_kernel<T, D, IL><<<(unsigned)(qb + kb), kThreads, 0, s>>>(a, hp, (int)qb);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;
-    weight_reduce_kernel<<<dim3(D / 32, 2), kThreads, 0, s>>>(a, D, (int)qb, (int)(qb + kb));
+    weight_reduce_kernel<<<dim3(D / 32, 2), 1024, 0, s>>>(a, D, (int)qb, (int)(qb + kb));
     return cudaGetLastError();
   }
 };

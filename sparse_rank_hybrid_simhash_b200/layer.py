@@ -4,6 +4,7 @@ the call into libelsaa on the tensors' own device."""
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -36,36 +37,35 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-def check(where: str, t: Optional[torch.Tensor], shape: Sequence[int], dtype: torch.dtype,
+def check(where: str, t: torch.Tensor, shape: Sequence[int], dtype: torch.dtype,
           device: torch.device) -> None:
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{where}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{where}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{where}: on {t.device}, expected {device}")
+    raise ValueError(f"{where}: on {t.device}, expected {device}")
 
 
 def strided(t: torch.Tensor) -> bool:
     """Whether the library takes the tensor where it lies: the last dimension
     contiguous, the other strides positive multiples of 16 bytes that no two
     rows share, the start on 16 bytes."""
-    if t.is_contiguous():
-        return t.data_ptr() & 15 == 0
-    e, d = t.element_size(), t.shape[-1]
-    if t.stride(-1) != 1 or t.data_ptr() & 15:
+    if t.data_ptr() & 15:
         return False
-    return all(n == 1 or (s >= d and s * e % 16 == 0)
-               for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    if t.is_contiguous():
+        return True
+    e, d = t.element_size(), t.shape[-1]
+    return t.stride(-1) == 1 and all(n == 1 or (s >= d and s * e % 16 == 0)
+                                     for n, s in zip(t.shape[:-1], t.stride()[:-1]))
 
 
 def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
     """The checked tensor, or a dense copy of one the library does not take
     where it lies (a broadcast one, an odd stride or offset)."""
     check(where, t, shape, dtype, device)
-    if strided(t):
-        return t
-    return t.clone(memory_format=torch.contiguous_format)
+    return t if strided(t) else t.clone(memory_format=torch.contiguous_format)
 
 
 def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
@@ -79,20 +79,22 @@ def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> to
 
 
 def as_small(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> Optional[torch.Tensor]:
-    """An optional dense int32 / fp32 tensor."""
+    """An optional int32 / fp32 tensor, dense and on 16 bytes (copied where it is not)."""
     if t is None:
         return None
     check(where, t, shape, dtype, device)
-    t = t.contiguous()
-    return t if t.data_ptr() & 15 == 0 else t.clone()
+    if t.is_contiguous() and not t.data_ptr() & 15:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
-def as_workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+def as_workspace(ws: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
+    """The caller's workspace (the library checks its size), or a new one of nbytes()."""
     if ws is None:
-        return alloc_workspace(nbytes, device)
+        return alloc_workspace(nbytes(), device)
     if ws.device != device:
         raise ValueError(f"ws: on {ws.device}, expected {device}")
-    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous uint8 tensor")
     return ws
 
@@ -100,7 +102,10 @@ def as_workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tenso
 def strides_of(dims: int, *tensors: Optional[torch.Tensor]):
     """Host array of the first `dims` strides of every tensor, or None where
     all are dense."""
-    if all(t is None or t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
         return None
     flat = []
     for t in tensors:
@@ -112,32 +117,29 @@ def ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-class on:
-    """Makes the tensors' device current and, where a stream is given, makes it
-    the one that allocations inside belong to."""
-
-    __slots__ = ("stream", "guards")
-
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {device}")
-        self.guards = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
+def on_device(at: int):
+    """Decorator of the entry points f(..., q, ..., stream=None), q the argument number ``at``:
+    runs f with q's device current and the given stream (or the device's current one) current
+    for its allocations; f gets the raw stream."""
+    def wrap(f):
+        @functools.wraps(f)
+        def call(*args, stream=None, **kw):
+            device = (args[at] if len(args) > at else kw["q"]).device
+            if device.type != "cuda":
+                raise ValueError(f"tensors must be on a CUDA device, got {device}")
+            if stream is None:
+                if device.index == torch.cuda.current_device():
+                    return f(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+                with torch.cuda.device(device):
+                    return f(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
             if stream.device != device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.guards.append(torch.cuda.stream(stream))
-        self.stream = stream
+            with torch.cuda.device(device), torch.cuda.stream(stream):
+                return f(*args, stream=stream.cuda_stream, **kw)
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return (self.stream or torch.cuda.current_stream()).cuda_stream
+        return call
 
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+    return wrap
 
 
 def ok(where: str, code: int) -> None:

@@ -66,48 +66,48 @@ def _cache(p: PagedParams, k_pages, v_pages, page_table, starts, lengths, dev):
             layer.as_small("lengths", lengths, (p.seqs,), torch.int32, dev))
 
 
+@layer.on_device(2)
 def write(p: PagedParams, rp: RotaryParams, q, k, v, table, q_weight, k_weight, k_pages, v_pages,
           page_table, starts, lengths, qo=None, ws=None, stream=None) -> torch.Tensor:
     """qo [T, H, d], the new tokens' queries normed and rotated at their positions; their keys
     (likewise) and values [T, Hkv, d] go into the pages.  ``rp``: H, Hkv, d and dtype as in ``p``."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
-        k = layer.as_input("k", k, (p.rows, p.Hkv, p.d), dt, dev)
-        v = layer.as_input("v", v, (p.rows, p.Hkv, p.d), dt, dev)
-        qo = layer.as_output("qo", qo, (p.rows, p.H, p.d), dt, dev)
-        if rp.rot_dim > 0:
-            if table is None:
-                raise ValueError("rot_dim > 0 needs a table")
-            table = layer.as_small("table", table, (rp.max_pos, rp.rot_dim // 2, 2), torch.float32, dev)
-        q_weight = layer.as_small("q_weight", q_weight, (p.d,), torch.float32, dev)
-        k_weight = layer.as_small("k_weight", k_weight, (p.d,), torch.float32, dev)
-        k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
-                                                               starts, lengths, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_paged_write", lib().elsaa_paged_write(
-            ctypes.byref(p), ctypes.byref(rp), ptr(q), ptr(k), ptr(v),
-            layer.strides_of(2, q, qo, k, v), ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo),
-            ptr(k_pages), ptr(v_pages), layer.strides_of(3, k_pages, v_pages), ptr(page_table),
-            ptr(starts), ptr(lengths), ptr(ws), ws.numel(), st))
+    q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
+    k = layer.as_input("k", k, (p.rows, p.Hkv, p.d), dt, dev)
+    v = layer.as_input("v", v, (p.rows, p.Hkv, p.d), dt, dev)
+    qo = layer.as_output("qo", qo, (p.rows, p.H, p.d), dt, dev)
+    if rp.rot_dim > 0:
+        if table is None:
+            raise ValueError("rot_dim > 0 needs a table")
+        table = layer.as_small("table", table, (rp.max_pos, rp.rot_dim // 2, 2), torch.float32, dev)
+    q_weight = layer.as_small("q_weight", q_weight, (p.d,), torch.float32, dev)
+    k_weight = layer.as_small("k_weight", k_weight, (p.d,), torch.float32, dev)
+    k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
+                                                           starts, lengths, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_paged_write", lib().elsaa_paged_write(
+        ctypes.byref(p), ctypes.byref(rp), ptr(q), ptr(k), ptr(v),
+        layer.strides_of(2, q, qo, k, v), ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo),
+        ptr(k_pages), ptr(v_pages), layer.strides_of(3, k_pages, v_pages), ptr(page_table),
+        ptr(starts), ptr(lengths), ptr(ws), ws.numel(), stream))
     return qo
 
 
+@layer.on_device(1)
 def attend(p: PagedParams, q, k_pages, v_pages, page_table, starts, lengths, y=None, ws=None,
            stream=None) -> torch.Tensor:
     """y [T, H, d]: attention of the new tokens q [T, H, d] over their sequences' cached keys and
     values (their own already written)."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
-        y = layer.as_output("y", y, (p.rows, p.H, p.d), dt, dev)
-        k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
-                                                               starts, lengths, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_paged_attend", lib().elsaa_paged_attend(
-            ctypes.byref(p), ptr(q), layer.strides_of(2, q, y), ptr(k_pages), ptr(v_pages),
-            layer.strides_of(3, k_pages, v_pages), ptr(page_table), ptr(starts), ptr(lengths),
-            ptr(y), ptr(ws), ws.numel(), st))
+    q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
+    y = layer.as_output("y", y, (p.rows, p.H, p.d), dt, dev)
+    k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
+                                                           starts, lengths, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_paged_attend", lib().elsaa_paged_attend(
+        ctypes.byref(p), ptr(q), layer.strides_of(2, q, y), ptr(k_pages), ptr(v_pages),
+        layer.strides_of(3, k_pages, v_pages), ptr(page_table), ptr(starts), ptr(lengths),
+        ptr(y), ptr(ws), ws.numel(), stream))
     return y

@@ -69,58 +69,58 @@ def _small(p: RotaryParams, table, q_weight, k_weight, positions, dev):
             layer.as_small("positions", positions, (p.B, p.N), torch.int32, dev))
 
 
+@layer.on_device(1)
 def forward(p: RotaryParams, q, k, table=None, q_weight=None, k_weight=None, positions=None,
             qo=None, ko=None, ws=None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(qo, ko): q [B, H, N, d] and k [B, Hkv, N, d] (or None) normed and rotated.  Views with
     other strides (heads of a fused projection) are read in place."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, sq, dt, dev)
-        qo = layer.as_output("qo", qo, sq, dt, dev)
-        if k is not None:
-            k = layer.as_input("k", k, sk, dt, dev)
-            ko = layer.as_output("ko", ko, sk, dt, dev)
-        elif ko is not None:
-            raise ValueError("ko without k")
-        table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_rotary_forward", lib().elsaa_rotary_forward(
-            ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, qo, ko), ptr(positions),
-            ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo), ptr(ko), ptr(ws), ws.numel(), st))
+    q = layer.as_input("q", q, sq, dt, dev)
+    qo = layer.as_output("qo", qo, sq, dt, dev)
+    if k is not None:
+        k = layer.as_input("k", k, sk, dt, dev)
+        ko = layer.as_output("ko", ko, sk, dt, dev)
+    elif ko is not None:
+        raise ValueError("ko without k")
+    table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_rotary_forward", lib().elsaa_rotary_forward(
+        ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, qo, ko), ptr(positions),
+        ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo), ptr(ko), ptr(ws), ws.numel(), stream))
     return qo, ko
 
 
+@layer.on_device(1)
 def backward(p: RotaryParams, q, k, table, q_weight, k_weight, dqo, dko, positions=None, dq=None,
              dk=None, dq_weight=None, dk_weight=None, ws=None, stream=None):
     """(dq, dk, dq_weight, dk_weight) of sum(qo * dqo) + sum(ko * dko); the weights' gradients
     are None without the norm, dk's and dk_weight's without k."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, sq, dt, dev)
-        dqo = layer.as_input("dqo", dqo, sq, dt, dev)
-        dq = layer.as_output("dq", dq, sq, dt, dev)
+    q = layer.as_input("q", q, sq, dt, dev)
+    dqo = layer.as_input("dqo", dqo, sq, dt, dev)
+    dq = layer.as_output("dq", dq, sq, dt, dev)
+    if k is not None:
+        k = layer.as_input("k", k, sk, dt, dev)
+        dko = layer.as_input("dko", dko, sk, dt, dev)
+        dk = layer.as_output("dk", dk, sk, dt, dev)
+    elif dko is not None or dk is not None:
+        raise ValueError("dko or dk without k")
+    if p.norm:
+        dq_weight = layer.as_output("dq_weight", dq_weight, (p.d,), torch.float32, dev)
         if k is not None:
-            k = layer.as_input("k", k, sk, dt, dev)
-            dko = layer.as_input("dko", dko, sk, dt, dev)
-            dk = layer.as_output("dk", dk, sk, dt, dev)
-        elif dko is not None or dk is not None:
-            raise ValueError("dko or dk without k")
-        if p.norm:
-            dq_weight = layer.as_output("dq_weight", dq_weight, (p.d,), torch.float32, dev)
-            if k is not None:
-                dk_weight = layer.as_output("dk_weight", dk_weight, (p.d,), torch.float32, dev)
-        else:
-            dq_weight = dk_weight = None
-        table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_rotary_backward", lib().elsaa_rotary_backward(
-            ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, dqo, dko, dq, dk),
-            ptr(positions), ptr(table), ptr(q_weight), ptr(k_weight), ptr(dqo), ptr(dko), ptr(dq),
-            ptr(dk), ptr(dq_weight), ptr(dk_weight), ptr(ws), ws.numel(), st))
+            dk_weight = layer.as_output("dk_weight", dk_weight, (p.d,), torch.float32, dev)
+    else:
+        dq_weight = dk_weight = None
+    table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_rotary_backward", lib().elsaa_rotary_backward(
+        ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, dqo, dko, dq, dk),
+        ptr(positions), ptr(table), ptr(q_weight), ptr(k_weight), ptr(dqo), ptr(dko), ptr(dq),
+        ptr(dk), ptr(dq_weight), ptr(dk_weight), ptr(ws), ws.numel(), stream))
     return dq, dk, dq_weight, dk_weight
 
 

@@ -46,54 +46,54 @@ def _shapes(p: WindowParams):
     return (p.B, p.H, p.N, p.d), (p.B, p.Hkv, p.N, p.d)
 
 
+@layer.on_device(1)
 def forward(p: WindowParams, q, k, v, lengths=None, y=None, lse=None, ws=None,
             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(y [B, H, N, d], lse [B, H, N] fp32).  Views of q, k, v, y with other strides are taken
     in place."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, sq, dt, dev)
-        k = layer.as_input("k", k, sk, dt, dev)
-        v = layer.as_input("v", v, sk, dt, dev)
-        y = layer.as_output("y", y, sq, dt, dev)
-        if lse is None:
-            lse = torch.empty(sq[:3], dtype=torch.float32, device=dev)
-        layer.check("lse", lse, sq[:3], torch.float32, dev)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-        lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p, False), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_window_forward", lib().elsaa_window_forward(
-            ctypes.byref(p), ptr(q), ptr(k), ptr(v), layer.strides_of(3, q, k, v, y), ptr(lengths),
-            ptr(y), ptr(lse), ptr(ws), ws.numel(), st))
+    q = layer.as_input("q", q, sq, dt, dev)
+    k = layer.as_input("k", k, sk, dt, dev)
+    v = layer.as_input("v", v, sk, dt, dev)
+    y = layer.as_output("y", y, sq, dt, dev)
+    if lse is None:
+        lse = torch.empty(sq[:3], dtype=torch.float32, device=dev)
+    layer.check("lse", lse, sq[:3], torch.float32, dev)
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p, False), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_window_forward", lib().elsaa_window_forward(
+        ctypes.byref(p), ptr(q), ptr(k), ptr(v), layer.strides_of(3, q, k, v, y), ptr(lengths),
+        ptr(y), ptr(lse), ptr(ws), ws.numel(), stream))
     return y, lse
 
 
+@layer.on_device(1)
 def backward(p: WindowParams, q, k, v, y, lse, dy, lengths=None, dq=None, dk=None, dv=None,
              ws=None, stream=None):
     """(dq, dk, dv) of sum(y * dy), from the y and lse of ``forward`` on the same inputs."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    with layer.on(dev, stream) as st:
-        q = layer.as_input("q", q, sq, dt, dev)
-        k = layer.as_input("k", k, sk, dt, dev)
-        v = layer.as_input("v", v, sk, dt, dev)
-        y = layer.as_input("y", y, sq, dt, dev)
-        dy = layer.as_input("dy", dy, sq, dt, dev)
-        layer.check("lse", lse, sq[:3], torch.float32, dev)
-        lse = lse.contiguous()
-        dq = layer.as_output("dq", dq, sq, dt, dev)
-        dk = layer.as_output("dk", dk, sk, dt, dev)
-        dv = layer.as_output("dv", dv, sk, dt, dev)
-        lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
-        ws = layer.as_workspace(ws, workspace_bytes(p, True), dev)
-        ptr = layer.ptr
-        layer.ok("elsaa_window_backward", lib().elsaa_window_backward(
-            ctypes.byref(p), ptr(q), ptr(k), ptr(v),
-            layer.strides_of(3, q, k, v, y, dy, dq, dk, dv), ptr(lengths), ptr(y), ptr(lse),
-            ptr(dy), ptr(dq), ptr(dk), ptr(dv), ptr(ws), ws.numel(), st))
+    q = layer.as_input("q", q, sq, dt, dev)
+    k = layer.as_input("k", k, sk, dt, dev)
+    v = layer.as_input("v", v, sk, dt, dev)
+    y = layer.as_input("y", y, sq, dt, dev)
+    dy = layer.as_input("dy", dy, sq, dt, dev)
+    layer.check("lse", lse, sq[:3], torch.float32, dev)
+    lse = lse.contiguous()
+    dq = layer.as_output("dq", dq, sq, dt, dev)
+    dk = layer.as_output("dk", dk, sk, dt, dev)
+    dv = layer.as_output("dv", dv, sk, dt, dev)
+    lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+    ws = layer.as_workspace(ws, lambda: workspace_bytes(p, True), dev)
+    ptr = layer.ptr
+    layer.ok("elsaa_window_backward", lib().elsaa_window_backward(
+        ctypes.byref(p), ptr(q), ptr(k), ptr(v),
+        layer.strides_of(3, q, k, v, y, dy, dq, dk, dv), ptr(lengths), ptr(y), ptr(lse),
+        ptr(dy), ptr(dq), ptr(dk), ptr(dv), ptr(ws), ws.numel(), stream))
     return dq, dk, dv
 
 
