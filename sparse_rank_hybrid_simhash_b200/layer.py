@@ -39,13 +39,12 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
 
 def check(where: str, t: torch.Tensor, shape: Sequence[int], dtype: torch.dtype,
           device: torch.device) -> None:
-    if t.dtype is dtype and t.shape == shape and t.device == device:
-        return
     if t.dtype != dtype:
         raise TypeError(f"{where}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{where}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{where}: on {t.device}, expected {device}")
+    if t.device != device:
+        raise ValueError(f"{where}: on {t.device}, expected {device}")
 
 
 def strided(t: torch.Tensor) -> bool:
@@ -64,12 +63,19 @@ def strided(t: torch.Tensor) -> bool:
 def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
     """The checked tensor, or a dense copy of one the library does not take
     where it lies (a broadcast one, an odd stride or offset)."""
-    check(where, t, shape, dtype, device)
-    return t if strided(t) else t.clone(memory_format=torch.contiguous_format)
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        check(where, t, shape, dtype, device)
+    if t.is_contiguous() and not t.data_ptr() & 15 or strided(t):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
-def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device,
+              like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The checked output, or a new dense one (``like``: of this shape and type)."""
     if t is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     check(where, t, shape, dtype, device)
     if not strided(t):
@@ -82,7 +88,8 @@ def as_small(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> Opt
     """An optional int32 / fp32 tensor, dense and on 16 bytes (copied where it is not)."""
     if t is None:
         return None
-    check(where, t, shape, dtype, device)
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        check(where, t, shape, dtype, device)
     if t.is_contiguous() and not t.data_ptr() & 15:
         return t
     return t.clone(memory_format=torch.contiguous_format)
@@ -117,6 +124,11 @@ def ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def on_device(at: int):
     """Decorator of the entry points f(..., q, ..., stream=None), q the argument number ``at``:
     runs f with q's device current and the given stream (or the device's current one) current
@@ -129,9 +141,9 @@ def on_device(at: int):
                 raise ValueError(f"tensors must be on a CUDA device, got {device}")
             if stream is None:
                 if device.index == torch.cuda.current_device():
-                    return f(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+                    return f(*args, stream=_raw_stream(device.index), **kw)
                 with torch.cuda.device(device):
-                    return f(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+                    return f(*args, stream=_raw_stream(device.index), **kw)
             if stream.device != device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
             with torch.cuda.device(device), torch.cuda.stream(stream):

@@ -58,8 +58,10 @@ def alloc_pages(p: PagedParams, device) -> Tuple[torch.Tensor, torch.Tensor]:
 def _cache(p: PagedParams, k_pages, v_pages, page_table, starts, lengths, dev):
     dt = layer.torch_dtype(p.dtype)
     shape = (p.pages, p.Hkv, p.page_size, p.d)
-    k_pages = layer.as_output("k_pages", k_pages, shape, dt, dev)
-    v_pages = layer.as_output("v_pages", v_pages, shape, dt, dev)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        layer.check(name, t, shape, dt, dev)
+        if not layer.strided(t):
+            raise ValueError(f"{name}: strides and start must be multiples of 16 bytes")
     return (k_pages, v_pages,
             layer.as_small("page_table", page_table, (p.seqs, p.table_width), torch.int32, dev),
             layer.as_small("starts", starts, (p.seqs + 1,), torch.int32, dev),
@@ -75,7 +77,7 @@ def write(p: PagedParams, rp: RotaryParams, q, k, v, table, q_weight, k_weight, 
     q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
     k = layer.as_input("k", k, (p.rows, p.Hkv, p.d), dt, dev)
     v = layer.as_input("v", v, (p.rows, p.Hkv, p.d), dt, dev)
-    qo = layer.as_output("qo", qo, (p.rows, p.H, p.d), dt, dev)
+    qo = layer.as_output("qo", qo, (p.rows, p.H, p.d), dt, dev, q)
     if rp.rot_dim > 0:
         if table is None:
             raise ValueError("rot_dim > 0 needs a table")
@@ -101,7 +103,7 @@ def attend(p: PagedParams, q, k_pages, v_pages, page_table, starts, lengths, y=N
     values (their own already written)."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
-    y = layer.as_output("y", y, (p.rows, p.H, p.d), dt, dev)
+    y = layer.as_output("y", y, (p.rows, p.H, p.d), dt, dev, q)
     k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
                                                            starts, lengths, dev)
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)

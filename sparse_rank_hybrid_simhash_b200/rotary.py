@@ -77,10 +77,10 @@ def forward(p: RotaryParams, q, k, table=None, q_weight=None, k_weight=None, pos
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
     q = layer.as_input("q", q, sq, dt, dev)
-    qo = layer.as_output("qo", qo, sq, dt, dev)
+    qo = layer.as_output("qo", qo, sq, dt, dev, q)
     if k is not None:
         k = layer.as_input("k", k, sk, dt, dev)
-        ko = layer.as_output("ko", ko, sk, dt, dev)
+        ko = layer.as_output("ko", ko, sk, dt, dev, k)
     elif ko is not None:
         raise ValueError("ko without k")
     table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
@@ -101,11 +101,11 @@ def backward(p: RotaryParams, q, k, table, q_weight, k_weight, dqo, dko, positio
     sq, sk = _shapes(p)
     q = layer.as_input("q", q, sq, dt, dev)
     dqo = layer.as_input("dqo", dqo, sq, dt, dev)
-    dq = layer.as_output("dq", dq, sq, dt, dev)
+    dq = layer.as_output("dq", dq, sq, dt, dev, q)
     if k is not None:
         k = layer.as_input("k", k, sk, dt, dev)
         dko = layer.as_input("dko", dko, sk, dt, dev)
-        dk = layer.as_output("dk", dk, sk, dt, dev)
+        dk = layer.as_output("dk", dk, sk, dt, dev, k)
     elif dko is not None or dk is not None:
         raise ValueError("dko or dk without k")
     if p.norm:

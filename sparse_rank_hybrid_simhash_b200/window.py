@@ -56,7 +56,7 @@ def forward(p: WindowParams, q, k, v, lengths=None, y=None, lse=None, ws=None,
     q = layer.as_input("q", q, sq, dt, dev)
     k = layer.as_input("k", k, sk, dt, dev)
     v = layer.as_input("v", v, sk, dt, dev)
-    y = layer.as_output("y", y, sq, dt, dev)
+    y = layer.as_output("y", y, sq, dt, dev, q)
     if lse is None:
         lse = torch.empty(sq[:3], dtype=torch.float32, device=dev)
     layer.check("lse", lse, sq[:3], torch.float32, dev)
@@ -84,9 +84,9 @@ def backward(p: WindowParams, q, k, v, y, lse, dy, lengths=None, dq=None, dk=Non
     dy = layer.as_input("dy", dy, sq, dt, dev)
     layer.check("lse", lse, sq[:3], torch.float32, dev)
     lse = lse.contiguous()
-    dq = layer.as_output("dq", dq, sq, dt, dev)
-    dk = layer.as_output("dk", dk, sk, dt, dev)
-    dv = layer.as_output("dv", dv, sk, dt, dev)
+    dq = layer.as_output("dq", dq, sq, dt, dev, q)
+    dk = layer.as_output("dk", dk, sk, dt, dev, k)
+    dv = layer.as_output("dv", dv, sk, dt, dev, v)
     lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p, True), dev)
     ptr = layer.ptr
