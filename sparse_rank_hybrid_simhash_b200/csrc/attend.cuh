@@ -33,21 +33,6 @@ __host__ __device__ inline KeyBlocks key_blocks(int p_lo, int p_hi, int window, 
 
 // ---- pages -----------------------------------------------------------------
 
-// Most row tiles of a paged call: rows (token, head of the group) of each
-// sequence fill tiles of their own.
-inline int64_t paged_tiles(const AttendArgs& a, int tile) {
-  return ((int64_t)a.rows * a.g + tile - 1) / tile + a.seqs;
-}
-
-struct PagedTile {
-  int seq;     // -1: no such tile
-  int tile;    // of the sequence
-  int rows;    // (token, head) rows of the sequence
-  int start;   // its first row of q
-  int pos0;    // position of its first new token
-  int len;     // context length with the new tokens
-};
-
 // New tokens of sequence b: clamped to what q holds and the context has
 // (anything else is recorded and left out).
 ELSAA_DEV int new_tokens(const AttendArgs& a, int b, int* start, int* len, bool lead) {
@@ -59,37 +44,6 @@ ELSAA_DEV int new_tokens(const AttendArgs& a, int b, int* start, int* len, bool 
   if (ok) return s1 - s0;
   if (lead) raise_error(a.err, ERR_CHECK);
   return 0;
-}
-
-// Tile `t` of the whole batch, by one warp: sequences in order, each with
-// ceil(tokens g / size) tiles.
-ELSAA_DEV PagedTile find_paged_tile(const AttendArgs& a, int t, int size) {
-  const int lane = threadIdx.x & 31;
-  PagedTile f{-1, 0, 0, 0, 0, 0};
-  for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-    int start = 0, len = 0, n = 0;
-    if (b0 + lane < a.seqs) n = new_tokens(a, b0 + lane, &start, &len, true);
-    const int rows = n * a.g, tiles = (rows + size - 1) / size;
-    int upto = tiles;   // inclusive sum over the lanes
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, t < upto);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      f.seq = b0 + w;
-      f.tile = t - __shfl_sync(0xffffffffu, upto - tiles, w);
-      f.rows = __shfl_sync(0xffffffffu, rows, w);
-      f.start = __shfl_sync(0xffffffffu, start, w);
-      f.len = __shfl_sync(0xffffffffu, len, w);
-      f.pos0 = f.len - __shfl_sync(0xffffffffu, n, w);
-      return f;
-    }
-    t -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return f;
 }
 
 // The page of token j of sequence b; -1 (recorded) where the entry is no page.

@@ -21,7 +21,7 @@ struct Strides {
 // Head of every workspace, zeroed once by the caller: the error word, and the
 // arrival counters of work cut between CTAs (which the calls leave at zero).
 constexpr size_t kHeadBytes = 8192;
-constexpr size_t kCounters = 256;   // byte offset of the counters
+constexpr size_t kCounters = 256;   // byte offset of the counters (at most 1984)
 
 // ---- norm and rotation -------------------------------------------------------
 
@@ -73,7 +73,7 @@ struct AttendArgs {
   int sinks;
   float scale;
   uint32_t* err;
-  uint32_t* counters;         // [CTAs][8 warps]
+  uint32_t* counters;         // [CTAs][8 warps], or [CTAs]
   float* delta;               // [B, H, N]: rowsum(y dy) (backward)
   // pages
   const int32_t *page_table, *starts;
@@ -86,6 +86,8 @@ cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
+// Workspace bytes of launch_paged_simt's partial rows.
+size_t paged_simt_scratch_bytes(int d, int64_t rows, int seqs, int g);
 
 // tcgen05 kernels: bf16, d = 64 or 128.
 bool attend_tc_supported(int d, bool bf16);

@@ -280,7 +280,11 @@ elsaa_status elsaa_paged_validate(const elsaa_paged_params* p) { return check(p)
 
 size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p) {
   if (check(p) != ELSAA_OK) return 0;
-  return kHeadBytes + paged_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->rows, p->H / p->Hkv);
+  const bool bf16 = p->dtype == ELSAA_BF16;
+  const int g = p->H / p->Hkv;
+  return kHeadBytes + (attend_tc_supported(p->d, bf16)
+                           ? paged_scratch_bytes(p->d, bf16, p->rows, g)
+                           : paged_simt_scratch_bytes(p->d, p->rows, p->seqs, g));
 }
 
 static bool page_strides_of(const elsaa_paged_params* p, const int64_t* given, Strides* kp,

@@ -1,18 +1,23 @@
-// Causal attention over a sliding window with sinks, and over a paged cache,
-// on CUDA cores: every type and head dim (fp32 data keep fp32 products, which
-// the tensor cores do not have).
+// Causal attention over a sliding window with sinks, and over a paged cache, on
+// CUDA cores: every type and head dim (fp32 data keep fp32 products, which the
+// tensor cores do not have).
 //
 // Query at position i sees the keys j <= i with i - j < window or j < sinks.
 // y_i = sum_j p_ij v_j, p = exp(scale q k - lse).  Backward, D_i = y_i . dy_i:
 //   dS = p (dy v - D),  dq = scale dS k,  dk = scale dS^T q,  dv = p^T dy.
 //
-// Tiles of 64 query rows against 64-key blocks in shared memory (fp32), a
-// 16 x 16 thread grid with a 4 x 4 score tile and 4 x D / 16 output values each;
-// one pass over the keys with the running maximum and sum.  Only the blocks
-// that some row of the tile sees are visited: the sinks' and the window's.
-// Bound: fp32 FMA issue (the products); the backward runs one kernel for dq
-// (query tiles) and one for dk and dv (key tiles, over all query heads of the
-// group), so every output has one writer and no atomics.
+// Tiles of R rows (64, or 16 where 64 would leave most of the card idle) against
+// 64-row blocks in shared memory (fp32), 256 threads as 16 x 16 with an R / 16 x 4
+// score tile and R / 16 x D / 16 output values each; one pass over the keys with the
+// running maximum and sum.  Only the blocks that some row of the tile sees are
+// visited: the sinks' and the window's.  The backward runs one kernel for dq (query
+// tiles) and one for dk and dv (key tiles, over all query heads of the group): every
+// output has one writer and no atomics.  Paged work is one list of (row tile, key
+// head, key block) units cut into equal runs, one per CTA; an item cut between CTAs
+// leaves unnormalised partial rows, which the last CTA to get there adds up in the
+// CTAs' order.
+// Bound: the fp32 products (FMA pipe) and the shared-memory reads that feed them
+// (a 4 x 4 score tile reads 8 vectors for 64 FMA a thread).
 #include <math.h>
 
 #include "attend.cuh"
@@ -23,74 +28,101 @@
 namespace elsaa {
 namespace {
 
-constexpr int kTile = 64;
+constexpr int kBlk = 64;
 constexpr int kThreads = 256;
-constexpr int kPs = kTile + 4;   // pitch of a 64 x 64 score tile
+constexpr int kPs = kBlk + 4;    // pitch of a score tile's rows
+constexpr int kRuns = 296;       // CTAs of a paged call (2 x 148)
+constexpr int kMinUnits = 2;     // a run shorter than this is not worth a CTA
 
 template <int D>
 constexpr int pitch() { return D + 4; }
 
-// 64 rows x D of fp32 in shared memory from row pointers (null: zeros).
-template <typename T, int D, typename F>
+ELSAA_DEV float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+ELSAA_DEV float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                     __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+
+// `rows` rows x D of fp32 in shared memory from row pointers (null: zeros).
+template <typename T, int D, int ROWS, typename F>
 ELSAA_DEV void load_tile(float* dst, F&& row_ptr) {
-  constexpr int PER = D / 4;   // 4 values a step
-  for (int i = threadIdx.x; i < kTile * PER; i += kThreads) {
+  constexpr int PER = D / 4, STEPS = ROWS * PER / kThreads;   // 4 values a step
+  static_assert(ROWS * PER % kThreads == 0 || ROWS * PER < kThreads, "whole steps");
+  auto step = [&](int i) {
     const int r = i / PER, c = (i % PER) * 4;
     const T* p = row_ptr(r);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p != nullptr) x = make_float4(to_f32(p[c]), to_f32(p[c + 1]), to_f32(p[c + 2]), to_f32(p[c + 3]));
-    *reinterpret_cast<float4*>(dst + r * pitch<D>() + c) = x;
+    *reinterpret_cast<float4*>(dst + r * pitch<D>() + c) = p ? load4(p + c) : make_float4(0, 0, 0, 0);
+  };
+  if constexpr (STEPS == 0) {
+    if (threadIdx.x < ROWS * PER) step(threadIdx.x);
+  } else {
+#pragma unroll 8
+    for (int s = 0; s < STEPS; ++s) step(threadIdx.x + s * kThreads);
   }
 }
 
-// s[a][c] = A[4 ty + a] . B[tx + 16 c] over D
-template <int D>
-ELSAA_DEV void scores(const float* A, const float* B, float s[4][4]) {
+// s[a][c] = A[RT ty + a] . B[tx + 16 c] over D
+template <int D, int RT>
+ELSAA_DEV void scores(const float* A, const float* B, float s[RT][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
 #pragma unroll 4
   for (int x = 0; x < D; x += 4) {
-    float4 u[4], w[4];
+    float4 u[RT], w[4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) u[a] = *reinterpret_cast<const float4*>(A + (4 * ty + a) * pitch<D>() + x);
+    for (int a = 0; a < RT; ++a) u[a] = load4(A + (RT * ty + a) * pitch<D>() + x);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * pitch<D>() + x);
+    for (int c = 0; c < 4; ++c) w[c] = load4(B + (tx + 16 * c) * pitch<D>() + x);
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < RT; ++a)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         s[a][c] += u[a].x * w[c].x + u[a].y * w[c].y + u[a].z * w[c].z + u[a].w * w[c].w;
   }
 }
 
-// The output columns of a thread: CW consecutive ones from col(c).
+// The output columns of a thread: R runs of W consecutive ones.
 template <int D>
 struct Cols {
-  static constexpr int W = D >= 64 ? 4 : 2;      // width of a run
-  static constexpr int R = D / 16 / W;           // runs
+  static constexpr int W = D >= 64 ? 4 : 2;
+  static constexpr int R = D / 16 / W;
   ELSAA_DEV static int at(int r) { return (threadIdx.x & 15) * W + r * 64; }
 };
 
-// o[a][] += sum_j P[4 ty + a][j] X[j][] over 64 j (P pitch kPs)
-template <int D>
-ELSAA_DEV void accumulate(const float* P, const float* X, float o[4][D / 16]) {
+// o[a][] += sum_j P[RT ty + a][j] X[j][] over 64 j (P pitch kPs)
+template <int D, int RT>
+ELSAA_DEV void accumulate(const float* P, const float* X, float o[RT][D / 16]) {
   using C = Cols<D>;
   const int ty = threadIdx.x >> 4;
 #pragma unroll 4
-  for (int j = 0; j < kTile; ++j) {
-    float p[4];
+  for (int j = 0; j < kBlk; j += 4) {
+    float p[RT][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) p[a] = P[(4 * ty + a) * kPs + j];
+    for (int a = 0; a < RT; ++a) {
+      const float4 v = load4(P + (RT * ty + a) * kPs + j);
+      p[a][0] = v.x, p[a][1] = v.y, p[a][2] = v.z, p[a][3] = v.w;
+    }
 #pragma unroll
-    for (int r = 0; r < C::R; ++r)
+    for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-      for (int e = 0; e < C::W; ++e) {
-        const float x = X[j * pitch<D>() + C::at(r) + e];
+      for (int r = 0; r < C::R; ++r) {
+        const float* x = X + (j + jj) * pitch<D>() + C::at(r);
+        float v[4];
+        if (C::W == 4) {
+          const float4 u = load4(x);
+          v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(x);
+          v[0] = u.x, v[1] = u.y;
+        }
 #pragma unroll
-        for (int a = 0; a < 4; ++a) o[a][r * C::W + e] += p[a] * x;
+        for (int e = 0; e < C::W; ++e)
+#pragma unroll
+          for (int a = 0; a < RT; ++a) o[a][r * C::W + e] += p[a][jj] * v[e];
       }
   }
 }
@@ -115,105 +147,42 @@ ELSAA_DEV float row_sum16(float v) {
   return v;
 }
 
-// ---- forward -------------------------------------------------------------------
-
-// PAGED: a tile's rows are (token, head of the group) pairs, head fastest;
-// else 64 tokens of one head.
-template <typename T, int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads)
-attend_simt_kernel(const AttendArgs a, int tiles) {
-  extern __shared__ __align__(16) float sm[];
-  float* Qs = sm;
-  float* Ks = Qs + kTile * pitch<D>();
-  float* Vs = Ks + kTile * pitch<D>();
-  float* Ps = Vs + kTile * pitch<D>();
-  __shared__ PagedTile found;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int b, h, hk, r0, len, pos0, rows;   // rows of the tile's (batch, head) or (sequence, key head)
-  if (PAGED) {
-    hk = blockIdx.x / tiles;
-    if (threadIdx.x < 32) {
-      const PagedTile t = find_paged_tile(a, blockIdx.x % tiles, kTile);
-      if (threadIdx.x == 0) found = t;
+// The running softmax of a thread's rows (replicated over the 16 threads of a row).
+template <int D, int RT>
+struct Rows {
+  float o[RT][D / 16], m[RT], l[RT];
+  ELSAA_DEV void clear() {
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      m[x] = -INFINITY, l[x] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[x][c] = 0.f;
     }
-    __syncthreads();
-    if (found.seq < 0) return;
-    b = found.seq;
-    r0 = found.tile * kTile;
-    rows = found.rows;
-    pos0 = found.pos0;
-    len = found.len;
-    h = 0;
-  } else {
-    const int bh = blockIdx.x / tiles;
-    b = bh / a.H;
-    h = bh % a.H;
-    hk = h / a.g;
-    r0 = (tiles - 1 - blockIdx.x % tiles) * kTile;   // the longest rows first
-    rows = a.N;
-    pos0 = 0;
-    len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
   }
-  const int g = PAGED ? a.g : 1;
-  auto token_of = [&](int r) { return (r0 + r) / g; };
-  auto q_off = [&](int r, const Strides& s) -> int64_t {
-    if (PAGED) return (int64_t)(found.start + token_of(r)) * s.n + (int64_t)(hk * g + (r0 + r) % g) * s.h;
-    return (int64_t)b * s.b + (int64_t)h * s.h + (int64_t)(r0 + r) * s.n;
-  };
-  auto key_ptr = [&](const void* base, const Strides& s, int j) -> const T* {
-    if (j >= len) return nullptr;
-    const T* p = static_cast<const T*>(base);
-    if (PAGED) {
-      const int page = page_of(a, b, j);
-      if (page < 0) return nullptr;
-      return p + (int64_t)page * s.b + (int64_t)hk * s.h + (int64_t)(j % a.page_size) * s.n;
-    }
-    return p + (int64_t)b * s.b + (int64_t)hk * s.h + (int64_t)j * s.n;
-  };
-  load_tile<T, D>(Qs, [&](int r) -> const T* {
-    return r0 + r < rows ? static_cast<const T*>(a.q) + q_off(r, a.sq) : nullptr;
-  });
-  // positions of the tile's first and last row
-  const int p_lo = pos0 + token_of(0), p_hi = min(len - 1, pos0 + token_of(min(kTile, rows - r0) - 1));
-  const KeyBlocks kb = key_blocks(max(p_lo, 0), p_hi, a.window, a.sinks, kTile);
-  float o[4][D / 16], m[4], l[4];
+  // one block of keys j0 .. j0 + 63; pos[x]: the row's position, -1 where it has none
+  ELSAA_DEV void block(const float* Qs, const float* Ks, const float* Vs, float* Ps, int j0,
+                       const int* pos, const AttendArgs& a) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float s[RT][4];
+    scores<D, RT>(Qs, Ks, s);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    m[x] = -INFINITY, l[x] = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[x][c] = 0.f;
-  }
-  for (int n = 0; n < kb.count(); ++n) {
-    const int j0 = kb.block(n) * kTile;
-    // a page entry that no row of the tile sees (holes between sinks and window) is not read
-    auto needed = [&](int j) { return j < a.sinks || (int64_t)j > (int64_t)p_lo - a.window; };
-    __syncthreads();
-    load_tile<T, D>(Ks, [&](int r) { return needed(j0 + r) ? key_ptr(a.k, a.sk, j0 + r) : nullptr; });
-    load_tile<T, D>(Vs, [&](int r) { return needed(j0 + r) ? key_ptr(a.v, a.sv, j0 + r) : nullptr; });
-    __syncthreads();
-    float s[4][4];
-    scores<D>(Qs, Ks, s);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int r = 4 * ty + x;
-      const int pos = pos0 + token_of(r);
-      const bool live = r0 + r < rows && pos < len;
+    for (int x = 0; x < RT; ++x) {
       float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int j = j0 + tx + 16 * c;
-        s[x][c] = live && sees(pos, j, a.window, a.sinks) ? s[x][c] * a.scale : -INFINITY;
+        s[x][c] = sees(pos[x], j, a.window, a.sinks) ? s[x][c] * a.scale : -INFINITY;
         top = fmaxf(top, s[x][c]);
       }
       top = fmaxf(m[x], row_max16(top));
       const float base = top == -INFINITY ? 0.f : top;
-      const float f = __expf(m[x] - base);
+      const float f = expf(m[x] - base);
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float p = expf(s[x][c] - base);
         sum += p;
-        Ps[r * kPs + tx + 16 * c] = p;
+        Ps[(RT * ty + x) * kPs + tx + 16 * c] = p;
       }
       l[x] = l[x] * f + row_sum16(sum);
       m[x] = top;
@@ -221,22 +190,261 @@ attend_simt_kernel(const AttendArgs a, int tiles) {
       for (int c = 0; c < D / 16; ++c) o[x][c] *= f;
     }
     __syncwarp();   // a row of P is written and read by the same half warp
-    accumulate<D>(Ps, Vs, o);
+    accumulate<D, RT>(Ps, Vs, o);
+  }
+};
+
+// ---- window forward --------------------------------------------------------------
+
+ELSAA_DEV int length_of(const AttendArgs& a, int b) {
+  return a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads)
+window_fwd_simt_kernel(const AttendArgs a, int tiles) {
+  constexpr int RT = ROWS / 16;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + ROWS * pitch<D>();
+  float* Vs = Ks + kBlk * pitch<D>();
+  float* Ps = Vs + kBlk * pitch<D>();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int bh = blockIdx.x / tiles, b = bh / a.H, h = bh % a.H, hk = h / a.g;
+  const int r0 = (tiles - 1 - (int)(blockIdx.x % tiles)) * ROWS;   // the longest rows first
+  const int len = length_of(a, b);
+  auto row = [&](const void* base, const Strides& s, int head, int n) -> const T* {
+    return n < len ? static_cast<const T*>(base) + b * s.b + head * s.h + n * s.n : nullptr;
+  };
+  load_tile<T, D, ROWS>(Qs, [&](int r) { return row(a.q, a.sq, h, r0 + r); });
+  const KeyBlocks kb = key_blocks(r0, min(len, r0 + ROWS) - 1, a.window, a.sinks, kBlk);
+  Rows<D, RT> st;
+  st.clear();
+  int pos[RT];
+#pragma unroll
+  for (int x = 0; x < RT; ++x) pos[x] = r0 + RT * ty + x < len ? r0 + RT * ty + x : -1;
+  for (int n = 0; n < kb.count(); ++n) {
+    const int j0 = kb.block(n) * kBlk;
+    __syncthreads();
+    load_tile<T, D, kBlk>(Ks, [&](int r) { return row(a.k, a.sk, hk, j0 + r); });
+    load_tile<T, D, kBlk>(Vs, [&](int r) { return row(a.v, a.sv, hk, j0 + r); });
+    __syncthreads();
+    st.block(Qs, Ks, Vs, Ps, j0, pos, a);
   }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int r = 4 * ty + x;
-    if (r0 + r >= rows) continue;
-    const float inv = l[x] > 0.f ? 1.0f / l[x] : 0.f;
+  for (int x = 0; x < RT; ++x) {
+    const int n = r0 + RT * ty + x;
+    if (n >= a.N) continue;
+    const float inv = st.l[x] > 0.f ? 1.0f / st.l[x] : 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[x][c] *= inv;
-    store_cols<T, D>(static_cast<T*>(a.y) + q_off(r, a.sy), o[x]);
-    if (!PAGED && tx == 0)
-      a.lse[((int64_t)b * a.H + h) * a.N + r0 + r] = l[x] > 0.f ? m[x] + logf(l[x]) : -INFINITY;
+    for (int c = 0; c < D / 16; ++c) st.o[x][c] *= inv;
+    store_cols<T, D>(static_cast<T*>(a.y) + b * a.sy.b + h * a.sy.h + n * a.sy.n, st.o[x]);
+    if (tx == 0)
+      a.lse[(int64_t)bh * a.N + n] = st.l[x] > 0.f ? st.m[x] + logf(st.l[x]) : -INFINITY;
   }
 }
 
-// ---- backward ------------------------------------------------------------------
+// ---- paged -----------------------------------------------------------------------
+
+// Row tiles of sequence b hold ROWS / g tokens.
+struct PagedItem {
+  int b, tile, hk, start, tokens, len;
+  int p_lo, p_hi;          // positions of the tile's rows
+  KeyBlocks kb;
+};
+ELSAA_DEV PagedItem paged_item(const AttendArgs& a, int tt, int b, int tile, int hk, int start,
+                               int tokens, int len) {
+  PagedItem it{b, tile, hk, start, tokens, len, 0, 0, {}};
+  it.p_lo = len - tokens + tile * tt;
+  it.p_hi = len - tokens + min(tokens, (tile + 1) * tt) - 1;
+  it.kb = key_blocks(it.p_lo, it.p_hi, a.window, a.sinks, kBlk);
+  return it;
+}
+ELSAA_DEV int64_t seq_units(const AttendArgs& a, int tt, int b, bool lead) {
+  int start, len;
+  const int n = new_tokens(a, b, &start, &len, lead);
+  int64_t u = 0;
+  for (int t = 0; t * tt < n; ++t) u += paged_item(a, tt, b, t, 0, start, n, len).kb.count();
+  return u * a.Hkv;
+}
+
+struct Run {
+  int b, tile, hk, off, units;   // where it begins, and its length
+  int64_t per;                   // units of a run
+};
+// The run of CTA `cta` of `ctas`, by one warp.
+ELSAA_DEV Run find_run(const AttendArgs& a, int tt, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  for (int b = lane; b < a.seqs; b += 32) total += seq_units(a, tt, b, cta == 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t per = max((total + ctas - 1) / ctas, (int64_t)kMinUnits);
+  Run c{0, 0, 0, 0, 0, per};
+  int64_t w = per * cta;
+  if (w >= total) return c;
+  c.units = (int)min(per, total - w);
+  for (int b0 = 0; b0 < a.seqs; b0 += 32) {
+    const int64_t mine = b0 + lane < a.seqs ? seq_units(a, tt, b0 + lane, false) : 0;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, w < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      int64_t rest = w - __shfl_sync(0xffffffffu, upto - mine, l);
+      c.b = b0 + l;
+      int start, len;
+      const int n = new_tokens(a, c.b, &start, &len, false);
+      for (; c.tile * tt < n; ++c.tile) {
+        const int64_t blk = paged_item(a, tt, c.b, c.tile, 0, start, n, len).kb.count();
+        if (rest < blk * a.Hkv) {
+          c.hk = (int)(rest / blk);
+          c.off = (int)(rest % blk);
+          break;
+        }
+        rest -= blk * a.Hkv;
+      }
+      return c;
+    }
+    w -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return c;
+}
+
+// Partial rows: [slot][row][D] and (m, l) [slot][row], slot = 2 cta + (not the run's first item).
+template <int ROWS>
+ELSAA_DEV float* partial_o(const AttendArgs& a, int d, int slot, int row) {
+  return reinterpret_cast<float*>(a.scratch) + ((int64_t)slot * ROWS + row) * d;
+}
+template <int ROWS>
+ELSAA_DEV float2* partial_ml(const AttendArgs& a, int d, int slot, int row) {
+  return reinterpret_cast<float2*>(partial_o<ROWS>(a, d, 2 * kRuns, 0)) + (int64_t)slot * ROWS + row;
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads)
+paged_simt_kernel(const AttendArgs a) {
+  constexpr int RT = ROWS / 16;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + ROWS * pitch<D>();
+  float* Vs = Ks + kBlk * pitch<D>();
+  float* Ps = Vs + kBlk * pitch<D>();
+  __shared__ Run run;
+  __shared__ int pages[kBlk], last;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = a.g, tt = ROWS / g;
+  if (threadIdx.x < 32) {
+    const Run c = find_run(a, tt, blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0) run = c;
+  }
+  __syncthreads();
+  int b = run.b, tile = run.tile, hk = run.hk, off = run.off, left = run.units, start = 0, len = 0, tokens = 0;
+  if (left > 0) tokens = new_tokens(a, b, &start, &len, false);
+  int64_t at = run.per * blockIdx.x;   // the next unit
+  for (int order = 0; left > 0; ++order) {
+    while (tile * tt >= tokens) {
+      if (++b >= a.seqs) return;       // (a later sequence holds the units left)
+      tile = hk = off = 0;
+      tokens = new_tokens(a, b, &start, &len, false);
+    }
+    const PagedItem it = paged_item(a, tt, b, tile, hk, start, tokens, len);
+    const int nblk = it.kb.count(), n0 = off, n1 = min(nblk, off + left);
+    // row r of the tile: token tile tt + r / g, head hk g + r % g
+    auto live = [&](int r) { return r / g < tt && tile * tt + r / g < tokens; };
+    auto at_row = [&](const Strides& s, int r) -> int64_t {
+      return (int64_t)(start + tile * tt + r / g) * s.n + (int64_t)(hk * g + r % g) * s.h;
+    };
+    __syncthreads();
+    load_tile<T, D, ROWS>(Qs, [&](int r) -> const T* {
+      return live(r) ? static_cast<const T*>(a.q) + at_row(a.sq, r) : nullptr;
+    });
+    Rows<D, RT> st;
+    st.clear();
+    int pos[RT];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) pos[x] = live(RT * ty + x) ? it.p_lo + (RT * ty + x) / g : -1;
+    for (int n = n0; n < n1; ++n) {
+      const int j0 = it.kb.block(n) * kBlk;
+      __syncthreads();
+      if (threadIdx.x < kBlk) {
+        // entries that no row of the tile sees are not looked up
+        const int j = j0 + threadIdx.x;
+        const bool need = j <= it.p_hi && (j < a.sinks || (int64_t)j > (int64_t)it.p_lo - a.window);
+        pages[threadIdx.x] = need ? page_of(a, b, j) : -1;
+      }
+      __syncthreads();
+      auto key = [&](const void* base, const Strides& s, int r) -> const T* {
+        return pages[r] >= 0 ? static_cast<const T*>(base) + (int64_t)pages[r] * s.b + (int64_t)hk * s.h +
+                                   (int64_t)((j0 + r) % a.page_size) * s.n
+                             : nullptr;
+      };
+      load_tile<T, D, kBlk>(Ks, [&](int r) { return key(a.k, a.sk, r); });
+      load_tile<T, D, kBlk>(Vs, [&](int r) { return key(a.v, a.sv, r); });
+      __syncthreads();
+      st.block(Qs, Ks, Vs, Ps, j0, pos, a);
+    }
+    const bool whole = n0 == 0 && n1 == nblk;
+    const int slot = (int)blockIdx.x * 2 + (order > 0 ? 1 : 0);
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      const int r = RT * ty + x;
+      if (!live(r)) continue;
+      if (whole) {
+        const float inv = st.l[x] > 0.f ? 1.0f / st.l[x] : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) st.o[x][c] *= inv;
+        store_cols<T, D>(static_cast<T*>(a.y) + at_row(a.sy, r), st.o[x]);
+      } else {
+        store_cols<float, D>(partial_o<ROWS>(a, D, slot, r), st.o[x]);
+        if (tx == 0) *partial_ml<ROWS>(a, D, slot, r) = make_float2(st.m[x], st.l[x]);
+      }
+    }
+    if (!whole) {
+      const int64_t begin = at - off;
+      const int cta0 = (int)(begin / run.per), cta1 = (int)((begin + nblk - 1) / run.per);
+      const int slot0 = begin == cta0 * run.per ? 0 : 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        last = atomicAdd(a.counters + cta0, 1u) == (uint32_t)(cta1 - cta0) ? 1 : 0;
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        for (int x = threadIdx.x; x < ROWS * (D / 4); x += kThreads) {
+          const int r = x / (D / 4), c = x % (D / 4) * 4;
+          if (!live(r)) break;   // (rows end with the tokens)
+          auto slot_of = [&](int i) { return 2 * i + (i == cta0 ? slot0 : 0); };
+          float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int i = cta0; i <= cta1; ++i) m = fmaxf(m, __ldcg(partial_ml<ROWS>(a, D, slot_of(i), r)).x);
+#pragma unroll 4
+          for (int i = cta0; i <= cta1; ++i) {
+            const float2 ml = __ldcg(partial_ml<ROWS>(a, D, slot_of(i), r));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(partial_o<ROWS>(a, D, slot_of(i), r) + c));
+            const float w = ml.x > -INFINITY ? expf(ml.x - m) : 0.f;
+            l += ml.y * w;
+            o[0] += v.x * w, o[1] += v.y * w, o[2] += v.z * w, o[3] += v.w * w;
+          }
+          const float inv = l > 0.f ? 1.0f / l : 0.f;
+          T* y = static_cast<T*>(a.y) + at_row(a.sy, r) + c;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(o[e] * inv);
+        }
+        if (threadIdx.x == 0) a.counters[cta0] = 0;
+      }
+    }
+    left -= n1 - n0;
+    at += n1 - n0;
+    off = 0;
+    if (++hk == a.Hkv) hk = 0, ++tile;
+  }
+}
+
+// ---- backward --------------------------------------------------------------------
 
 // delta = rowsum(y dy), one warp a row (rows behind a length are not read).
 template <typename T>
@@ -246,7 +454,7 @@ __global__ void __launch_bounds__(kThreads) window_delta_kernel(const AttendArgs
   if (row >= (int64_t)a.B * a.H * a.N) return;
   const int n = (int)(row % a.N), h = (int)(row / a.N % a.H), b = (int)(row / a.N / a.H);
   float s = 0.f;
-  if (!a.lengths || n < a.lengths[b]) {
+  if (n < length_of(a, b)) {
     const T* y = static_cast<const T*>(a.y) + b * a.sy.b + h * a.sy.h + n * a.sy.n;
     const T* g = static_cast<const T*>(a.dy) + b * a.sdy.b + h * a.sdy.h + n * a.sdy.n;
     for (int c = lane; c < a.d; c += 32) s += to_f32(y[c]) * to_f32(g[c]);
@@ -255,179 +463,204 @@ __global__ void __launch_bounds__(kThreads) window_delta_kernel(const AttendArgs
   if (lane == 0) a.delta[row] = s;
 }
 
-template <typename T, int D>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const AttendArgs a, int tiles) {
+  constexpr int RT = ROWS / 16;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
-  float* Gs = Qs + kTile * pitch<D>();
-  float* Ks = Gs + kTile * pitch<D>();
-  float* Vs = Ks + kTile * pitch<D>();
-  float* Ps = Vs + kTile * pitch<D>();
+  float* Gs = Qs + ROWS * pitch<D>();
+  float* Ks = Gs + ROWS * pitch<D>();
+  float* Vs = Ks + kBlk * pitch<D>();
+  float* Ps = Vs + kBlk * pitch<D>();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int bh = blockIdx.x / tiles, b = bh / a.H, h = bh % a.H, hk = h / a.g;
-  const int r0 = (tiles - 1 - blockIdx.x % tiles) * kTile;
-  const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+  const int r0 = (tiles - 1 - (int)(blockIdx.x % tiles)) * ROWS;
+  const int len = length_of(a, b);
   auto row = [&](const void* base, const Strides& s, int head, int n) -> const T* {
     return n < len ? static_cast<const T*>(base) + b * s.b + head * s.h + n * s.n : nullptr;
   };
-  load_tile<T, D>(Qs, [&](int r) { return row(a.q, a.sq, h, r0 + r); });
-  load_tile<T, D>(Gs, [&](int r) { return row(a.dy, a.sdy, h, r0 + r); });
-  float lse[4], del[4], o[4][D / 16];
+  load_tile<T, D, ROWS>(Qs, [&](int r) { return row(a.q, a.sq, h, r0 + r); });
+  load_tile<T, D, ROWS>(Gs, [&](int r) { return row(a.dy, a.sdy, h, r0 + r); });
+  float lse[RT], del[RT], o[RT][D / 16];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int n = r0 + 4 * ty + x;
+  for (int x = 0; x < RT; ++x) {
+    const int n = r0 + RT * ty + x;
     const bool live = n < len;
     lse[x] = live ? a.lse[(int64_t)bh * a.N + n] : 0.f;
     del[x] = live ? a.delta[(int64_t)bh * a.N + n] : 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[x][c] = 0.f;
   }
-  const KeyBlocks kb = key_blocks(r0, min(len, r0 + kTile) - 1, a.window, a.sinks, kTile);
+  const KeyBlocks kb = key_blocks(r0, min(len, r0 + ROWS) - 1, a.window, a.sinks, kBlk);
   for (int n = 0; n < kb.count(); ++n) {
-    const int j0 = kb.block(n) * kTile;
+    const int j0 = kb.block(n) * kBlk;
     __syncthreads();
-    load_tile<T, D>(Ks, [&](int r) { return row(a.k, a.sk, hk, j0 + r); });
-    load_tile<T, D>(Vs, [&](int r) { return row(a.v, a.sv, hk, j0 + r); });
+    load_tile<T, D, kBlk>(Ks, [&](int r) { return row(a.k, a.sk, hk, j0 + r); });
+    load_tile<T, D, kBlk>(Vs, [&](int r) { return row(a.v, a.sv, hk, j0 + r); });
     __syncthreads();
-    float s[4][4], t[4][4];
-    scores<D>(Qs, Ks, s);
-    scores<D>(Gs, Vs, t);
+    float s[RT][4], t[RT][4];
+    scores<D, RT>(Qs, Ks, s);
+    scores<D, RT>(Gs, Vs, t);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int pos = r0 + 4 * ty + x;
+    for (int x = 0; x < RT; ++x) {
+      const int pos = r0 + RT * ty + x;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int j = j0 + tx + 16 * c;
         const bool see = pos < len && sees(pos, j, a.window, a.sinks);
-        Ps[(4 * ty + x) * kPs + tx + 16 * c] =
+        Ps[(RT * ty + x) * kPs + tx + 16 * c] =
             see ? expf(s[x][c] * a.scale - lse[x]) * (t[x][c] - del[x]) * a.scale : 0.f;
       }
     }
     __syncwarp();
-    accumulate<D>(Ps, Ks, o);
+    accumulate<D, RT>(Ps, Ks, o);
   }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int n = r0 + 4 * ty + x;
+  for (int x = 0; x < RT; ++x) {
+    const int n = r0 + RT * ty + x;
     if (n < a.N) store_cols<T, D>(static_cast<T*>(a.dq) + b * a.sdq.b + h * a.sdq.h + n * a.sdq.n, o[x]);
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) window_dkv_simt_kernel(const AttendArgs a, int tiles) {
+  constexpr int RT = ROWS / 16;
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
-  float* Vs = Ks + kTile * pitch<D>();
-  float* Qs = Vs + kTile * pitch<D>();
-  float* Gs = Qs + kTile * pitch<D>();
-  float* Ps = Gs + kTile * pitch<D>();   // [key][query]
-  float* Ds = Ps + kTile * kPs;
+  float* Vs = Ks + ROWS * pitch<D>();
+  float* Qs = Vs + ROWS * pitch<D>();
+  float* Gs = Qs + kBlk * pitch<D>();
+  float* Ps = Gs + kBlk * pitch<D>();   // [key][query]
+  float* Ds = Ps + ROWS * kPs;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int bk = blockIdx.x / tiles, b = bk / a.Hkv, hk = bk % a.Hkv;
-  const int j0 = (int)(blockIdx.x % tiles) * kTile;   // the sinks' tile, the longest, first
-  const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+  const int j0 = (int)(blockIdx.x % tiles) * ROWS;   // the sinks' tile, the longest, first
+  const int len = length_of(a, b);
   auto row = [&](const void* base, const Strides& s, int head, int n) -> const T* {
     return n < len ? static_cast<const T*>(base) + b * s.b + head * s.h + n * s.n : nullptr;
   };
-  load_tile<T, D>(Ks, [&](int r) { return row(a.k, a.sk, hk, j0 + r); });
-  load_tile<T, D>(Vs, [&](int r) { return row(a.v, a.sv, hk, j0 + r); });
-  float ok[4][D / 16], ov[4][D / 16];
+  load_tile<T, D, ROWS>(Ks, [&](int r) { return row(a.k, a.sk, hk, j0 + r); });
+  load_tile<T, D, ROWS>(Vs, [&](int r) { return row(a.v, a.sv, hk, j0 + r); });
+  float ok[RT][D / 16], ov[RT][D / 16];
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
+  for (int x = 0; x < RT; ++x)
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ok[x][c] = ov[x][c] = 0.f;
-  const int64_t last = j0 < a.sinks ? len : (int64_t)j0 + kTile - 1 + a.window;
-  const int i_end = (int)(last < len ? last : len);   // queries j0 .. i_end - 1 may see the tile
+  const int64_t reach = j0 < a.sinks ? len : (int64_t)j0 + ROWS - 1 + a.window;
+  const int i_end = (int)(reach < len ? reach : len);   // queries j0 .. i_end - 1 may see the tile
   for (int h = hk * a.g; h < (hk + 1) * a.g; ++h) {
     const int64_t rows = ((int64_t)b * a.H + h) * a.N;
-    for (int i0 = j0; i0 < i_end; i0 += kTile) {
+    for (int i0 = j0; i0 < i_end; i0 += kBlk) {
       __syncthreads();
-      load_tile<T, D>(Qs, [&](int r) { return row(a.q, a.sq, h, i0 + r); });
-      load_tile<T, D>(Gs, [&](int r) { return row(a.dy, a.sdy, h, i0 + r); });
+      load_tile<T, D, kBlk>(Qs, [&](int r) { return row(a.q, a.sq, h, i0 + r); });
+      load_tile<T, D, kBlk>(Gs, [&](int r) { return row(a.dy, a.sdy, h, i0 + r); });
       __syncthreads();
-      float s[4][4], t[4][4];
-      scores<D>(Ks, Qs, s);
-      scores<D>(Vs, Gs, t);
+      float s[RT][4], t[RT][4];
+      scores<D, RT>(Ks, Qs, s);
+      scores<D, RT>(Vs, Gs, t);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int i = i0 + tx + 16 * c;
         const float lse = i < len ? a.lse[rows + i] : 0.f, del = i < len ? a.delta[rows + i] : 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = j0 + 4 * ty + x;
+        for (int x = 0; x < RT; ++x) {
+          const int j = j0 + RT * ty + x;
           const bool see = i < len && sees(i, j, a.window, a.sinks);
           const float p = see ? expf(s[x][c] * a.scale - lse) : 0.f;
-          Ps[(4 * ty + x) * kPs + tx + 16 * c] = p;
-          Ds[(4 * ty + x) * kPs + tx + 16 * c] = see ? p * (t[x][c] - del) * a.scale : 0.f;
+          Ps[(RT * ty + x) * kPs + tx + 16 * c] = p;
+          Ds[(RT * ty + x) * kPs + tx + 16 * c] = see ? p * (t[x][c] - del) * a.scale : 0.f;
         }
       }
       __syncwarp();
-      accumulate<D>(Ps, Gs, ov);
-      accumulate<D>(Ds, Qs, ok);
+      accumulate<D, RT>(Ps, Gs, ov);
+      accumulate<D, RT>(Ds, Qs, ok);
     }
   }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int n = j0 + 4 * ty + x;
+  for (int x = 0; x < RT; ++x) {
+    const int n = j0 + RT * ty + x;
     if (n >= a.N) continue;
     store_cols<T, D>(static_cast<T*>(a.dk) + b * a.sdk.b + hk * a.sdk.h + n * a.sdk.n, ok[x]);
     store_cols<T, D>(static_cast<T*>(a.dv) + b * a.sdv.b + hk * a.sdv.h + n * a.sdv.n, ov[x]);
   }
 }
 
-// ---- launches ------------------------------------------------------------------
+// ---- launches --------------------------------------------------------------------
 
-template <typename K>
-cudaError_t run(K kernel, int64_t blocks, size_t smem, const AttendArgs& a, int tiles,
-                cudaStream_t s) {
+template <typename K, typename... A>
+cudaError_t run(K kernel, int64_t blocks, size_t smem, cudaStream_t s, A... args) {
   if (blocks <= 0 || blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, kThreads, smem, s>>>(a, tiles);
+  kernel<<<(unsigned)blocks, kThreads, smem, s>>>(args...);
   return cudaGetLastError();
 }
 
+// Bytes of `tiles` R-row tiles, `blocks` 64-row blocks and `scores` R x 64 score tiles.
 template <int D>
-constexpr size_t tile_bytes(int row_tiles, int score_tiles) {
-  return sizeof(float) * kTile * ((size_t)row_tiles * pitch<D>() + (size_t)score_tiles * kPs);
+constexpr size_t bytes(int R, int tiles, int blocks, int scores) {
+  return sizeof(float) * ((size_t)(tiles * R + blocks * kBlk) * pitch<D>() + (size_t)scores * R * kPs);
 }
 
-template <typename T, int D>
+// 16-row tiles where 64-row tiles would be fewer than the SMs: a tile of 16 does a
+// quarter of the work of one of 64 at half its efficiency.
+bool small_tiles(int64_t heads, int N) { return heads * ((N + 63) / 64) < 148; }
+
+template <typename T, int D, int R>
 cudaError_t forward(const AttendArgs& a, cudaStream_t s) {
-  const int tiles = (a.N + kTile - 1) / kTile;
-  return run(attend_simt_kernel<T, D, false>, (int64_t)a.B * a.H * tiles, tile_bytes<D>(3, 1), a,
-             tiles, s);
+  const int tiles = (a.N + R - 1) / R;
+  return run(window_fwd_simt_kernel<T, D, R>, (int64_t)a.B * a.H * tiles, bytes<D>(R, 1, 2, 1), s, a, tiles);
 }
-template <typename T, int D>
-cudaError_t backward(const AttendArgs& a, cudaStream_t s) {
-  const int tiles = (a.N + kTile - 1) / kTile;
-  const cudaError_t e = run(window_dq_simt_kernel<T, D>, (int64_t)a.B * a.H * tiles,
-                            tile_bytes<D>(4, 1), a, tiles, s);
-  if (e != cudaSuccess) return e;
-  return run(window_dkv_simt_kernel<T, D>, (int64_t)a.B * a.Hkv * tiles, tile_bytes<D>(4, 2), a,
-             tiles, s);
+template <typename T, int D, int R>
+cudaError_t dq(const AttendArgs& a, cudaStream_t s) {
+  const int tiles = (a.N + R - 1) / R;
+  return run(window_dq_simt_kernel<T, D, R>, (int64_t)a.B * a.H * tiles, bytes<D>(R, 2, 2, 1), s, a, tiles);
+}
+template <typename T, int D, int R>
+cudaError_t dkv(const AttendArgs& a, cudaStream_t s) {
+  const int tiles = (a.N + R - 1) / R;
+  return run(window_dkv_simt_kernel<T, D, R>, (int64_t)a.B * a.Hkv * tiles, bytes<D>(R, 2, 2, 2), s, a, tiles);
+}
+
+// Rows of a paged tile: 16 where a sequence's new rows fill no more (and the group fits).
+int paged_tile_rows(int64_t rows, int seqs, int g) {
+  return g <= 16 && (rows + seqs - 1) / seqs * g <= 16 ? 16 : 64;
 }
 template <typename T, int D>
 cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
-  const int64_t tiles = paged_tiles(a, kTile);
-  return run(attend_simt_kernel<T, D, true>, tiles * a.Hkv, tile_bytes<D>(3, 1), a, (int)tiles, s);
+  if (paged_tile_rows(a.rows, a.seqs, a.g) == 16)
+    return run(paged_simt_kernel<T, D, 16>, kRuns, bytes<D>(16, 1, 2, 1), s, a);
+  return run(paged_simt_kernel<T, D, 64>, kRuns, bytes<D>(64, 1, 2, 1), s, a);
 }
 
-template <int D>
+template <typename T, int D>
 struct Launch {
-  static cudaError_t fwd(const AttendArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? forward<__nv_bfloat16, D>(a, s) : forward<float, D>(a, s);
+  static cudaError_t fwd(const AttendArgs& a, cudaStream_t s) {
+    return small_tiles((int64_t)a.B * a.H, a.N) ? forward<T, D, 16>(a, s) : forward<T, D, 64>(a, s);
   }
-  static cudaError_t bwd(const AttendArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? backward<__nv_bfloat16, D>(a, s) : backward<float, D>(a, s);
+  static cudaError_t bwd(const AttendArgs& a, cudaStream_t s) {
+    const cudaError_t e = small_tiles((int64_t)a.B * a.H, a.N) ? dq<T, D, 16>(a, s) : dq<T, D, 64>(a, s);
+    if (e != cudaSuccess) return e;
+    return small_tiles((int64_t)a.B * a.Hkv, a.N) ? dkv<T, D, 16>(a, s) : dkv<T, D, 64>(a, s);
   }
-  static cudaError_t paged(const AttendArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? pages<__nv_bfloat16, D>(a, s) : pages<float, D>(a, s);
-  }
+  static cudaError_t paged(const AttendArgs& a, cudaStream_t s) { return pages<T, D>(a, s); }
 };
 
+// f<T, D> of the problem's type and head dim.
+#define ELSAA_BY_SHAPE(f)                                                                       \
+  (bf16 ? (a.d == 32   ? Launch<__nv_bfloat16, 32>::f(a, s)                                     \
+           : a.d == 64 ? Launch<__nv_bfloat16, 64>::f(a, s)                                     \
+                       : Launch<__nv_bfloat16, 128>::f(a, s))                                   \
+        : (a.d == 32   ? Launch<float, 32>::f(a, s)                                             \
+           : a.d == 64 ? Launch<float, 64>::f(a, s)                                             \
+                       : Launch<float, 128>::f(a, s)))
+
 }  // namespace
+
+size_t paged_simt_scratch_bytes(int d, int64_t rows, int seqs, int g) {
+  return (size_t)2 * kRuns * paged_tile_rows(rows, seqs, g) * (d + 2) * sizeof(float);
+}
 
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.H * a.N, warps = kThreads / 32;
@@ -440,16 +673,13 @@ cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s) 
 }
 
 cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s) {
-  return a.d == 32 ? Launch<32>::fwd(a, bf16, s)
-         : a.d == 64 ? Launch<64>::fwd(a, bf16, s) : Launch<128>::fwd(a, bf16, s);
+  return ELSAA_BY_SHAPE(fwd);
 }
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s) {
-  return a.d == 32 ? Launch<32>::bwd(a, bf16, s)
-         : a.d == 64 ? Launch<64>::bwd(a, bf16, s) : Launch<128>::bwd(a, bf16, s);
+  return ELSAA_BY_SHAPE(bwd);
 }
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s) {
-  return a.d == 32 ? Launch<32>::paged(a, bf16, s)
-         : a.d == 64 ? Launch<64>::paged(a, bf16, s) : Launch<128>::paged(a, bf16, s);
+  return ELSAA_BY_SHAPE(paged);
 }
 
 }  // namespace elsaa

@@ -149,6 +149,7 @@ WINDOW = [
     (1, 2, 1, 131, 64, "f32", 0, 0, (100,), True),
     (2, 3, 3, 190, 128, "f32", 1, 0, (65, 190), False),
     (1, 4, 4, 70, 128, "f32", 33, 70, None, False),
+    (4, 16, 8, 520, 32, "f32", 200, 3, (520, 0, 64, 65), False),
     (2, 4, 2, 150, 32, "bf16", 40, 2, (150, 64), False),
 ]
 
@@ -265,6 +266,10 @@ PAGED = [
     (4, 2, 64, "f32", 16, 0, 0, [(1, 300), (33, 90), (0, 10)]),
     (8, 1, 128, "f32", 48, 50, 3, [(2, 400), (1, 1)]),
     (2, 2, 32, "f32", 16, 1, 0, [(4, 60)]),
+    (12, 4, 128, "f32", 32, 0, 0, [(1, 3000), (1, 5)]),
+    (6, 1, 32, "bf16", 64, 0, 0, [(1, 2500)]),
+    (2, 2, 64, "f32", 16, 700, 5, [(100, 1500), (1, 1200)]),
+    (8, 4, 32, "f32", 16, 0, 0, [(1, 1 + 53 * b) for b in range(40)]),
     (8, 8, 64, "bf16", 128, 128, 0, [(1, 1 + 37 * b) for b in range(70)]),
 ]
 
