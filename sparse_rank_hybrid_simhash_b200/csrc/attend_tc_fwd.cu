@@ -941,8 +941,7 @@ cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
 
 bool attend_tc_supported(int d, bool bf16) { return bf16 && (d == 64 || d == 128); }
 
-size_t paged_scratch_bytes(int d, bool bf16, int64_t rows, int g) {
-  if (!attend_tc_supported(d, bf16)) return 0;
+size_t paged_scratch_bytes(int d, int64_t rows, int g) {
   return (size_t)kMaxCtas * 4 * slot_rows(rows, g) * (d + 2) * sizeof(float);
 }
 

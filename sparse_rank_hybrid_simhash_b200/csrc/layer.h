@@ -86,8 +86,6 @@ cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
-// Workspace bytes of launch_paged_simt's partial rows.
-size_t paged_simt_scratch_bytes(int d, int64_t rows, int seqs, int g);
 
 // tcgen05 kernels: bf16, d = 64 or 128.
 bool attend_tc_supported(int d, bool bf16);
@@ -98,7 +96,10 @@ cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
 // Workspace bytes of the window backward: row statistics, and partials of cut tiles.
 size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N);
 // Workspace bytes of launch_paged_tc's partial rows.
-size_t paged_scratch_bytes(int d, bool bf16, int64_t rows, int g);
+size_t paged_scratch_bytes(int d, int64_t rows, int g);
+// A few rows a sequence (decoding), bf16, d = 64 or 128.
+bool paged_decode_supported(int d, bool bf16, int64_t rows, int seqs, int g);
+cudaError_t launch_paged_decode(const AttendArgs& a, cudaStream_t s);
 
 // A 128-byte-swizzled bf16 tensor map of a [n3, n2, n1, d] tensor with the
 // given element strides (d contiguous) and box.

@@ -6,6 +6,7 @@
 
 #include "internal.h"
 #include "layer.h"
+#include "paged_runs.cuh"
 
 using namespace elsaa;
 
@@ -282,9 +283,10 @@ size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p) {
   if (check(p) != ELSAA_OK) return 0;
   const bool bf16 = p->dtype == ELSAA_BF16;
   const int g = p->H / p->Hkv;
-  return kHeadBytes + (attend_tc_supported(p->d, bf16)
-                           ? paged_scratch_bytes(p->d, bf16, p->rows, g)
-                           : paged_simt_scratch_bytes(p->d, p->rows, p->seqs, g));
+  // (the tensor-core kernel's, or the kernels' with 64-key blocks)
+  if (attend_tc_supported(p->d, bf16) && !paged_decode_supported(p->d, bf16, p->rows, p->seqs, g))
+    return kHeadBytes + paged_scratch_bytes(p->d, p->rows, g);
+  return kHeadBytes + paged_runs_bytes(p->d, paged_tile_rows(p->rows, p->seqs, g));
 }
 
 static bool page_strides_of(const elsaa_paged_params* p, const int64_t* given, Strides* kp,
@@ -385,6 +387,8 @@ elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
   a.pages = p->pages;
   a.table_width = p->table_width;
   const bool bf16 = p->dtype == ELSAA_BF16;
+  if (paged_decode_supported(p->d, bf16, p->rows, p->seqs, a.g))
+    return cuda_status(launch_paged_decode(a, (cudaStream_t)stream));
   return cuda_status(attend_tc_supported(p->d, bf16)
                          ? launch_paged_tc(a, (cudaStream_t)stream)
                          : launch_paged_simt(a, bf16, (cudaStream_t)stream));

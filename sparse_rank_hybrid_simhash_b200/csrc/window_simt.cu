@@ -21,6 +21,7 @@
 #include <math.h>
 
 #include "attend.cuh"
+#include "paged_runs.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "layer.h"
@@ -28,11 +29,8 @@
 namespace elsaa {
 namespace {
 
-constexpr int kBlk = 64;
 constexpr int kThreads = 256;
 constexpr int kPs = kBlk + 4;    // pitch of a score tile's rows
-constexpr int kRuns = 296;       // CTAs of a paged call (2 x 148)
-constexpr int kMinUnits = 2;     // a run shorter than this is not worth a CTA
 
 template <int D>
 constexpr int pitch() { return D + 4; }
@@ -246,85 +244,6 @@ window_fwd_simt_kernel(const AttendArgs a, int tiles) {
 
 // ---- paged -----------------------------------------------------------------------
 
-// Row tiles of sequence b hold ROWS / g tokens.
-struct PagedItem {
-  int b, tile, hk, start, tokens, len;
-  int p_lo, p_hi;          // positions of the tile's rows
-  KeyBlocks kb;
-};
-ELSAA_DEV PagedItem paged_item(const AttendArgs& a, int tt, int b, int tile, int hk, int start,
-                               int tokens, int len) {
-  PagedItem it{b, tile, hk, start, tokens, len, 0, 0, {}};
-  it.p_lo = len - tokens + tile * tt;
-  it.p_hi = len - tokens + min(tokens, (tile + 1) * tt) - 1;
-  it.kb = key_blocks(it.p_lo, it.p_hi, a.window, a.sinks, kBlk);
-  return it;
-}
-ELSAA_DEV int64_t seq_units(const AttendArgs& a, int tt, int b, bool lead) {
-  int start, len;
-  const int n = new_tokens(a, b, &start, &len, lead);
-  int64_t u = 0;
-  for (int t = 0; t * tt < n; ++t) u += paged_item(a, tt, b, t, 0, start, n, len).kb.count();
-  return u * a.Hkv;
-}
-
-struct Run {
-  int b, tile, hk, off, units;   // where it begins, and its length
-  int64_t per;                   // units of a run
-};
-// The run of CTA `cta` of `ctas`, by one warp.
-ELSAA_DEV Run find_run(const AttendArgs& a, int tt, int cta, int ctas) {
-  const int lane = threadIdx.x & 31;
-  int64_t total = 0;
-  for (int b = lane; b < a.seqs; b += 32) total += seq_units(a, tt, b, cta == 0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int64_t per = max((total + ctas - 1) / ctas, (int64_t)kMinUnits);
-  Run c{0, 0, 0, 0, 0, per};
-  int64_t w = per * cta;
-  if (w >= total) return c;
-  c.units = (int)min(per, total - w);
-  for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-    const int64_t mine = b0 + lane < a.seqs ? seq_units(a, tt, b0 + lane, false) : 0;
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, w < upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      int64_t rest = w - __shfl_sync(0xffffffffu, upto - mine, l);
-      c.b = b0 + l;
-      int start, len;
-      const int n = new_tokens(a, c.b, &start, &len, false);
-      for (; c.tile * tt < n; ++c.tile) {
-        const int64_t blk = paged_item(a, tt, c.b, c.tile, 0, start, n, len).kb.count();
-        if (rest < blk * a.Hkv) {
-          c.hk = (int)(rest / blk);
-          c.off = (int)(rest % blk);
-          break;
-        }
-        rest -= blk * a.Hkv;
-      }
-      return c;
-    }
-    w -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return c;
-}
-
-// Partial rows: [slot][row][D] and (m, l) [slot][row], slot = 2 cta + (not the run's first item).
-template <int ROWS>
-ELSAA_DEV float* partial_o(const AttendArgs& a, int d, int slot, int row) {
-  return reinterpret_cast<float*>(a.scratch) + ((int64_t)slot * ROWS + row) * d;
-}
-template <int ROWS>
-ELSAA_DEV float2* partial_ml(const AttendArgs& a, int d, int slot, int row) {
-  return reinterpret_cast<float2*>(partial_o<ROWS>(a, d, 2 * kRuns, 0)) + (int64_t)slot * ROWS + row;
-}
-
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
 paged_simt_kernel(const AttendArgs a) {
@@ -342,8 +261,8 @@ paged_simt_kernel(const AttendArgs a) {
     if (threadIdx.x == 0) run = c;
   }
   __syncthreads();
-  int b = run.b, tile = run.tile, hk = run.hk, off = run.off, left = run.units, start = 0, len = 0, tokens = 0;
-  if (left > 0) tokens = new_tokens(a, b, &start, &len, false);
+  int b = run.b, tile = run.tile, hk = run.hk, off = run.off, left = run.units;
+  int start = run.start, len = run.len, tokens = run.tokens;
   int64_t at = run.per * blockIdx.x;   // the next unit
   for (int order = 0; left > 0; ++order) {
     while (tile * tt >= tokens) {
@@ -351,7 +270,7 @@ paged_simt_kernel(const AttendArgs a) {
       tile = hk = off = 0;
       tokens = new_tokens(a, b, &start, &len, false);
     }
-    const PagedItem it = paged_item(a, tt, b, tile, hk, start, tokens, len);
+    const PagedItem it = paged_item(a, tt, tile, tokens, len);
     const int nblk = it.kb.count(), n0 = off, n1 = min(nblk, off + left);
     // row r of the tile: token tile tt + r / g, head hk g + r % g
     auto live = [&](int r) { return r / g < tt && tile * tt + r / g < tokens; };
@@ -404,9 +323,8 @@ paged_simt_kernel(const AttendArgs a) {
       }
     }
     if (!whole) {
-      const int64_t begin = at - off;
-      const int cta0 = (int)(begin / run.per), cta1 = (int)((begin + nblk - 1) / run.per);
-      const int slot0 = begin == cta0 * run.per ? 0 : 1;
+      const Ctas c = ctas_of(at - off, nblk, run.per);
+      const int cta0 = c.first, cta1 = c.last, slot0 = c.slot0;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0)
@@ -623,10 +541,6 @@ cudaError_t dkv(const AttendArgs& a, cudaStream_t s) {
   return run(window_dkv_simt_kernel<T, D, R>, (int64_t)a.B * a.Hkv * tiles, bytes<D>(R, 2, 2, 2), s, a, tiles);
 }
 
-// Rows of a paged tile: 16 where a sequence's new rows fill no more (and the group fits).
-int paged_tile_rows(int64_t rows, int seqs, int g) {
-  return g <= 16 && (rows + seqs - 1) / seqs * g <= 16 ? 16 : 64;
-}
 template <typename T, int D>
 cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
   if (paged_tile_rows(a.rows, a.seqs, a.g) == 16)
@@ -657,10 +571,6 @@ struct Launch {
                        : Launch<float, 128>::f(a, s)))
 
 }  // namespace
-
-size_t paged_simt_scratch_bytes(int d, int64_t rows, int seqs, int g) {
-  return (size_t)2 * kRuns * paged_tile_rows(rows, seqs, g) * (d + 2) * sizeof(float);
-}
 
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.H * a.N, warps = kThreads / 32;
