@@ -31,6 +31,12 @@ __host__ __device__ inline KeyBlocks key_blocks(int p_lo, int p_hi, int window, 
   return k;
 }
 
+// x / y of values below 2^63, in 32 bits where they fit (four times as fast).
+ELSAA_DEV int64_t div64(int64_t x, int64_t y) {
+  if (((uint64_t)x | (uint64_t)y) >> 32 == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+
 // ---- pages -----------------------------------------------------------------
 
 // New tokens of sequence b: clamped to what q holds and the context has

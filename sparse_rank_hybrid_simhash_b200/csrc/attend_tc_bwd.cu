@@ -98,46 +98,63 @@ ELSAA_DEV int length_of(const AttendArgs& a, int b) {
 
 // ---- row statistics (and the zeros of empty tiles) ------------------------------------------------------------
 
+// Four rows a lane group, all their loads in flight before the first sum.
+constexpr int kStatRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const Stats st) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
   const int c = (threadIdx.x % LANES) * 8;
-  const int64_t x = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
-  const bool in = x < (int64_t)a.B * a.H * st.pad;
-  const int n = in ? (int)(x % st.pad) : 0;
-  const int64_t bh = in ? x / st.pad : 0;
-  const int h = (int)(bh % a.H), b = (int)(bh / a.H);
-  float s = 0.f, nl = -INFINITY;
-  if (in && n < length_of(a, b)) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) +
-                                                    b * a.sy.b + h * a.sy.h + n * a.sy.n + c);
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy) +
-                                                    b * a.sdy.b + h * a.sdy.h + n * a.sdy.n + c);
-    const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w};
+  const int pad = (int)st.pad, rows = a.B * a.H * pad;   // (below 2^31)
+  const int x0 = (int)blockIdx.x * (ROWS * kStatRows) + threadIdx.x / LANES;
+  uint4 u[kStatRows], w[kStatRows];
+  float nl[kStatRows];
+  bool empty[kStatRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s += __uint_as_float(ua[i] << 16) * __uint_as_float(wa[i] << 16) +
-           __uint_as_float(ua[i] & 0xffff0000u) * __uint_as_float(wa[i] & 0xffff0000u);
-    const float l = a.lse[bh * a.N + n];
-    if (l > -INFINITY) nl = -l * 1.4426950408889634f;
+  for (int i = 0; i < kStatRows; ++i) {
+    const int x = x0 + i * ROWS;
+    u[i] = w[i] = make_uint4(0, 0, 0, 0);
+    nl[i] = INFINITY;
+    empty[i] = false;
+    if (x < rows) {
+      const int bh = x / pad, n = x - bh * pad, b = bh / a.H, h = bh - b * a.H, len = length_of(a, b);
+      if (n < len) {
+        u[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) + b * a.sy.b +
+                                               h * a.sy.h + n * a.sy.n + c);
+        w[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy) + b * a.sdy.b +
+                                               h * a.sdy.h + n * a.sdy.n + c);
+        nl[i] = a.lse[(int64_t)bh * a.N + n];
+      }
+      empty[i] = n < a.N && n / kBlock * kBlock >= len;
+    }
   }
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (in && c == 0) {
-    st.nl[x] = nl;
-    st.nd[x] = -s;
-  }
-  if (in && n < a.N && n / kBlock * kBlock >= length_of(a, b)) {
-    // a tile behind the length is no item of the kernels below: its zeros
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dq) + b * a.sdq.b + h * a.sdq.h +
-                              n * a.sdq.n + c) = z;
-    if (h % a.g == 0) {
-      const int hk = h / a.g;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk) + b * a.sdk.b + hk * a.sdk.h +
-                                n * a.sdk.n + c) = z;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv) + b * a.sdv.b + hk * a.sdv.h +
-                                n * a.sdv.n + c) = z;
+  for (int i = 0; i < kStatRows; ++i) {
+    const int x = x0 + i * ROWS;
+    const uint32_t ua[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, wa[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s += __uint_as_float(ua[e] << 16) * __uint_as_float(wa[e] << 16) +
+           __uint_as_float(ua[e] & 0xffff0000u) * __uint_as_float(wa[e] & 0xffff0000u);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (x < rows && c == 0) {
+      // (a row without keys has lse -inf; like a row behind the length it gets P = 0)
+      st.nl[x] = fabsf(nl[i]) == INFINITY ? -INFINITY : -nl[i] * 1.4426950408889634f;
+      st.nd[x] = -s;
+    }
+    if (empty[i]) {   // a tile behind the length is no item of the kernels below: its zeros
+      const int bh = x / pad, n = x - bh * pad, b = bh / a.H, h = bh - b * a.H;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dq) + b * a.sdq.b + h * a.sdq.h +
+                                n * a.sdq.n + c) = z;
+      if (h % a.g == 0) {
+        const int hk = h / a.g;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk) + b * a.sdk.b + hk * a.sdk.h +
+                                  n * a.sdk.n + c) = z;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv) + b * a.sdv.b + hk * a.sdv.h +
+                                  n * a.sdv.n + c) = z;
+      }
     }
   }
 }
@@ -1052,7 +1069,7 @@ cudaError_t backward(const AttendArgs& args, cudaStream_t s) {
       (e = make_map_4d(&maps.v, a.v, D, a.N, a.Hkv, a.B, a.sv.n, a.sv.h, a.sv.b, box)) != cudaSuccess ||
       (e = make_map_4d(&maps.dy, a.dy, D, a.N, a.H, a.B, a.sdy.n, a.sdy.h, a.sdy.b, box)) != cudaSuccess)
     return e;
-  constexpr int kRows = 256 / (D / 8);
+  constexpr int kRows = 256 / (D / 8) * kStatRows;
   stats_kernel<D><<<(unsigned)((rows + kRows - 1) / kRows), 256, 0, s>>>(a, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int smem = (int)Lay<D>::kDyn;

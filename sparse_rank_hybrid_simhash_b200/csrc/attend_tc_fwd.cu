@@ -25,9 +25,11 @@
 // warp of every CTA).  A second kernel for that cost 12 us a call.
 //
 // Roles (384 threads, one CTA per SM): warps 0..3 and 4..7 softmax and output of
-// the two streams, warp 8 TMA, warps 9 and 10 the streams' products, warp 11 hands
-// out the items through a ring in shared memory (registers move between whole warpgroups:
-// a softmax thread holds its row of S).  K and V blocks pass
+// the two streams, warp 8 copies Q and K, warps 9 and 10 issue the streams' products,
+// warp 11 copies V and hands out the items through a ring in shared memory (registers move
+// between whole warpgroups: a softmax thread holds its row of S).  With pages of 16
+// tokens a block is 16 copies each of K and V, at about 70 cycles a copy a warp: two
+// copying warps keep up with the pages' bytes.  K and V blocks pass
 // through one ring of slots (K0 V0 K1 V1 ...).  Keys behind a length may hold
 // anything: their scores are replaced, and the MMA warps zero their value rows
 // in shared memory (0 times a stray infinity is not 0).
@@ -51,7 +53,7 @@ using namespace tc;
 constexpr int kThreads = 384;
 // registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kItemWarp = 11;
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTO = 256;            // O of stream s at kTO + 128 s; S (and P) at 128 s
 constexpr float kGrow = 8.0f;            // log2 of the growth that rescales O
@@ -128,6 +130,12 @@ ELSAA_DEV void item_blocks(Item& it, const AttendArgs& a) {
   it.nblk = it.sink_blocks + max(it.k_last[0], it.k_last[1]) - it.first + 1;
 }
 
+// Where a paged CTA's run begins, and its length (0: no work).
+struct Cut {
+  int b, pair, hk, off, units;
+  int start, tokens, len;       // of sequence b
+};
+
 constexpr int kItems = 4;
 struct Bars {
   uint64_t full[8], empty[8];   // ring slots
@@ -137,7 +145,7 @@ struct Bars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
   uint32_t tmem;
-  int32_t cut[5];               // a paged CTA's first item (Cut)
+  Cut cut;                      // a paged CTA's first item
   int64_t per;                  // units of a run
   Item items[kItems];
 };
@@ -200,41 +208,39 @@ ELSAA_DEV Item paged_item(const AttendArgs& a, const Shape& sh, int b, int pair,
   return it;
 }
 
-struct Cut {
-  int b, pair, hk, off;   // where a run begins: its item and block
-  int units;              // its length
-};
-
-// Units (tile pair, key head, block) of sequence b.
-ELSAA_DEV int64_t seq_units(const AttendArgs& a, const Shape& sh, int b, bool lead) {
-  int start, len;
-  const int n = new_tokens(a, b, &start, &len, lead);
+// Units (tile pair, key head, block) of a sequence.
+ELSAA_DEV int64_t seq_units(const AttendArgs& a, const Shape& sh, int tokens, int len) {
   int64_t u = 0;
-  const int pairs = pairs_of(n, sh.tt);
-  for (int p = 0; p < pairs; ++p) u += paged_item(a, sh, b, p, 0, start, n, len).nblk;
+  const int pairs = pairs_of(tokens, sh.tt);
+  for (int p = 0; p < pairs; ++p) u += paged_item(a, sh, 0, p, 0, 0, tokens, len).nblk;
   return u * a.Hkv;
 }
 
-ELSAA_DEV int64_t run_length(int64_t total, int ctas) {
-  const int64_t per = (total + ctas - 1) / ctas;
-  return per > kMinUnits ? per : kMinUnits;
-}
-
-// The run of CTA `cta` of `ctas`, by one warp; units 0: nothing is left for it.
-// *per: units of a run.
+// The run of CTA `cta` of `ctas`, by one warp; *per: units of a run.
 ELSAA_DEV Cut find_run(const AttendArgs& a, const Shape& sh, int cta, int ctas, int64_t* per) {
   const int lane = threadIdx.x & 31;
-  Cut c{0, 0, 0, 0, 0};
+  Cut c{0, 0, 0, 0, 0, 0, 0, 0};
   int64_t total = 0, mine = 0;
-  for (int b = lane; b < a.seqs; b += 32) total += mine = seq_units(a, sh, b, cta == 0);
+  int start = 0, len = 0, n = 0;
+  for (int b = lane; b < a.seqs; b += 32) {
+    n = new_tokens(a, b, &start, &len, cta == 0);
+    total += mine = seq_units(a, sh, n, len);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  *per = run_length(total, ctas);
+  *per = div64(total + ctas - 1, ctas);
+  if (*per < kMinUnits) *per = kMinUnits;
   int64_t w = *per * cta;
   if (w >= total) return c;
   c.units = (int)(*per < total - w ? *per : total - w);
   for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-    if (a.seqs > 32) mine = b0 + lane < a.seqs ? seq_units(a, sh, b0 + lane, false) : 0;
+    if (a.seqs > 32) {
+      mine = n = 0;
+      if (b0 + lane < a.seqs) {
+        n = new_tokens(a, b0 + lane, &start, &len, false);
+        mine = seq_units(a, sh, n, len);
+      }
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -246,17 +252,18 @@ ELSAA_DEV Cut find_run(const AttendArgs& a, const Shape& sh, int cta, int ctas, 
       const int l = __ffs(hit) - 1;
       int64_t rest = w - __shfl_sync(0xffffffffu, upto - mine, l);
       c.b = b0 + l;
-      int start, len;
-      const int n = new_tokens(a, c.b, &start, &len, false);
-      const int pairs = pairs_of(n, sh.tt);
-      for (c.pair = 0; c.pair < pairs; ++c.pair) {
-        const int64_t blk = paged_item(a, sh, c.b, c.pair, 0, start, n, len).nblk;
-        if (rest < blk * a.Hkv) {
-          c.hk = (int)(rest / blk);
-          c.off = (int)(rest % blk);
+      c.start = __shfl_sync(0xffffffffu, start, l);
+      c.tokens = __shfl_sync(0xffffffffu, n, l);
+      c.len = __shfl_sync(0xffffffffu, len, l);
+      const int pairs = pairs_of(c.tokens, sh.tt);
+      for (; c.pair < pairs; ++c.pair) {
+        const int blk = paged_item(a, sh, c.b, c.pair, 0, c.start, c.tokens, c.len).nblk;
+        if (rest < (int64_t)blk * a.Hkv) {
+          c.hk = (int)div64(rest, blk);
+          c.off = (int)(rest - (int64_t)c.hk * blk);
           break;
         }
-        rest -= blk * a.Hkv;
+        rest -= (int64_t)blk * a.Hkv;
       }
       return c;
     }
@@ -274,13 +281,12 @@ struct Walk {
   int b, pair, hk, off, left, start, tokens, len;   // pages
   int order;                                 // items so far
   int64_t per, at;                           // pages: units of a run, and the next unit
-  ELSAA_DEV Walk(const AttendArgs& a_, const Shape& sh_, int64_t items_, const int32_t* cut, int64_t per_)
+  ELSAA_DEV Walk(const AttendArgs& a_, const Shape& sh_, int64_t items_, const Cut& c, int64_t per_)
       : a(a_), sh(sh_), x(blockIdx.x), items(items_), order(0), per(per_) {
     if (PAGED) {
       at = per * blockIdx.x;
-      b = cut[0], pair = cut[1], hk = cut[2], off = cut[3], left = cut[4];
-      start = tokens = len = 0;
-      if (left > 0) tokens = new_tokens(a, b, &start, &len, false);
+      b = c.b, pair = c.pair, hk = c.hk, off = c.off, left = c.units;
+      start = c.start, tokens = c.tokens, len = c.len;
     }
   }
   ELSAA_DEV bool next(Item& it) {
@@ -303,8 +309,8 @@ struct Walk {
     it.cta0 = it.cta1 = it.slot0 = 0;
     if (it.n1 - it.n0 < it.nblk) {
       const int64_t begin = at - off;
-      it.cta0 = (int)(begin / per);
-      it.cta1 = (int)((begin + it.nblk - 1) / per);
+      it.cta0 = (int)div64(begin, per);
+      it.cta1 = (int)div64(begin + it.nblk - 1, per);
       it.slot0 = begin == it.cta0 * per ? 0 : 1;
     }
     left -= it.n1 - it.n0;
@@ -415,6 +421,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     if (tid == 0) raise_error(a.err, ERR_CHECK);
     return;
   }
+  if (tid == 32 * kKWarp) {
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+  }
   if (tid == 0) {
     for (int i = 0; i < SL; ++i) {
       mbar_init(&bars->full[i], 1);
@@ -431,7 +442,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     mbar_init(&bars->x_done, 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 11);   // eight softmax warps, TMA, two MMA
+      mbar_init(&bars->item_empty[i], 12);   // eight softmax warps, K, V, two MMA
     }
     mbar_init(&bars->drain, 2);
     fence_mbar_init();
@@ -440,13 +451,12 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     int64_t per;
     const Cut c = find_run(a, sh, blockIdx.x, gridDim.x, &per);
     if (lane == 0) {
-      bars->cut[0] = c.b, bars->cut[1] = c.pair, bars->cut[2] = c.hk;
-      bars->cut[3] = c.off, bars->cut[4] = c.units;
+      bars->cut = c;
       bars->per = per;
     }
   }
   __syncthreads();
-  if (PAGED && bars->cut[4] == 0) return;
+  if (PAGED && bars->cut.units == 0) return;
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem, kTmemCols);
     tmem_relinquish();
@@ -470,7 +480,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     ++ni;
   };
 
-  if (warp < kTmaWarp) {
+  if (warp < kKWarp) {
     regs_up<kSoftmaxRegs>();
     // ------------------------------------------------------------------ softmax and output
     const int st = warp >> 2, row = tid & 127;
@@ -680,67 +690,56 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     }
   } else {
     regs_down<kOtherRegs>();
-    if (warp == kTmaWarp) {
-      // ------------------------------------------------------------------ copies
-      uint32_t nr = 0, nq = 0;   // ring loads and Q loads so far
+    if (warp == kKWarp || warp == kVWarp) {
+      // ------------------------------------------------------------------ copies (and items)
+      const int kv = warp == kVWarp ? 1 : 0;
+      const CUtensorMap* map = kv ? &maps.v : &maps.k;
       const int subs = PAGED ? kBlock / sh.sub : 1;
-      // the slot for the next load, free and armed
-      auto acquire = [&]() -> uint32_t {
-        const uint32_t s = nr % SL;
-        if (nr >= SL) ok = warp_wait(&bars->empty[s], (nr / SL - 1) & 1, a.err);
-        if (ok && lane == 0) mbar_arrive_expect_tx(&bars->full[s], L::kTile);
+      RingPos<SL> at;            // K and V take the slots in turn
+      if (kv) at.next();
+      uint32_t loads = 0, nq = 0;
+      // pages: this lane's box of block n; boxes behind the length, or that no row of the
+      // item sees, are not looked up, and a page outside the pool reads as zeros
+      auto lookup = [&](const Item& it, int n) -> int {
+        if (!PAGED || lane >= subs || n >= it.n1) return a.pages;
+        const int j = it.block(n) * kBlock + lane * sh.sub;
+        if (j > max(it.p_last[0], it.p_last[1]) ||
+            !(j < a.sinks || (int64_t)j + sh.sub - 1 > (int64_t)it.p_first[0] - a.window))
+          return a.pages;
+        const int page = page_of(a, it.b, j);
+        return page < 0 ? a.pages : page;
+      };
+      auto load_block = [&](const Item& it, int n, int page) {
+        // (a fresh barrier counts as released)
+        ok = ok && warp_wait(&bars->empty[at.slot], at.phase ^ 1, a.err);
+        if (!ok) return;
+        uint64_t* bar = &bars->full[at.slot];
+        if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
         __syncwarp();
-        if (ok) ++nr;
-        return s;
-      };
-      auto load_block = [&](const Item& it, int n) {
         const int j0 = it.block(n) * kBlock;
-        int page = 0, slot = 0;
-        if (PAGED && lane < subs) {
-          // boxes behind the length, or that no row of the item sees, are not looked
-          // up; a page outside the pool reads as zeros
-          const int j = j0 + lane * sh.sub;
-          const int p_hi = max(it.p_last[0], it.p_last[1]);
-          page = a.pages;
-          if (j <= p_hi && (j < a.sinks || (int64_t)j + sh.sub - 1 > (int64_t)it.p_first[0] - a.window)) {
-            page = page_of(a, it.b, j);
-            if (page < 0) page = a.pages;
-            slot = j % a.page_size;
+        const uint32_t dst = sbase + L::kRing + at.slot * L::kTile;
+        if (lane < subs) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            if (PAGED)
+              tma_load_4d(dst + c * kAtom + lane * sh.sub * 128, map, 64 * c,
+                          (j0 + lane * sh.sub) % a.page_size, it.hk, page, bar);
+            else
+              tma_load_4d(dst + c * kAtom, map, 64 * c, j0, it.hk, it.b, bar);
           }
         }
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const uint32_t s = acquire();
-          if (!ok) break;
-          const CUtensorMap* map = kv ? &maps.v : &maps.k;
-          const uint32_t dst = sbase + L::kRing + s * L::kTile;
-          if (lane < subs) {
-  #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              if (PAGED)
-                tma_load_4d(dst + c * kAtom + lane * sh.sub * 128, map, 64 * c, slot, it.hk, page,
-                            &bars->full[s]);
-              else
-                tma_load_4d(dst + c * kAtom, map, 64 * c, j0, it.hk, it.b, &bars->full[s]);
-            }
-          }
-          __syncwarp();
-        }
+        __syncwarp();
+        at.next(), at.next();
+        ++loads;
       };
-      while (const Item* item = take()) {
-        const Item& it = *item;
-        if (it.n0 >= it.n1) {
-          give_back();
-          continue;
-        }
-        load_block(it, it.n0);
-        // Q behind the first block: its slots wait for the previous item's last scores
-        if (ok && nq > 0) ok = warp_wait(&bars->q_empty, (nq - 1) & 1, a.err);
-        if (!ok) break;
+      auto load_q = [&](const Item& it) {
+        if (nq > 0) ok = ok && warp_wait(&bars->q_empty, (nq - 1) & 1, a.err);
+        if (!ok) return;
         if (lane == 0) {
           const int tiles = it.split ? 1 : 2;
           const uint32_t rows = PAGED ? sh.tt * a.g : kBlock;
           mbar_arrive_expect_tx(&bars->q_full, tiles * rows * D * 2);
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < 2; ++s)
             for (int c = 0; c < (s < tiles ? D / 64 : 0); ++c) {
               const uint32_t dst = sbase + L::kQ + s * L::kTile + c * kAtom;
@@ -752,18 +751,59 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
         __syncwarp();
         ++nq;
-        for (int n = it.n0 + 1, n1 = it.n1; n < n1 && ok; ++n) load_block(it, n);
+      };
+      Walk<PAGED> walk(a, sh, items, bars->cut, bars->per);   // (V's warp, lane 0)
+      uint32_t given = 0;
+      bool more = kv == 1;
+      auto hand_out = [&]() {
+        if (!more) return;
+        const uint32_t i = given % kItems;
+        ok = ok && warp_wait(&bars->item_empty[i], ((given / kItems) & 1) ^ 1, a.err);
+        if (!ok) return;
+        if (lane == 0) {
+          Item it;
+          more = walk.next(it);
+          if (!more) it.order = -1;
+          bars->items[i] = it;
+          mbar_arrive(&bars->item_full[i]);
+        }
+        more = __shfl_sync(0xffffffffu, more, 0);
+        ++given;
+      };
+      hand_out();
+      for (;;) {
+        hand_out();   // one ahead of what is copied
+        const Item* item = take();
+        if (item == nullptr) break;
+        const Item& it = *item;
+        const int n0 = it.n0, n1 = it.n1;
+        if (n0 < n1) {
+          int page = lookup(it, n0);
+          // Q of the first item first; later ones behind the first block, which need not
+          // wait for the last item's scores
+          const bool late = nq > 0;
+          if (!kv && !late) load_q(it);
+          for (int n = n0; n < n1 && ok; ++n) {
+            const int now = page;
+            page = lookup(it, n + 1);   // (in flight while the slot is awaited)
+            load_block(it, n, now);
+            if (!kv && late && n == n0) load_q(it);
+          }
+        }
+        if (!ok) break;
         give_back();
       }
       // every copy this warp started has landed before the CTA may exit
       if (lane == 0) {
-        for (uint32_t i = nr > SL ? nr - SL : 0; i < nr; ++i)
+        for (uint32_t m = loads > SL / 2 ? loads - SL / 2 : 0; m < loads; ++m) {
+          const uint32_t i = 2 * m + kv;
           mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
+        }
         if (nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, a.err);
       }
       __syncwarp();
 
-    } else if (warp < kItemWarp) {
+    } else {
       // ------------------------------------------------------------------ products
       // a warp a stream: one's waits and bookkeeping run under the other's products
       constexpr uint32_t id_pv = idesc_bf16(128, D, false, true);
@@ -847,22 +887,6 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       }
       __syncwarp();
 
-    } else {
-      // ------------------------------------------------------------------ items
-      if (lane == 0) {
-        Walk<PAGED> walk(a, sh, items, bars->cut, bars->per);
-        for (bool more = true; more; ++ni) {
-          if (ni >= kItems &&
-              !mbar_wait(&bars->item_empty[ni % kItems], (ni / kItems - 1) & 1, a.err))
-            break;
-          Item it;
-          more = walk.next(it);
-          if (!more) it.order = -1;
-          bars->items[ni % kItems] = it;
-          mbar_arrive(&bars->item_full[ni % kItems]);
-        }
-      }
-      __syncwarp();
     }
   }
   fence_before();

@@ -97,7 +97,7 @@ cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
 size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N);
 // Workspace bytes of launch_paged_tc's partial rows.
 size_t paged_scratch_bytes(int d, int64_t rows, int g);
-// A few rows a sequence (decoding), bf16, d = 64 or 128.
+// A few rows a sequence (decoding), bf16.
 bool paged_decode_supported(int d, bool bf16, int64_t rows, int seqs, int g);
 cudaError_t launch_paged_decode(const AttendArgs& a, cudaStream_t s);
 

@@ -48,6 +48,9 @@ elsaa_status check(const elsaa_window_params* p) {
   if (!p || !shape_ok(p->B, p->H, p->Hkv, p->N, p->d, p->dtype, &why)) return why;
   if (p->window < 0 || p->sinks < 0 || isnan(p->scale) || isinf(p->scale))
     return ELSAA_ERR_INVALID_ARG;
+  // (the rows padded to whole tiles, too)
+  if ((int64_t)p->B * p->H * (((int64_t)p->N + 127) / 128 * 128) > INT32_MAX - 4096)
+    return ELSAA_ERR_INVALID_ARG;
   return ELSAA_OK;
 }
 

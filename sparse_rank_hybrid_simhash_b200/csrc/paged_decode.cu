@@ -1,5 +1,4 @@
-// Attention of a few new rows a sequence over a paged cache (decoding: bf16, d = 64 or
-// 128, at most 16 (token, head of the group) rows a sequence on average).
+// Attention of a few new rows a sequence over a paged cache (decoding: bf16, at most 16 (token, head of the group) rows a sequence on average).
 //
 // Bound: HBM, each key and value of the contexts read once; the products of 16 rows
 // are a hundredth of what the bytes cost.  So the work per byte is kept small and many
@@ -34,7 +33,7 @@ template <int D>
 struct Lay {
   static constexpr int kRow = D * 2;                      // bytes of a row
   static constexpr int kStage = 2 * kKeys * kRow;         // K and V
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 3 : D == 64 ? 6 : 8;
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kPitch = D + 4;                    // floats of a joined row
   static constexpr int kDyn = kWarps * kWarpBytes;
@@ -67,6 +66,11 @@ ELSAA_DEV uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Where chunk c of row r lies in its row: the eight rows that an ldmatrix reads at one
+// chunk fall into different banks.
+template <int D>
+ELSAA_DEV int place(int c, int r) { return D == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendArgs a, float scale_log2) {
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendA
         for (int x = 0; x < kKeys * CH / 32; ++x) {
           const int r = (x * 32 + lane) / CH, c = (x * 32 + lane) % CH;
           const int pg = __shfl_sync(0xffffffffu, page, r);
-          const uint32_t to = dst + r * L::kRow + ((c ^ (r & 7)) << 4);
+          const uint32_t to = dst + r * L::kRow + (place<D>(c, r) << 4);
           const int64_t p = pg >= 0 ? pg : 0;
           const int64_t in = (int64_t)(slot0 + r);
           const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + p * a.sk.b +
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendA
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t kf[4];
-          ldsm4(ks + r * L::kRow + (((2 * k + ((lane >> 3) & 1)) ^ (r & 7)) << 4), kf);
+          ldsm4(ks + r * L::kRow + (place<D>(2 * k + ((lane >> 3) & 1), r) << 4), kf);
           mma16816(s[0], qf[k], kf[0], kf[1]);
           mma16816(s[1], qf[k], kf[2], kf[3]);
         }
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendA
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           uint32_t vf[4];
-          ldsm4_t(vs + r * L::kRow + (((2 * c + (lane >> 4)) ^ (r & 7)) << 4), vf);
+          ldsm4_t(vs + r * L::kRow + (place<D>(2 * c + (lane >> 4), r) << 4), vf);
           mma16816(o[2 * c], pf, vf[0], vf[1]);
           mma16816(o[2 * c + 1], pf, vf[2], vf[3]);
         }
@@ -327,11 +331,11 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
 }  // namespace
 
 bool paged_decode_supported(int d, bool bf16, int64_t rows, int seqs, int g) {
-  return bf16 && (d == 64 || d == 128) && paged_tile_rows(rows, seqs, g) == kRows;
+  return bf16 && (d == 32 || d == 64 || d == 128) && paged_tile_rows(rows, seqs, g) == kRows;
 }
 
 cudaError_t launch_paged_decode(const AttendArgs& a, cudaStream_t s) {
-  return a.d == 64 ? launch<64>(a, s) : launch<128>(a, s);
+  return a.d == 32 ? launch<32>(a, s) : a.d == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace elsaa

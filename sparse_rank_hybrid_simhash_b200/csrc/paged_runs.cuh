@@ -38,12 +38,6 @@ ELSAA_DEV int64_t seq_units(const AttendArgs& a, int tt, int tokens, int len) {
   return u * a.Hkv;
 }
 
-// x / y of values below 2^63, in 32 bits where they fit (four times as fast).
-ELSAA_DEV int64_t div64(int64_t x, int64_t y) {
-  if (((uint64_t)x | (uint64_t)y) >> 32 == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
-}
-
 struct Run {
   int b, tile, hk, off, units;   // where it begins, and its length (0: no work)
   int start, tokens, len;        // of sequence b

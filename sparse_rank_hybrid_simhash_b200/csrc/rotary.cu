@@ -230,10 +230,10 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
     const float* tab = table_row(a, pos, live && col == 0);
     const bool ok = a.rot == 0 || tab != nullptr;
     const Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
-    for (int h = h0; h < h1; h += 2) {
-      uint4 rx[2], rg[2];
+    for (int h = h0; h < h1; h += kBatch) {
+      uint4 rx[kBatch], rg[kBatch];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
         if (live && ok && h + u < h1) {   // (a row without a position was written as zeros: no gradient)
           rx[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
@@ -241,7 +241,7 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
         }
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         if (h + u >= h1) break;
         float x[V], g[V];
         unpack<T>(rx[u], x);
