@@ -72,10 +72,10 @@ ELSAA_DEV void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, u
       : "memory");
 }
 
-// 128 x 128 product of two K-major tiles over D.
-template <int D>
+// 128 x N product of two K-major tiles over D.
+template <int D, int N = kBlock>
 ELSAA_DEV void mma_tiles(uint32_t d_tmem, uint32_t ad, uint32_t bd) {
-  constexpr uint32_t id = idesc_bf16(128, kBlock, false, false);
+  constexpr uint32_t id = idesc_bf16(128, N, false, false);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32) >> 4;

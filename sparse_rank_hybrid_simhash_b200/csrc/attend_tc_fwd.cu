@@ -3,8 +3,10 @@
 // pipeline, one pass over the keys with the running maximum and sum.
 //
 // Two streams of 128 query rows share every 128-key block of K and V: S = Q K^T
-// (TMEM), P = 2^(scale log2e S - m) written over S as bf16, O += P V (TMEM).  While
-// one stream's softmax works, the tensor cores run the other's products.  A row
+// (TMEM), P = 2^(scale log2e S - m) written over S as bf16, O += P V (TMEM).  A stream
+// works on 64-key halves in turn: while its softmax reads one, the tensor cores put
+// the other's P into O and the next S in its place.  (With whole blocks the softmax
+// waited for both products: a block took 3560 cycles of a CTA at d = 128.)  A row
 // belongs to one thread, so maximum, sum and rescaling stay in its registers.  O is
 // rescaled only when a row's maximum has grown by more than 2^8 over the one it
 // used so far (P <= 2^8 otherwise; bf16 keeps the same relative precision there,
@@ -93,41 +95,38 @@ struct Item {
   int start, tokens;        // pages: first row of q, new tokens
   bool split;               // one tile, alternate blocks
   int sink_blocks, first, nblk, n0, n1;
-  int k_first[2], k_last[2], sink_top;
+  int f64[2], l64[2], s64;  // a stream's window in 64-key halves of blocks, and the sinks'
   int order;                // the CTA's items before it; -1: there are no more
   int cta0, cta1, slot0;    // a cut item: its CTAs, and whether it is not the first of cta0's
   ELSAA_DEV int block(int n) const { return n < sink_blocks ? n : first + n - sink_blocks; }
-  ELSAA_DEV bool uses(int s, int n) const {
-    if (split) return (n & 1) == s;
-    const int kb = block(n);
-    return kb <= pick(k_last, s) && (kb >= pick(k_first, s) || kb < sink_top);
+  // whether the stream uses half h of block n
+  ELSAA_DEV bool uses(int s, int n, int h) const {
+    if (split && (n & 1) != s) return false;
+    const int x = 2 * block(n) + h;
+    return x <= pick(l64, s) && (x >= pick(f64, s) || x < s64);
   }
-  // the last block of [n0, n1) that the stream uses; n0 - 1: none
+  // the last half (2 n + h) of [n0, n1) that the stream uses; 2 n0 - 1: none
   ELSAA_DEV int last_use(int s) const {
-    int n = n1 - 1;
-    while (n >= n0 && !uses(s, n)) --n;
-    return n;
+    int x = 2 * n1 - 1;
+    while (x >= 2 * n0 && !uses(s, x >> 1, x & 1)) --x;
+    return x;
   }
 };
 
 ELSAA_DEV void item_blocks(Item& it, const AttendArgs& a) {
-  it.sink_top = (int)(((int64_t)a.sinks + kBlock - 1) / kBlock);
+  it.s64 = (int)(((int64_t)a.sinks + 63) / 64);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    it.k_first[s] = 0;
-    it.k_last[s] = -1;
-    if (it.p_last[s] >= 0) {
-      const KeyBlocks k = key_blocks(it.p_first[s], it.p_last[s], a.window, a.sinks, kBlock);
-      it.k_first[s] = k.first;
-      it.k_last[s] = k.last;
-    }
+    const int lo = it.p_first[s] - a.window + 1;
+    it.f64[s] = lo > 0 ? lo / 64 : 0;
+    it.l64[s] = it.p_last[s] >= 0 ? it.p_last[s] / 64 : -1;
   }
   // the union: stream 0 starts and ends no later than stream 1 (where that has rows)
   it.nblk = it.sink_blocks = it.first = 0;
   if (it.p_last[0] < 0) return;
-  it.first = it.k_first[0];
-  it.sink_blocks = min(it.sink_top, it.first);
-  it.nblk = it.sink_blocks + max(it.k_last[0], it.k_last[1]) - it.first + 1;
+  it.first = it.f64[0] >> 1;
+  it.sink_blocks = min((it.s64 + 1) >> 1, it.first);
+  it.nblk = it.sink_blocks + (max(it.l64[0], it.l64[1]) >> 1) - it.first + 1;
 }
 
 // Where a paged CTA's run begins, and its length (0: no work).
@@ -140,7 +139,8 @@ constexpr int kItems = 4;
 struct Bars {
   uint64_t full[8], empty[8];   // ring slots
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2][2], p_full[2][2];   // [stream][half]
+  uint64_t pv_done[2], o_full[2];
   uint64_t x_full, x_done;      // a split item: O of stream 1 given, and read
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
@@ -434,8 +434,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 2);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_full[s], 4);   // a stream's warps
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bars->s_full[s][h], 1);
+        mbar_init(&bars->p_full[s][h], 4);   // a stream's warps
+      }
+      mbar_init(&bars->pv_done[s], 1);
       mbar_init(&bars->o_full[s], 1);
     }
     mbar_init(&bars->x_full, 4);
@@ -487,7 +490,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + 128 * st + lane_off, tO = tmem + kTO + 128 * st + lane_off;
     float* ml1 = reinterpret_cast<float*>(smem + L::kMl);
-    uint32_t ns = 0, no = 0, nx = 0;
+    uint32_t ns = 0, np = 0, no = 0, nx = 0;   // ns: phases of both halves' S, one bit each
     const int tok_of_row = PAGED ? row / a.g : row;
     while (const Item* item = take()) {
       const Item& it = *item;
@@ -500,27 +503,28 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       bool any = false;
       const int n1 = it.n1, sink_blocks = it.sink_blocks, shift = it.first - sink_blocks;
       const int p_first = pick(it.p_first, st), edge = pick(it.p_last, st) - a.window;
-      const int k_first = pick(it.k_first, st), k_last = pick(it.k_last, st), sink_top = it.sink_top;
+      const int f64 = pick(it.f64, st), l64 = pick(it.l64, st), s64 = it.s64;
       const bool split = it.split;
-      for (int n = it.n0; n < n1; ++n) {
-        const int kb = n < sink_blocks ? n : n + shift;
-        if (split ? (n & 1) != st : kb > k_last || (kb < k_first && kb >= sink_top)) continue;
-        ok = warp_wait(&bars->s_full[st], ns & 1, a.err);
+#pragma unroll 1
+      for (int x = 2 * it.n0; x < 2 * n1 && ok; ++x) {   // half x & 1 of block x >> 1
+        const int n = x >> 1, h = x & 1, k64 = 2 * (n < sink_blocks ? n : n + shift) + h;
+        if ((split && (n & 1) != st) || k64 > l64 || (k64 < f64 && k64 >= s64)) continue;
+        ok = warp_wait(&bars->s_full[st][h], (ns >> h) & 1, a.err);
         if (!ok) break;
-        ++ns;
+        ns ^= 1u << h;
         fence_after();
         if (warp_live) {
-          const int j0 = kb * kBlock;
-          float sv[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sv + 32 * c);
+          const int j0 = k64 * 64;
+          float sv[64];
+          tmem_ld32(tS + 64 * h, sv);
+          tmem_ld32(tS + 64 * h + 32, sv + 32);
           tmem_ld_wait();
-          // some row of the tile does not see all of the block
-          if (j0 + kBlock - 1 > p_first || j0 <= edge) {
+          // some row of the tile does not see all of the half
+          if (j0 + 63 > p_first || j0 <= edge) {
             const int hi = pos - j0, lo = pos - a.window + 1 - j0;
-            const int sk = (int)min((int64_t)a.sinks - j0, (int64_t)kBlock);
+            const int sk = (int)min((int64_t)a.sinks - j0, (int64_t)64);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
               const uint32_t see = upto_bits(hi - 32 * c) &
                                    (~upto_bits(lo - 1 - 32 * c) | upto_bits(sk - 1 - 32 * c));
 #pragma unroll
@@ -530,7 +534,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           }
           float t0 = sv[0], t1 = sv[1], t2 = sv[2], t3 = sv[3];
 #pragma unroll
-          for (int e = 4; e < 128; e += 4) {
+          for (int e = 4; e < 64; e += 4) {
             t0 = fmaxf(t0, sv[e]);
             t1 = fmaxf(t1, sv[e + 1]);
             t2 = fmaxf(t2, sv[e + 2]);
@@ -543,6 +547,9 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             if (grow) m = top;
             l *= f;
             if (any) {
+              // the last product into O has ended
+              ok = warp_wait(&bars->pv_done[st], (np - 1) & 1, a.err);
+              fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 float ov[16];
@@ -558,7 +565,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           const float base = m == -INFINITY ? 0.f : m;
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t packed[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -569,14 +576,15 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
               const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
               packed[e >> 1] = *reinterpret_cast<const uint32_t*>(&hv);
             }
-            tmem_st16(tS + 16 * c, packed);   // over S, which is all in registers
+            tmem_st16(tS + 64 * h + 16 * c, packed);   // over S, which is all in registers
           }
           l += l0 + l1;
           tmem_st_wait();
         }
         any = true;
+        ++np;
         fence_before();
-        warp_arrive(&bars->p_full[st]);
+        warp_arrive(&bars->p_full[st][h]);
       }
       if (!ok) break;
       if (any) {
@@ -812,7 +820,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       const uint32_t tS = uniform(tmem + 128 * st), tO = uniform(tmem + kTO + 128 * st);
       const uint32_t q_d = row_desc(sbase + L::kQ);
       const uint32_t k_d = row_desc(sbase + L::kRing), v_d = col_desc(sbase + L::kRing);
-      uint32_t nq = 0, np = 0;
+      uint32_t nq = 0, np = 0;   // np: phases of both halves' P, one bit each
       RingPos<SL> at;   // the ring slot of the next load: K of a block, then V
       auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, a.err); };
       while (const Item* item = take()) {
@@ -824,11 +832,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
         const int last = it.last_use(st);
         const uint32_t qd = uniform(q_d + (it.split || st == 0 ? 0 : kStep));
-        bool pend = false;
+        bool pend[2] = {false, false};
         uint32_t add = 0, sv = 0;          // slot of V of block n - 1
         for (int n = n0; n <= n1 && ok; ++n) {
           // what block n needs is awaited before the softmax of block n - 1
-          const bool more = n < n1, use = more && it.uses(st, n);
+          const bool more = n < n1;
           const uint32_t sk = at.slot;
           if (more) {
             ok = wait(&bars->full[sk], at.phase);
@@ -836,37 +844,46 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             at.next();
           }
           const uint32_t kd = uniform(k_d + sk * kStep), vd = uniform(v_d + sv * kStep);
-          const uint32_t acc = uniform(add);
-          if (pend) {
-            ok = ok && wait(&bars->p_full[st], np & 1);
-            ++np;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool use = more && it.uses(st, n, h);
+            const uint32_t acc = uniform(add);
+            if (pend[h]) {
+              ok = ok && wait(&bars->p_full[st][h], (np >> h) & 1);
+              np ^= 1u << h;
+            }
+            if (!ok) break;
+            fence_after();
+            if (elect_one()) {
+              if (pend[h]) {               // O (+)= P V of half h of block n - 1
+#pragma unroll
+                for (int x = 0; x < 64; x += 16)
+                  mma_ts(tO, tS + 64 * h + (x >> 1), vd + (64 * h + x) * 8, id_pv, x > 0 ? 1u : acc);
+                mma_commit(&bars->pv_done[st]);
+                if (2 * (n - 1) + h == last) mma_commit(&bars->o_full[st]);
+              }
+              if (use) {                   // S = Q K^T of half h of block n
+                mma_tiles<D, 64>(tS + 64 * h, qd, kd + 512 * h);
+                mma_commit(&bars->s_full[st][h]);
+              }
+            }
+            __syncwarp();
+            if (pend[h]) add = 1;
+            pend[h] = use;
           }
           if (!ok) break;
-          fence_after();
           if (elect_one()) {
-            if (pend) {                    // O (+)= P V of block n - 1
-#pragma unroll
-              for (int x = 0; x < kBlock; x += 16)
-                mma_ts(tO, tS + (x >> 1), vd + x * 8, id_pv, x > 0 ? 1u : acc);
-              if (n - 1 == last) mma_commit(&bars->o_full[st]);
-            }
             if (n > n0) mma_commit(&bars->empty[sv]);
-            if (use) {                     // S = Q K^T of block n
-              mma_tiles<D>(tS, qd, kd);
-              mma_commit(&bars->s_full[st]);
-            }
             if (more) mma_commit(&bars->empty[sk]);
             if (n + 1 == n1) mma_commit(&bars->q_empty);
           }
           __syncwarp();
-          if (pend) add = 1;
-          pend = use;
           if (more) {                      // V of block n
             sv = at.slot;
             ok = wait(&bars->full[sv], at.phase);
             at.next();
             const int live = len - it.block(n) * kBlock;
-            if (ok && use && live < kBlock && (PAGED || a.lengths != nullptr)) {
+            if (ok && (pend[0] || pend[1]) && live < kBlock && (PAGED || a.lengths != nullptr)) {
               // value rows behind the length: zeros (both warps may write them)
               uint8_t* v = smem + L::kRing + sv * L::kTile;
               for (int r = live * 8 + lane; r < kBlock * 8; r += 32)
