@@ -451,8 +451,8 @@ window_dkv_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           const float4 l = *reinterpret_cast<const float4*>(nl + e);
           fma2(p[e], p[e + 1], scale_log2, scale_log2, l.x, l.y);
           fma2(p[e + 2], p[e + 3], scale_log2, scale_log2, l.z, l.w);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) p[e + x] = ex2(p[e + x]);
+          exp2_pair<D == 64>(e >> 1, p[e], p[e + 1]);
+          exp2_pair<D == 64>((e >> 1) + 1, p[e + 2], p[e + 3]);
         }
         if (i0 < j0 + kBlock - 1 ||
             (j0 + kBlock > a.sinks && (int64_t)i0 + kBlock - 1 >= (int64_t)j0 + a.window)) {
@@ -809,8 +809,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           fma2(p[e], p[e + 1], scale_log2, scale_log2, nl, nl);
-          p[e] = ex2(p[e]);
-          p[e + 1] = ex2(p[e + 1]);
+          exp2_pair<D == 64>(e >> 1, p[e], p[e + 1]);
         }
         if (j0 + kBlock - 1 > r0 || (int64_t)j0 <= (int64_t)p_last - a.window) {
           const int hi = r - j0 - 64 * half, lo = r - a.window + 1 - j0 - 64 * half;

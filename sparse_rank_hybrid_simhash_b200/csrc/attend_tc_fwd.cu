@@ -571,9 +571,9 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             for (int e = 0; e < 32; e += 2) {
               float a0 = sv[32 * c + e], a1 = sv[32 * c + e + 1];
               fma2(a0, a1, sh.scale_log2, sh.scale_log2, -base, -base);
-              const float p0 = ex2(a0), p1 = ex2(a1);
-              add2(l0, l1, p0, p1);
-              const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
+              exp2_pair<true>(e >> 1, a0, a1);
+              add2(l0, l1, a0, a1);
+              const __nv_bfloat162 hv = __floats2bfloat162_rn(a0, a1);
               packed[e >> 1] = *reinterpret_cast<const uint32_t*>(&hv);
             }
             tmem_st16(tS + 64 * h + 16 * c, packed);   // over S, which is all in registers

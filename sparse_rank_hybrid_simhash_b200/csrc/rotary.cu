@@ -133,7 +133,7 @@ ELSAA_DEV void row_forward(float* x, const float* w, const Angles<V, IL>& a, int
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += x[i] * x[i];
     ss = group_sum<LANES>(ss);
-    const float r = 1.0f / sqrtf(ss * (1.0f / D) + g.eps);
+    const float r = rsqrtf(ss * (1.0f / D) + g.eps);   // (2 units off at most)
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = x[i] * r * w[i];
   }
@@ -230,29 +230,37 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
     const float* tab = table_row(a, pos, live && col == 0);
     const bool ok = a.rot == 0 || tab != nullptr;
     const Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
-    for (int h = h0; h < h1; h += kBatch) {
-      uint4 rx[kBatch], rg[kBatch];
+    // two heads a step, the next two's rows in flight meanwhile
+    uint4 rx[2], rg[2];
+    auto load = [&](int h) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
+      for (int u = 0; u < 2; ++u) {
         rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
         if (live && ok && h + u < h1) {   // (a row without a position was written as zeros: no gradient)
           rx[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
           rg[u] = *reinterpret_cast<const uint4*>(dy + (h + u) * sg.h);
         }
       }
+    };
+    load(h0);
+    for (int h = h0; h < h1; h += 2) {
+      uint4 cx[2], cg[2];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
+      for (int u = 0; u < 2; ++u) cx[u] = rx[u], cg[u] = rg[u];
+      load(h + 2);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         if (h + u >= h1) break;
         float x[V], g[V];
-        unpack<T>(rx[u], x);
-        unpack<T>(rg[u], g);
+        unpack<T>(cx[u], x);
+        unpack<T>(cg[u], g);
         rotate<V, IL, true, LANES>(g, ang, col, a.rot);
         if (a.norm) {
           float ss = 0.f;
 #pragma unroll
           for (int i = 0; i < V; ++i) ss += x[i] * x[i];
           ss = group_sum<LANES>(ss);
-          const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
           float dot = 0.f;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
