@@ -9,14 +9,16 @@
 // dn = du w, dx = r (dn - n mean(dn n)).
 //
 // Bound: HBM, each row read once and written once (backward: x and dy read, dx
-// written).  A row is held by a group of d / V lanes with one 16-byte load each
-// (V = 8 bf16 or 4 fp32 values), so the sums are shuffles within the group; in
-// halves a lane's partner values sit rot / (2 V) lanes away.  A group keeps its
-// token's cos and sin in registers and walks several heads of that token,
-// so the table (8 rot / 2 bytes a token, more than a bf16 row) is read once per
-// head chunk, not per head; four heads' rows are in flight at a time (an output may
-// be its input, so the compiler must keep a later row's load behind an earlier
-// row's store: text-32k queries and keys 102 us without the batches).
+// written), with instruction issue close behind.  A row is held by a group of d / V
+// lanes with one 16-byte load each (V = 8 bf16 or 4 fp32 values), so the sums are
+// shuffles within the group; in halves a lane's partner values sit rot / (2 V) lanes
+// away and come over as the raw 16 bytes.  A group walks several heads of its token
+// and keeps what does not depend on the head in registers, weight and angle folded:
+//   y_i = r (x_i A_i + x_o B_i),  A_i = w_i cos,  B_i = -+ w_o sin  (o: i's partner)
+// (text-32k queries and keys, rotating after the norm: 80 us, issue active 74 % of the
+// time).  Two or four heads' rows are in flight at a time (an output may be its
+// input, so the compiler must keep a later row's load behind an earlier store: 102 us
+// without).
 #include "common.cuh"
 #include "internal.h"
 #include "layer.h"
@@ -26,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;       // heads whose rows are in flight
+constexpr int kFwdBlocks = 4, kBackBlocks = 3;   // resident blocks an SM
 constexpr int kStarts = 2048;   // sequence starts kept in shared memory
 
 template <typename T>
@@ -71,73 +74,83 @@ ELSAA_DEV float group_sum(float v) {
   return v;
 }
 
-// The angles of a lane's V values: cos[i], sin[i] of value i's pair (in
-// halves), or of pair i / 2 in cos[i / 2] (interleaved).  Lanes past the
-// rotated part get (1, 0).
-template <int V, bool IL>
-struct Angles {
-  static constexpr int C = IL ? V / 2 : V;
-  float cs[C], sn[C];
-};
-template <int V, bool IL>
-ELSAA_DEV Angles<V, IL> load_angles(const float* row, int col, int rot) {
-  Angles<V, IL> a;
-  constexpr int C = Angles<V, IL>::C;
+// The partner values of a lane's 16 bytes: those of the lane `from` (halves), or the
+// neighbours in a pair (interleaved).
+template <typename T, bool IL>
+ELSAA_DEV void partners(const uint4& raw, int from, const float* x, float* o) {
+  constexpr int V = Vec<T>::V;
+  if (IL) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) a.cs[i] = 1.f, a.sn[i] = 0.f;
-  if (col < rot) {
+    for (int i = 0; i < V; ++i) o[i] = x[i ^ 1];
+  } else {
+    const uint4 r = make_uint4(__shfl_sync(0xffffffffu, raw.x, from), __shfl_sync(0xffffffffu, raw.y, from),
+                               __shfl_sync(0xffffffffu, raw.z, from), __shfl_sync(0xffffffffu, raw.w, from));
+    unpack<T>(r, o);
+  }
+}
+// The lane that holds the partners of this lane's columns (halves).
+template <int V>
+ELSAA_DEV int partner_lane(int col, int rot) {
+  const int lane = threadIdx.x & 31, hop = rot / (2 * V);
+  return col >= rot ? lane : col < rot / 2 ? lane + hop : lane - hop;
+}
+
+// The rotation of a lane's V values at a table row, u_i = x_i a_i + x_o b_i; columns
+// past the rotated part: (1, 0).
+template <int V, bool IL>
+struct Turn {
+  float a[V], b[V];
+  ELSAA_DEV Turn(const float* row, int col, int rot) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = 1.f, b[i] = 0.f;
+    if (col >= rot) return;
     const int first = IL ? col / 2 : (col < rot / 2 ? col : col - rot / 2);
+    constexpr int C = IL ? V / 2 : V;   // pairs of these columns
 #pragma unroll
     for (int i = 0; i < C; i += 2) {
       const float4 t = *reinterpret_cast<const float4*>(row + 2 * (first + i));
-      a.cs[i] = t.x, a.sn[i] = t.y, a.cs[i + 1] = t.z, a.sn[i + 1] = t.w;
+      const float c[2] = {t.x, t.z}, sn[2] = {t.y, t.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (IL) {
+          a[2 * (i + e)] = a[2 * (i + e) + 1] = c[e];
+          b[2 * (i + e)] = -sn[e];
+          b[2 * (i + e) + 1] = sn[e];
+        } else {
+          a[i + e] = c[e];
+          b[i + e] = col < rot / 2 ? -sn[e] : sn[e];
+        }
+      }
     }
   }
-  return a;
-}
-
-// u rotated in place (BACK: by the transposed rotation).  Every lane of the
-// warp takes part.
-template <int V, bool IL, bool BACK, int LANES>
-ELSAA_DEV void rotate(float* u, const Angles<V, IL>& a, int col, int rot) {
-  if (IL) {
-#pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float c = a.cs[i / 2], s = BACK ? -a.sn[i / 2] : a.sn[i / 2];
-      const float x = u[i], y = u[i + 1];
-      u[i] = x * c - y * s;
-      u[i + 1] = y * c + x * s;
-    }
-  } else {
-    const int hop = rot / (2 * V);
-    const bool low = col < rot / 2, in = col < rot;
-    const int lane = threadIdx.x & 31;
-    const int from = !in ? lane : low ? lane + hop : lane - hop;
-    // the value a adds -sin b, the value b adds +sin a; both signs turn in BACK
-    const float sign = low != BACK ? -1.f : 1.f;
+  // the weights of the values (w) and of their partners folded in
+  ELSAA_DEV void weigh(const float* w, int col, int rot) {
+    if (w == nullptr) return;
+    const int other = col >= rot ? col : col < rot / 2 ? col + rot / 2 : col - rot / 2;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float other = __shfl_sync(0xffffffffu, u[i], from);
-      u[i] = u[i] * a.cs[i] + sign * other * a.sn[i];
+      a[i] *= __ldg(w + col + i);
+      b[i] *= __ldg(w + (IL ? col + (i ^ 1) : other + i));
     }
   }
-}
+};
 
-// Forward of one row (in x, out in x): norm, weight, rotation.
-template <int D, int V, bool IL>
-ELSAA_DEV void row_forward(float* x, const float* w, const Angles<V, IL>& a, int col,
-                           const RotaryArgs& g) {
-  constexpr int LANES = D / V;
+// One row forward: x (its raw 16 bytes) to y.
+template <typename T, int D, bool IL>
+ELSAA_DEV void row_forward(const uint4& raw, const Turn<Vec<T>::V, IL>& t, int from, const RotaryArgs& g,
+                           float* y) {
+  constexpr int V = Vec<T>::V, LANES = D / V;
+  float x[V], o[V], r = 1.f;
+  unpack<T>(raw, x);
+  partners<T, IL>(raw, from, x, o);
   if (g.norm) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += x[i] * x[i];
-    ss = group_sum<LANES>(ss);
-    const float r = rsqrtf(ss * (1.0f / D) + g.eps);   // (2 units off at most)
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = x[i] * r * w[i];
+    r = rsqrtf(group_sum<LANES>(ss) * (1.0f / D) + g.eps);   // (2 units off at most)
   }
-  rotate<V, IL, false, LANES>(x, a, col, g.rot);
+#pragma unroll
+  for (int i = 0; i < V; ++i) y[i] = r * (x[i] * t.a[i] + o[i] * t.b[i]);
 }
 
 template <int V>
@@ -158,7 +171,7 @@ ELSAA_DEV const float* table_row(const RotaryArgs& a, int pos, bool lead) {
 
 // blockIdx.y: chunks of HP query heads, then of HP key heads.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kFwdBlocks)
 norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
   constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
   const int col = (threadIdx.x % LANES) * V;
@@ -174,22 +187,25 @@ norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
   const int pos = a.positions && live ? a.positions[tok] : n;
   const float* tab = table_row(a, pos, live && col == 0);
   const bool ok = a.rot == 0 || tab != nullptr;
-  Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
-  float w[V];
-  load_weight<V>(is_q ? a.wq : a.wk, col, w);
-  for (int h = h0; h < h1; h += kBatch) {
-    uint4 raw[kBatch];
+  uint4 raw[kBatch];
+  auto load = [&](int h) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       raw[u] = make_uint4(0, 0, 0, 0);
       if (live && h + u < h1) raw[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
     }
+  };
+  load(h0);   // (in flight while the angles are fetched)
+  Turn<V, IL> turn(tab, live && ok ? col : D, live && ok ? a.rot : 0);
+  turn.weigh(is_q ? a.wq : a.wk, col, a.rot);
+  const int from = partner_lane<V>(col, a.rot);
+  for (int h = h0; h < h1; h += kBatch) {
+    if (h > h0) load(h);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (h + u >= h1) break;
       float x[V];
-      unpack<T>(raw[u], x);
-      row_forward<D, V, IL>(x, w, ang, col, a);
+      row_forward<T, D, IL>(raw[u], turn, from, a, x);
       if (!ok)
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = 0.f;
@@ -202,7 +218,7 @@ norm_rotate_kernel(const RotaryArgs a, int hp, int q_chunks) {
 // queries, the rest those of the keys; each block leaves one partial sum of
 // its weight's gradient.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kBackBlocks)
 norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   constexpr int V = Vec<T>::V, LANES = D / V, ROWS = kThreads / LANES;
   const int col = (threadIdx.x % LANES) * V;
@@ -214,6 +230,7 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   const int first = is_q ? blockIdx.x : blockIdx.x - q_blocks;
   const int step = is_q ? q_blocks : gridDim.x - q_blocks;
   const Strides si = is_q ? a.sq : a.sk, sg = is_q ? a.sdqo : a.sdko, so = is_q ? a.sqo : a.sko;
+  const int from = partner_lane<V>(col, a.rot);
   float w[V], dw[V];
   load_weight<V>(is_q ? a.wq : a.wk, col, w);
 #pragma unroll
@@ -229,49 +246,49 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
     const int pos = a.positions && live ? a.positions[tok] : n;
     const float* tab = table_row(a, pos, live && col == 0);
     const bool ok = a.rot == 0 || tab != nullptr;
-    const Angles<V, IL> ang = load_angles<V, IL>(tab, ok && live ? col : D, ok ? a.rot : 0);
-    // two heads a step, the next two's rows in flight meanwhile
-    uint4 rx[2], rg[2];
+    uint4 cx[2], cg[2];
     auto load = [&](int h) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
+        cx[u] = cg[u] = make_uint4(0, 0, 0, 0);
         if (live && ok && h + u < h1) {   // (a row without a position was written as zeros: no gradient)
-          rx[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
-          rg[u] = *reinterpret_cast<const uint4*>(dy + (h + u) * sg.h);
+          cx[u] = *reinterpret_cast<const uint4*>(in + (h + u) * si.h);
+          cg[u] = *reinterpret_cast<const uint4*>(dy + (h + u) * sg.h);
         }
       }
     };
-    load(h0);
+    load(h0);   // (in flight while the angles are fetched)
+    const Turn<V, IL> turn(tab, live && ok ? col : D, live && ok ? a.rot : 0);
     for (int h = h0; h < h1; h += 2) {
-      uint4 cx[2], cg[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) cx[u] = rx[u], cg[u] = rg[u];
-      load(h + 2);
+      if (h > h0) load(h);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (h + u >= h1) break;
-        float x[V], g[V];
-        unpack<T>(cx[u], x);
+        // du, the transposed rotation of dy (b turns its sign); with n = x r, t = du x:
+        // dw += t r,  dx = du w r - x r^3 mean(t w)
+        float x[V], g[V], o[V];
         unpack<T>(cg[u], g);
-        rotate<V, IL, true, LANES>(g, ang, col, a.rot);
-        if (a.norm) {
-          float ss = 0.f;
+        partners<T, IL>(cg[u], from, g, o);
 #pragma unroll
-          for (int i = 0; i < V; ++i) ss += x[i] * x[i];
-          ss = group_sum<LANES>(ss);
-          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-          float dot = 0.f;
+        for (int i = 0; i < V; ++i) g[i] = g[i] * turn.a[i] - o[i] * turn.b[i];
+        if (a.norm) {
+          unpack<T>(cx[u], x);
+          float ss = 0.f, dot = 0.f;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            x[i] *= r;
-            if (ok) dw[i] += g[i] * x[i];
-            g[i] *= w[i];
-            dot += g[i] * x[i];
+            ss += x[i] * x[i];
+            o[i] = g[i] * x[i];
+            dot += o[i] * w[i];
           }
-          dot = group_sum<LANES>(dot) * (1.0f / D);
+          ss = group_sum<LANES>(ss);   // (every lane of the warp, whatever its row)
+          dot = group_sum<LANES>(dot);
+          const float r = ok ? rsqrtf(ss * (1.0f / D) + a.eps) : 0.f;
+          const float f = (r * r) * (r * (1.0f / D) * dot);
 #pragma unroll
-          for (int i = 0; i < V; ++i) g[i] = ok ? r * (g[i] - x[i] * dot) : 0.f;
+          for (int i = 0; i < V; ++i) {
+            dw[i] += o[i] * r;
+            g[i] = g[i] * (w[i] * r) - x[i] * f;
+          }
         }
         if (live) store_row(out + (h + u) * so.h, g);
       }
@@ -373,9 +390,9 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
   const int64_t oh = kind == 0 ? a.sqo.h : a.skp.h;
   const float* tab = ok ? table_row(a, pos, col == 0) : nullptr;
   const bool pos_ok = ok && (a.rot == 0 || tab != nullptr);
-  const Angles<V, IL> ang = load_angles<V, IL>(tab, pos_ok ? col : D, pos_ok ? a.rot : 0);
-  float w[V];
-  load_weight<V>(kind == 0 ? a.wq : a.wk, col, w);
+  Turn<V, IL> turn(tab, pos_ok ? col : D, pos_ok ? a.rot : 0);
+  turn.weigh(kind == 0 ? a.wq : a.wk, col, a.rot);
+  const int from = partner_lane<V>(col, a.rot);
   for (int h = h0; h < h1; h += kBatch) {
     uint4 raw[kBatch];
 #pragma unroll
@@ -387,8 +404,7 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
     for (int u = 0; u < kBatch; ++u) {
       if (h + u >= h1) break;
       float x[V];
-      unpack<T>(raw[u], x);
-      row_forward<D, V, IL>(x, w, ang, col, a);
+      row_forward<T, D, IL>(raw[u], turn, from, a, x);
       if (!pos_ok)
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = 0.f;
