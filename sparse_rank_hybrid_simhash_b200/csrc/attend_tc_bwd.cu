@@ -1089,8 +1089,7 @@ cudaError_t backward(const AttendArgs& args, cudaStream_t s) {
 
 }  // namespace
 
-size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N) {
-  if (!attend_tc_supported(d, bf16)) return align_up((size_t)(B * H * N) * sizeof(float));
+size_t window_tc_scratch_bytes(int d, int64_t B, int64_t H, int64_t N) {
   return (size_t)(B * H * padded_rows((int)N)) * 2 * sizeof(float) +
          (size_t)kMaxCtas * 2 * 2 * kBlock * d * sizeof(float);
 }

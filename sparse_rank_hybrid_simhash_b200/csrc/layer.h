@@ -85,16 +85,18 @@ struct AttendArgs {
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
+// (a.delta: window_simt_scratch_bytes of workspace, row statistics and partials of shared tiles)
+size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int64_t N);
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 
 // tcgen05 kernels: bf16, d = 64 or 128.
 bool attend_tc_supported(int d, bool bf16);
 cudaError_t launch_window_fwd_tc(const AttendArgs& a, cudaStream_t s);
-// (a.delta: window_scratch_bytes of workspace)
+// (a.delta: window_tc_scratch_bytes of workspace)
 cudaError_t launch_window_bwd_tc(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
-// Workspace bytes of the window backward: row statistics, and partials of cut tiles.
-size_t window_scratch_bytes(int d, bool bf16, int64_t B, int64_t H, int64_t N);
+// Workspace bytes of it: row statistics, and partials of cut tiles.
+size_t window_tc_scratch_bytes(int d, int64_t B, int64_t H, int64_t N);
 // Workspace bytes of launch_paged_tc's partial rows.
 size_t paged_scratch_bytes(int d, int64_t rows, int g);
 // A few rows a sequence (decoding), bf16.

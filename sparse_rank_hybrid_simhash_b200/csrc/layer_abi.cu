@@ -204,7 +204,9 @@ elsaa_status elsaa_window_validate(const elsaa_window_params* p) { return check(
 size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backward) {
   if (check(p) != ELSAA_OK) return 0;
   if (!backward) return kHeadBytes;
-  return kHeadBytes + window_scratch_bytes(p->d, p->dtype == ELSAA_BF16, p->B, p->H, p->N);
+  return kHeadBytes + (attend_tc_supported(p->d, p->dtype == ELSAA_BF16)
+                           ? window_tc_scratch_bytes(p->d, p->B, p->H, p->N)
+                           : window_simt_scratch_bytes(p->d, p->B, p->H, p->Hkv, p->N));
 }
 
 static elsaa_status window_args(const elsaa_window_params* p, const void* const* tensors,

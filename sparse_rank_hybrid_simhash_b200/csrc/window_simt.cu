@@ -440,8 +440,12 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const AttendAr
   }
 }
 
+// `parts` CTAs share a key tile's (head of the group, query block) list; with more than
+// one, each leaves its sums in `partial` ([tile][part][2][ROWS][D]) and the last to
+// come adds them up in order.
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) window_dkv_simt_kernel(const AttendArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads)
+window_dkv_simt_kernel(const AttendArgs a, int tiles, int parts, float* partial) {
   constexpr int RT = ROWS / 16;
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
@@ -450,9 +454,11 @@ __global__ void __launch_bounds__(kThreads) window_dkv_simt_kernel(const AttendA
   float* Gs = Qs + kBlk * pitch<D>();
   float* Ps = Gs + kBlk * pitch<D>();   // [key][query]
   float* Ds = Ps + ROWS * kPs;
+  __shared__ int last;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int bk = blockIdx.x / tiles, b = bk / a.Hkv, hk = bk % a.Hkv;
-  const int j0 = (int)(blockIdx.x % tiles) * ROWS;   // the sinks' tile, the longest, first
+  const int part = blockIdx.x % parts, item = blockIdx.x / parts;
+  const int bk = item / tiles, b = bk / a.Hkv, hk = bk % a.Hkv;
+  const int j0 = item % tiles * ROWS;   // the sinks' tile, the longest, first
   const int len = length_of(a, b);
   auto row = [&](const void* base, const Strides& s, int head, int n) -> const T* {
     return n < len ? static_cast<const T*>(base) + b * s.b + head * s.h + n * s.n : nullptr;
@@ -466,33 +472,64 @@ __global__ void __launch_bounds__(kThreads) window_dkv_simt_kernel(const AttendA
     for (int c = 0; c < D / 16; ++c) ok[x][c] = ov[x][c] = 0.f;
   const int64_t reach = j0 < a.sinks ? len : (int64_t)j0 + ROWS - 1 + a.window;
   const int i_end = (int)(reach < len ? reach : len);   // queries j0 .. i_end - 1 may see the tile
-  for (int h = hk * a.g; h < (hk + 1) * a.g; ++h) {
+  const int nq = i_end > j0 ? (i_end - j0 + kBlk - 1) / kBlk : 0;
+  const int64_t list = (int64_t)nq * a.g;
+  for (int n = (int)(list * part / parts); n < (int)(list * (part + 1) / parts); ++n) {
+    const int h = hk * a.g + n / nq, i0 = j0 + n % nq * kBlk;
     const int64_t rows = ((int64_t)b * a.H + h) * a.N;
-    for (int i0 = j0; i0 < i_end; i0 += kBlk) {
-      __syncthreads();
-      load_tile<T, D, kBlk>(Qs, [&](int r) { return row(a.q, a.sq, h, i0 + r); });
-      load_tile<T, D, kBlk>(Gs, [&](int r) { return row(a.dy, a.sdy, h, i0 + r); });
-      __syncthreads();
-      float s[RT][4], t[RT][4];
-      scores<D, RT>(Ks, Qs, s);
-      scores<D, RT>(Vs, Gs, t);
+    __syncthreads();
+    load_tile<T, D, kBlk>(Qs, [&](int r) { return row(a.q, a.sq, h, i0 + r); });
+    load_tile<T, D, kBlk>(Gs, [&](int r) { return row(a.dy, a.sdy, h, i0 + r); });
+    __syncthreads();
+    float s[RT][4], t[RT][4];
+    scores<D, RT>(Ks, Qs, s);
+    scores<D, RT>(Vs, Gs, t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int i = i0 + tx + 16 * c;
-        const float lse = i < len ? a.lse[rows + i] : 0.f, del = i < len ? a.delta[rows + i] : 0.f;
+    for (int c = 0; c < 4; ++c) {
+      const int i = i0 + tx + 16 * c;
+      const float lse = i < len ? a.lse[rows + i] : 0.f, del = i < len ? a.delta[rows + i] : 0.f;
 #pragma unroll
-        for (int x = 0; x < RT; ++x) {
-          const int j = j0 + RT * ty + x;
-          const bool see = i < len && sees(i, j, a.window, a.sinks);
-          const float p = see ? expf(s[x][c] * a.scale - lse) : 0.f;
-          Ps[(RT * ty + x) * kPs + tx + 16 * c] = p;
-          Ds[(RT * ty + x) * kPs + tx + 16 * c] = see ? p * (t[x][c] - del) * a.scale : 0.f;
-        }
+      for (int x = 0; x < RT; ++x) {
+        const int j = j0 + RT * ty + x;
+        const bool see = i < len && sees(i, j, a.window, a.sinks);
+        const float p = see ? expf(s[x][c] * a.scale - lse) : 0.f;
+        Ps[(RT * ty + x) * kPs + tx + 16 * c] = p;
+        Ds[(RT * ty + x) * kPs + tx + 16 * c] = see ? p * (t[x][c] - del) * a.scale : 0.f;
       }
-      __syncwarp();
-      accumulate<D, RT>(Ps, Gs, ov);
-      accumulate<D, RT>(Ds, Qs, ok);
     }
+    __syncwarp();
+    accumulate<D, RT>(Ps, Gs, ov);
+    accumulate<D, RT>(Ds, Qs, ok);
+  }
+  if (parts > 1) {
+    float* base = partial + (int64_t)item * parts * 2 * ROWS * D;
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      store_cols<float, D>(base + ((int64_t)part * 2 * ROWS + RT * ty + x) * D, ov[x]);
+      store_cols<float, D>(base + (((int64_t)part * 2 + 1) * ROWS + RT * ty + x) * D, ok[x]);
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.counters + item, 1u) == (uint32_t)(parts - 1) ? 1 : 0;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    using C = Cols<D>;
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        float sv = 0.f, sk = 0.f;
+        const int col = C::at(c / C::W) + c % C::W;
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q) {
+          sv += __ldcg(base + ((int64_t)q * 2 * ROWS + RT * ty + x) * D + col);
+          sk += __ldcg(base + (((int64_t)q * 2 + 1) * ROWS + RT * ty + x) * D + col);
+        }
+        ov[x][c] = sv;
+        ok[x][c] = sk;
+      }
+    if (threadIdx.x == 0) a.counters[item] = 0;
   }
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
@@ -535,10 +572,18 @@ cudaError_t dq(const AttendArgs& a, cudaStream_t s) {
   const int tiles = (a.N + R - 1) / R;
   return run(window_dq_simt_kernel<T, D, R>, (int64_t)a.B * a.H * tiles, bytes<D>(R, 2, 2, 1), s, a, tiles);
 }
+// CTAs that share a key tile: as many as give every SM two, at most 16.
+int dkv_parts(int64_t items) {
+  const int64_t p = (296 + items - 1) / items;
+  return (int)(p > 16 ? 16 : p);
+}
 template <typename T, int D, int R>
 cudaError_t dkv(const AttendArgs& a, cudaStream_t s) {
   const int tiles = (a.N + R - 1) / R;
-  return run(window_dkv_simt_kernel<T, D, R>, (int64_t)a.B * a.Hkv * tiles, bytes<D>(R, 2, 2, 2), s, a, tiles);
+  const int64_t items = (int64_t)a.B * a.Hkv * tiles;
+  const int parts = dkv_parts(items);
+  return run(window_dkv_simt_kernel<T, D, R>, items * parts, bytes<D>(R, 2, 2, 2), s, a, tiles, parts,
+             a.delta + align_up((size_t)a.B * a.H * a.N * sizeof(float)) / sizeof(float));
 }
 
 template <typename T, int D>
@@ -571,6 +616,14 @@ struct Launch {
                        : Launch<float, 128>::f(a, s)))
 
 }  // namespace
+
+size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int64_t N) {
+  const int R = small_tiles(B * Hkv, (int)N) ? 16 : 64;
+  const int64_t items = B * Hkv * ((N + R - 1) / R);
+  const int parts = dkv_parts(items);
+  return align_up((size_t)(B * H * N) * sizeof(float)) +
+         (parts > 1 ? (size_t)items * parts * 2 * R * d * sizeof(float) : 0);
+}
 
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.H * a.N, warps = kThreads / 32;

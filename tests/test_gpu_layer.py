@@ -150,6 +150,8 @@ WINDOW = [
     (2, 3, 3, 190, 128, "f32", 1, 0, (65, 190), False),
     (1, 4, 4, 70, 128, "f32", 33, 70, None, False),
     (4, 16, 8, 520, 32, "f32", 200, 3, (520, 0, 64, 65), False),
+    (1, 8, 1, 700, 128, "f32", 0, 0, (650,), False),
+    (1, 8, 1, 400, 32, "bf16", 90, 20, None, True),
     (2, 4, 2, 150, 32, "bf16", 40, 2, (150, 64), False),
 ]
 
