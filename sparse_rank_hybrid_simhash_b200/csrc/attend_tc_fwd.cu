@@ -208,11 +208,20 @@ ELSAA_DEV Item paged_item(const AttendArgs& a, const Shape& sh, int b, int pair,
   return it;
 }
 
+// Blocks of tile pair `pair` (paged_item's nblk; a pair's rows are successive, so its
+// list is that of its first and last row).
+ELSAA_DEV int pair_blocks(const AttendArgs& a, const Shape& sh, int pair, int tokens, int len) {
+  const int t0 = 2 * pair * sh.tt, p_lo = len - tokens + t0;
+  const int p_hi = len - tokens + min(tokens, t0 + 2 * sh.tt) - 1;
+  const int lo = p_lo - a.window + 1, first = lo > 0 ? lo >> 7 : 0;
+  const int s128 = (int)(((int64_t)a.sinks + 127) >> 7);
+  return min(s128, first) + (p_hi >> 7) - first + 1;
+}
 // Units (tile pair, key head, block) of a sequence.
 ELSAA_DEV int64_t seq_units(const AttendArgs& a, const Shape& sh, int tokens, int len) {
   int64_t u = 0;
   const int pairs = pairs_of(tokens, sh.tt);
-  for (int p = 0; p < pairs; ++p) u += paged_item(a, sh, 0, p, 0, 0, tokens, len).nblk;
+  for (int p = 0; p < pairs; ++p) u += pair_blocks(a, sh, p, tokens, len);
   return u * a.Hkv;
 }
 
@@ -257,7 +266,7 @@ ELSAA_DEV Cut find_run(const AttendArgs& a, const Shape& sh, int cta, int ctas, 
       c.len = __shfl_sync(0xffffffffu, len, l);
       const int pairs = pairs_of(c.tokens, sh.tt);
       for (; c.pair < pairs; ++c.pair) {
-        const int blk = paged_item(a, sh, c.b, c.pair, 0, c.start, c.tokens, c.len).nblk;
+        const int blk = pair_blocks(a, sh, c.pair, c.tokens, c.len);
         if (rest < (int64_t)blk * a.Hkv) {
           c.hk = (int)div64(rest, blk);
           c.off = (int)(rest - (int64_t)c.hk * blk);
