@@ -4,8 +4,8 @@
 // are a hundredth of what the bytes cost.  So the work per byte is kept small and many
 // loads in flight: a warp is a pipeline of its own with 16 keys a stage (K and V
 // rows by cp.async into 16-byte chunks swizzled by their row, no barrier but the
-// warp's), four warps a CTA take the 16-key quarters of each 64-key block, two CTAs
-// an SM, 128 KB in flight.  Scores, softmax and output stay in registers: S = Q K^T
+// warp's), four warps a CTA take the 16-key quarters of each 64-key block, two or three
+// CTAs an SM, 128 KB in flight.  Scores, softmax and output stay in registers: S = Q K^T
 // and O += P V by 16 x 8 x 16 tensor instructions (a 128-row tcgen05 tile holds 8 to
 // 16 live rows here, its S, P and O go through TMEM with a barrier each way, and the
 // blocks that wait there take the ring's slots: 50 % of the bandwidth at contexts of
@@ -28,12 +28,14 @@ using namespace tc;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRows = 16, kKeys = 16;        // rows of a tile, keys of a stage
 constexpr float kGrow = 8.0f;                // log2 of the growth that rescales O
+constexpr int kAhead = 4;                    // page lookups in flight
 
 template <int D>
 struct Lay {
   static constexpr int kRow = D * 2;                      // bytes of a row
   static constexpr int kStage = 2 * kKeys * kRow;         // K and V
-  static constexpr int kStages = D == 128 ? 3 : D == 64 ? 6 : 8;
+  static constexpr int kStages = D == 128 ? 3 : D == 64 ? 4 : 8;
+  static constexpr int kCtas = D == 128 ? 2 : 3;          // an SM
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kPitch = D + 4;                    // floats of a joined row
   static constexpr int kDyn = kWarps * kWarpBytes;
@@ -73,7 +75,7 @@ template <int D>
 ELSAA_DEV int place(int c, int r) { return D == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendArgs a, float scale_log2) {
+__global__ void __launch_bounds__(kThreads, Lay<D>::kCtas) paged_decode_kernel(const AttendArgs a, float scale_log2) {
   using L = Lay<D>;
   constexpr int ST = L::kStages, CH = D / 8;   // 16-byte chunks of a row
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -136,7 +138,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendA
     };
 #pragma unroll
     for (int x = 0; x < ST - 1; ++x) load(n0 + x, lookup(n0 + x));
-    int page = lookup(n0 + ST - 1);
+    int ahead[kAhead];   // pages of the next loads (a lookup takes about as long as two blocks)
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) ahead[x] = lookup(n0 + ST - 1 + x);
 
     // Q as the A operand of every K step (rows quad and quad + 8)
     uint32_t qf[D / 16][4];
@@ -230,8 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const AttendA
         }
       }
       __syncwarp();   // the stage has been read by every lane
-      load(n + ST - 1, page);
-      page = lookup(n + ST);
+      load(n + ST - 1, ahead[0]);
+#pragma unroll
+      for (int x = 0; x + 1 < kAhead; ++x) ahead[x] = ahead[x + 1];
+      ahead[kAhead - 1] = lookup(n + ST - 1 + kAhead);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -324,7 +330,8 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(
       paged_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kDyn);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D><<<kRuns, kThreads, Lay<D>::kDyn, s>>>(a, a.scale * 1.4426950408889634f);
+  static_assert(148 * Lay<D>::kCtas <= kRuns, "partials of every CTA");
+  paged_decode_kernel<D><<<148 * Lay<D>::kCtas, kThreads, Lay<D>::kDyn, s>>>(a, a.scale * 1.4426950408889634f);
   return cudaGetLastError();
 }
 

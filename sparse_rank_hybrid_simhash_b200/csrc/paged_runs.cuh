@@ -8,7 +8,7 @@
 namespace elsaa {
 
 constexpr int kBlk = 64;         // keys of a block
-constexpr int kRuns = 296;       // CTAs of a paged call (2 x 148)
+constexpr int kRuns = 444;       // most CTAs of a paged call (3 x 148)
 constexpr int kMinUnits = 2;     // a run shorter than this is not worth a CTA
 
 // Rows of a tile: 16 where a sequence's new (token, head of the group) rows fill no

@@ -589,8 +589,8 @@ cudaError_t dkv(const AttendArgs& a, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t pages(const AttendArgs& a, cudaStream_t s) {
   if (paged_tile_rows(a.rows, a.seqs, a.g) == 16)
-    return run(paged_simt_kernel<T, D, 16>, kRuns, bytes<D>(16, 1, 2, 1), s, a);
-  return run(paged_simt_kernel<T, D, 64>, kRuns, bytes<D>(64, 1, 2, 1), s, a);
+    return run(paged_simt_kernel<T, D, 16>, 296, bytes<D>(16, 1, 2, 1), s, a);
+  return run(paged_simt_kernel<T, D, 64>, 296, bytes<D>(64, 1, 2, 1), s, a);
 }
 
 template <typename T, int D>
