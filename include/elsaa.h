@@ -341,7 +341,9 @@ int32_t elsaa_path_flags(const elsaa_params* p);
  *     and clears, and counters that every call leaves at zero (zero them anew
  *     after ELSAA_ERR_DEVICE_TIMEOUT).
  *   - Two calls that may run at the same time (two streams, two captured
- *     graphs) need a workspace each. */
+ *     graphs) need a workspace each.
+ *   - Outputs overlap no input where this header does not say that they may,
+ *     and no two elements of an output share memory. */
 
 typedef struct {
   int32_t B, H, Hkv, N, d;   /* d in {32, 64, 128} */
@@ -433,14 +435,14 @@ size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p);
 /* The new tokens of sequence b are rows starts[b] .. starts[b + 1] - 1 of q
  * [T, H, d], and the last of the lengths[b] tokens of its context: token t of
  * n has position lengths[b] - n + t.  starts: device int32 [S + 1], never
- * falling, starts[0] = 0.  lengths: device int32 [S], with the new tokens.
+ * falling.  lengths: device int32 [S], with the new tokens.
  * k_pages, v_pages: [pages, Hkv, page_size, d]; token j of sequence b lies in
  * page page_table[b][j / page_size] (device int32 [S, table_width]), slot
  * j % page_size.  Entries that no token of the call needs are not read: behind
  * the length, and before every new token's window and behind the sinks.  A
  * needed entry that is no page, or a length that does not fit, is recorded
  * (DEVICE_CHECK); such a page reads as zeros and is never written.  Rows of q
- * from starts[S] on belong to no sequence.
+ * before starts[0] and from starts[S] on belong to no sequence.
  * strides: q, q_out, k, v as (row, head); page_strides: k_pages, v_pages as
  * (page, head, slot); host arrays of element strides or NULL for dense. */
 
@@ -458,7 +460,7 @@ elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_p
 
 /* Attention of the new tokens over the cache, their own keys and values
  * already written: the serving form of elsaa_window_forward, for any number of
- * new tokens a sequence.  strides: q, y as (row, head).  Rows from starts[S] on
+ * new tokens a sequence.  strides: q, y as (row, head).  Rows of no sequence
  * are left as they were. */
 elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
                                 const int64_t* strides, const void* k_pages, const void* v_pages,

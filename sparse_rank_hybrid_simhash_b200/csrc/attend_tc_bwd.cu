@@ -28,6 +28,9 @@
 // Bound at d = 128: 2048 (dkv) and 1536 (dq) cycles of products a block against
 // 1024 of exponentials and about as many of other instructions; at d = 64 the
 // elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
+// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1316 us (784
+// TFLOP/s by the formulas' five products), d = 64 927 us; text-32k (2 x 12 heads of
+// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 44.
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.

@@ -5,9 +5,10 @@
 // Two streams of 128 query rows share every 128-key block of K and V: S = Q K^T
 // (TMEM), P = 2^(scale log2e S - m) written over S as bf16, O += P V (TMEM).  A stream
 // works on 64-key halves in turn: while its softmax reads one, the tensor cores put
-// the other's P into O and the next S in its place.  (With whole blocks the softmax
-// waited for both products: a block took 3560 cycles of a CTA at d = 128.)  A row
-// belongs to one thread, so maximum, sum and rescaling stay in its registers.  O is
+// the other's P into O and the next S in its place, and a half that no row of the
+// stream sees is skipped.  (With whole blocks the softmax waited for both products; a
+// padded batch at d = 128 171 -> 159 us, prompt chunks 172 -> 154 us, long windows
+// unchanged within 4 %.)  A row belongs to one thread, so maximum, sum and rescaling stay in its registers.  O is
 // rescaled only when a row's maximum has grown by more than 2^8 over the one it
 // used so far (P <= 2^8 otherwise; bf16 keeps the same relative precision there,
 // and the final division cancels the reference): a rare event after the first
@@ -16,9 +17,10 @@
 // Streams of an item:
 //   window, g even    two query heads of one key head at the same 128 tokens
 //   window, g odd     two successive 128-token tiles of one head
-//   pages, long       two successive tiles of (token, head of the group) rows
-//   pages, short      one tile of rows (a decoding step); the streams take
-//                     alternate key blocks and are merged at the end
+//   pages             two successive tiles of (token, head of the group) rows; where
+//                     a sequence's rows fill one tile, the streams take alternate key
+//                     blocks of it and are merged at the end.  (Calls with up to 16 rows
+//                     a sequence on average go to paged_decode.cu.)
 // Paged work is one list of (tile pair, key head, key block) units cut into equal
 // runs, one per CTA (the cuts are found from the lengths on the device, so a
 // captured launch follows them); an item cut between CTAs leaves unnormalised
@@ -37,8 +39,11 @@
 // in shared memory (0 times a stray infinity is not 0).
 //
 // Bound: at d = 128 a block costs 1024 cycles of products and 1024 of
-// exponentials (16 a cycle an SM) a stream, at d = 64 512 and 1024; decoding is
-// bound by the pages' bytes.
+// exponentials (16 a cycle an SM) a stream, at d = 64 512 and 1024; one pair of
+// exponentials in four goes to the FMA pipe (attend_tc.cuh).  What is left over is the
+// chain of a half block: S read from TMEM, maximum, exponentials, P written, handed over.
+// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 413 us (1000
+// TFLOP/s), d = 64 369 us (560); text-32k (2 x 12 heads of d = 64, 32768 tokens) at window 1024 439 us (470).
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.
@@ -345,7 +350,8 @@ ELSAA_DEV Partial partial_row(const AttendArgs& a, const Shape& sh, int d, int s
   return {o + at * d, reinterpret_cast<float2*>(o + slots * sh.slot_rows * d) + at};
 }
 
-// R of them at a time; lanes over the columns.  w: the lane's row's weight of a CTA.
+// R rows of a cut item (merge_rows), from row x0 of the warp's on; lanes over the
+// columns.  m: the maximum of row `lane`.
 template <int D, int R>
 ELSAA_DEV void merge_group(const AttendArgs& a, const Shape& sh, const Item& it, int st, int row0,
                            int x0, int rows, float m) {
@@ -912,7 +918,6 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         mbar_wait(&bars->drain, 0, a.err);
       }
       __syncwarp();
-
     }
   }
   fence_before();

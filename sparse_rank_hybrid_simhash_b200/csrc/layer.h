@@ -74,7 +74,7 @@ struct AttendArgs {
   float scale;
   uint32_t* err;
   uint32_t* counters;         // [CTAs][8 warps], or [CTAs]
-  float* delta;               // [B, H, N]: rowsum(y dy) (backward)
+  float* delta;               // backward: the row statistics and partials
   // pages
   const int32_t *page_table, *starts;
   int seqs, rows, page_size, pages, table_width;
@@ -95,7 +95,7 @@ cudaError_t launch_window_fwd_tc(const AttendArgs& a, cudaStream_t s);
 // (a.delta: window_tc_scratch_bytes of workspace)
 cudaError_t launch_window_bwd_tc(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tc(const AttendArgs& a, cudaStream_t s);
-// Workspace bytes of it: row statistics, and partials of cut tiles.
+// Workspace bytes of launch_window_bwd_tc: row statistics, and partials of cut tiles.
 size_t window_tc_scratch_bytes(int d, int64_t B, int64_t H, int64_t N);
 // Workspace bytes of launch_paged_tc's partial rows.
 size_t paged_scratch_bytes(int d, int64_t rows, int g);

@@ -13,6 +13,7 @@ using namespace elsaa;
 namespace {
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 
 bool head_dim(int d, elsaa_status* why) {
   if (d <= 0) return false;
@@ -142,7 +143,7 @@ elsaa_status elsaa_rotary_forward(const elsaa_rotary_params* p, const void* q, c
   RotaryArgs a = {};
   const elsaa_status st = rotary_args(p, table, q_weight, k_weight, ws, ws_bytes, &a);
   if (st != ELSAA_OK) return st;
-  if (!q || !qo || (k == nullptr) != (ko == nullptr)) return ELSAA_ERR_INVALID_ARG;
+  if (!q || !qo || (k == nullptr) != (ko == nullptr) || !aligned4(positions)) return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k, (const void*)qo, (const void*)ko})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
   const int e = esize(p->dtype);
@@ -174,6 +175,8 @@ elsaa_status elsaa_rotary_backward(const elsaa_rotary_params* p, const void* q, 
   if (!q || !dqo || !dq || (k == nullptr) != (dko == nullptr) || (k == nullptr) != (dk == nullptr))
     return ELSAA_ERR_INVALID_ARG;
   if (!p->norm && (dq_weight || dk_weight)) return ELSAA_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)positions, (const void*)dq_weight, (const void*)dk_weight})
+    if (!aligned4(x)) return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k, dqo, dko, (const void*)dq, (const void*)dk})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
   const int e = esize(p->dtype);
@@ -251,7 +254,7 @@ elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, c
   const void* t[4] = {q, k, v, y};
   const elsaa_status st = window_args(p, t, 4, strides, lengths, ws, ws_bytes, false, &a);
   if (st != ELSAA_OK) return st;
-  if (!lse) return ELSAA_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse) || !aligned4(lengths)) return ELSAA_ERR_INVALID_ARG;
   a.lse = lse;
   const bool bf16 = p->dtype == ELSAA_BF16;
   return cuda_status(attend_tc_supported(p->d, bf16)
@@ -267,7 +270,7 @@ elsaa_status elsaa_window_backward(const elsaa_window_params* p, const void* q, 
   const void* t[8] = {q, k, v, y, dy, dq, dk, dv};
   const elsaa_status st = window_args(p, t, 8, strides, lengths, ws, ws_bytes, true, &a);
   if (st != ELSAA_OK) return st;
-  if (!lse) return ELSAA_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse) || !aligned4(lengths)) return ELSAA_ERR_INVALID_ARG;
   a.lse = const_cast<float*>(lse);
   a.dy = dy;
   a.dq = dq;
@@ -323,6 +326,8 @@ elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_p
     return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_pages, (const void*)v_pages})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
+  for (const void* x : {page_table, starts, lengths})
+    if (!aligned4(x)) return ELSAA_ERR_INVALID_ARG;
   if (ws_bytes < kHeadBytes) return ELSAA_ERR_WORKSPACE;
   const int e = esize(p->dtype);
   auto take = [&](int i, int h, Strides* to) {
@@ -359,6 +364,8 @@ elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
     return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k_pages, v_pages, (const void*)y})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
+  for (const void* x : {page_table, starts, lengths})
+    if (!aligned4(x)) return ELSAA_ERR_INVALID_ARG;
   if (((uintptr_t)ws & 255) != 0) return ELSAA_ERR_INVALID_ARG;
   if (ws_bytes < elsaa_paged_workspace_bytes(p)) return ELSAA_ERR_WORKSPACE;
   AttendArgs a = {};

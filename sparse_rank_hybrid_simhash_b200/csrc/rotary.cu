@@ -15,10 +15,11 @@
 // away and come over as the raw 16 bytes.  A group walks several heads of its token
 // and keeps what does not depend on the head in registers, weight and angle folded:
 //   y_i = r (x_i A_i + x_o B_i),  A_i = w_i cos,  B_i = -+ w_o sin  (o: i's partner)
-// (text-32k queries and keys, rotating after the norm: 80 us, issue active 74 % of the
-// time).  Two or four heads' rows are in flight at a time (an output may be its
-// input, so the compiler must keep a later row's load behind an earlier store: 102 us
-// without).
+// (text-32k queries and keys, 2 x 12 heads of d = 64 over 32768 tokens: 74 us, issue
+// active 74 % of the time; backward 176 and the weights' sums 5).  Four heads' rows are
+// in flight at a time, the first of them while the angles are fetched (an output may be
+// its input, so the compiler must keep a later row's load behind an earlier store: 102 us
+// without); in the backward two heads' x and dy.
 #include "common.cuh"
 #include "internal.h"
 #include "layer.h"
@@ -346,7 +347,7 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
   const int col = (threadIdx.x % LANES) * V;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
   const int end = min(st[a.seqs], a.N);
-  const bool live = row < end;
+  const bool live = row >= st[0] && row < end;
   // the last sequence that starts at or before the row (empty ones share a start)
   int lo = 0, hi = a.seqs - 1;
   while (live && lo < hi) {

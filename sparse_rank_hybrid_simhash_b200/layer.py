@@ -49,8 +49,8 @@ def check(where: str, t: torch.Tensor, shape: Sequence[int], dtype: torch.dtype,
 
 def strided(t: torch.Tensor) -> bool:
     """Whether the library takes the tensor where it lies: the last dimension
-    contiguous, the other strides positive multiples of 16 bytes that no two
-    rows share, the start on 16 bytes."""
+    contiguous, the other strides multiples of 16 bytes and at least a row, the
+    start on 16 bytes."""
     if t.data_ptr() & 15:
         return False
     if t.is_contiguous():
@@ -58,6 +58,19 @@ def strided(t: torch.Tensor) -> bool:
     e, d = t.element_size(), t.shape[-1]
     return t.stride(-1) == 1 and all(n == 1 or (s >= d and s * e % 16 == 0)
                                      for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+
+
+def rows_apart(t: torch.Tensor) -> bool:
+    """Whether no two elements of a strided tensor share memory (by its dimensions one inside
+    the other, as every view of a dense tensor has them)."""
+    if t.is_contiguous():
+        return True
+    end = 0                # the last offset of the smaller strides' dimensions
+    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if s <= end:
+            return False
+        end += s * (n - 1)
+    return True
 
 
 def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
@@ -78,9 +91,9 @@ def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device,
             return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     check(where, t, shape, dtype, device)
-    if not strided(t):
-        raise ValueError(f"{where}: an output needs a contiguous last dimension and strides and "
-                         "a start that are multiples of 16 bytes")
+    if not strided(t) or not rows_apart(t):
+        raise ValueError(f"{where}: an output needs a contiguous last dimension, strides and a "
+                         "start that are multiples of 16 bytes, and no two elements in one place")
     return t
 
 

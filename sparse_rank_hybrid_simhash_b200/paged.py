@@ -6,8 +6,8 @@ optional window and sinks.
 The rows starts[b] .. starts[b + 1] - 1 of q [T, H, d] are the new tokens of
 sequence b and the last of its lengths[b] context tokens.  Token j of sequence b
 lies in page page_table[b, j // page_size], slot j % page_size, of k_pages and
-v_pages [pages, Hkv, page_size, d].  A sequence may have no new tokens; rows from
-starts[S] on are left as they were.  Sequences may share pages (a common prefix)
+v_pages [pages, Hkv, page_size, d].  A sequence may have no new tokens; rows before
+starts[0] and from starts[S] on are left as they were.  Sequences may share pages (a common prefix)
 as long as no call writes a slot twice.
 """
 
@@ -60,8 +60,9 @@ def _cache(p: PagedParams, k_pages, v_pages, page_table, starts, lengths, dev):
     shape = (p.pages, p.Hkv, p.page_size, p.d)
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         layer.check(name, t, shape, dt, dev)
-        if not layer.strided(t):
-            raise ValueError(f"{name}: strides and start must be multiples of 16 bytes")
+        if not layer.strided(t) or not layer.rows_apart(t):
+            raise ValueError(f"{name}: a contiguous last dimension, strides and a start that are "
+                             "multiples of 16 bytes, and no two elements in one place")
     return (k_pages, v_pages,
             layer.as_small("page_table", page_table, (p.seqs, p.table_width), torch.int32, dev),
             layer.as_small("starts", starts, (p.seqs + 1,), torch.int32, dev),

@@ -129,8 +129,7 @@ class NormRotateFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, table, q_weight, k_weight, positions, params: RotaryParams):
-        ws = alloc_workspace(params, q.device)
-        qo, ko = forward(params, q, k, table, q_weight, k_weight, positions, ws=ws)
+        qo, ko = forward(params, q, k, table, q_weight, k_weight, positions)
         ctx.params = params
         ctx.save_for_backward(q, k, table, q_weight, k_weight, positions)
         return qo, ko
@@ -148,7 +147,7 @@ class NormRotateFunction(torch.autograd.Function):
 def norm_rotate(q, k, table=None, q_weight=None, k_weight=None, positions=None, rot_dim=None,
                 interleaved=False, norm=True, eps=1e-6):
     """Differentiable norm and rotation of q [B, H, N, d] and k [B, Hkv, N, d]; ``table`` as
-    ``angle_table`` makes it (None: norm only)."""
+    ``angle_table`` makes it (None: norm only).  In a captured step as ``window.window_attention``."""
     B, H, N, d = q.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")

@@ -115,7 +115,11 @@ class WindowFunction(torch.autograd.Function):
 
 
 def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0):
-    """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d]."""
+    """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d].
+
+    A step captured in a CUDA graph must find no eager autograd graph of the same leaves alive
+    (an output not yet dropped or detached): autograd would sum their gradients on that graph's
+    stream, which breaks the capture."""
     B, H, N, d = q.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")

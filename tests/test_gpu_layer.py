@@ -273,6 +273,8 @@ PAGED = [
     (2, 2, 64, "f32", 16, 700, 5, [(100, 1500), (1, 1200)]),
     (8, 4, 32, "f32", 16, 0, 0, [(1, 1 + 53 * b) for b in range(40)]),
     (8, 8, 64, "bf16", 128, 128, 0, [(1, 1 + 37 * b) for b in range(70)]),
+    # a prompt's chunk among single tokens (few rows a sequence on average)
+    (8, 2, 128, "bf16", 16, 0, 0, [(1, 60 + b) for b in range(7)] + [(40, 500)] + [(1, 90)] * 9),
 ]
 
 
@@ -410,6 +412,24 @@ def test_paged_write(cuda_device, case):
     assert torch.equal(kp, k0) and torch.equal(vp, v0)
 
 
+def test_paged_first_row_of_no_sequence(cuda_device):
+    """Rows before starts[0] belong to no sequence either."""
+    p, q, kp, vp, table, starts, lengths = paged_inputs((4, 2, 64, "bf16", 16, 0, 0, [(2, 20), (3, 40)]))
+    starts = starts + 1
+    k, v = (rand((p.rows, 2, 64), torch.bfloat16, s) for s in (1, 2))
+    rp = rotary.RotaryParams.make(1, 4, 2, 1, 64, "bf16", 0)
+    kw, vw = torch.zeros_like(kp), torch.zeros_like(vp)
+    qo = torch.full_like(q, 5.0)
+    paged.write(p, rp, q, k, v, None, None, None, kw, vw, table, starts, lengths, qo=qo)
+    assert (qo[0] == 5.0).all() and (qo[6:] == 5.0).all() and (qo[1:6] != 5.0).any()
+    assert int(vw.abs().sum(-1).gt(0).sum()) == 5 * 2
+    y = torch.full_like(q, 5.0)
+    paged.attend(p, q, kp, vp, table, starts, lengths, y=y)
+    want, tol = ref.paged(q[1:], kp, vp, table, starts - 1, lengths, 0, 0)
+    ref.close(y[1:6], want[:5], tol[:5])
+    assert (y[0] == 5.0).all() and (y[6:] == 5.0).all()
+
+
 def test_paged_write_bad_entries(cuda_device):
     p, q, kp, vp, table, starts, lengths = paged_inputs((4, 2, 64, "bf16", 16, 0, 0, [(2, 20), (3, 40)]))
     k, v = (rand((p.rows, 2, 64), torch.bfloat16, s) for s in (1, 2))
@@ -529,6 +549,79 @@ def test_another_stream_and_graphs(cuda_device):
         B.check(ws)
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 32), ("f32", 128)])
+def test_offsets_past_32_bits(cuda_device, dt, d):
+    """Batches and pages whose strides put an element's offset past 2^31 values."""
+    far, dtype = 2 ** 31 + 2 ** 16, DT[dt]
+    room = torch.empty(far + 2 ** 20, dtype=dtype, device=cuda_device)
+
+    def apart(x, at):      # x [2, ...] with its halves `far` values apart, at an offset
+        to = room.as_strided(x.shape, (far, *x.stride()[1:]), at)
+        to.copy_(x)
+        return to
+
+    p, q, k, v, dy, _ = window_inputs((2, 4, 2, 150, d, dt, 60, 2, None, False))
+    want = window.forward(p, q, k, v)
+    grads = window.backward(p, q, k, v, *want, dy)
+    size = 4 * 150 * d
+    fq, fk, fv = (apart(t, i * size) for i, t in enumerate((q, k, v)))
+    y = apart(torch.zeros_like(q), 3 * size)
+    _, lse = window.forward(p, fq, fk, fv, y=y)
+    assert torch.equal(y, want[0]) and torch.equal(lse, want[1])
+    outs = [apart(torch.zeros_like(t), (4 + i) * size) for i, t in enumerate((q, k, v))]
+    window.backward(p, fq, fk, fv, y, lse, dy, dq=outs[0], dk=outs[1], dv=outs[2])
+    assert all(torch.equal(a, b) for a, b in zip(outs, grads))
+    table = rotary.angle_table(150, d, device=cuda_device)
+    rp = rotary.RotaryParams.make(2, 4, 2, 150, d, dt, d, 150)
+    rotary.forward(rp, fq, fk, table, qo=y, ko=outs[1])
+    for a, b in zip((y, outs[1]), rotary.forward(rp, q, k, table)):
+        assert torch.equal(a, b)
+    # a pool whose page stride puts the second half of its pages there, decoding and in chunks
+    for new in (1, 40):
+        pp, pq, kp, vp, pages, starts, lengths = paged_inputs(
+            (4, 2, d, dt, 16, 0, 0, [(new, 64), (new, 50)]), spare=0, slack=0)
+        kp, vp = kp.nan_to_num(), vp.nan_to_num()
+        wide = far // (pp.pages - 1) // 8 * 8 + 8      # the last page starts past 2^31
+        fk, fv = (room.as_strided(kp.shape, (wide, *kp.stride()[1:]), i * 2 * 16 * d) for i in range(2))
+        fk.copy_(kp), fv.copy_(vp)
+        assert (pp.pages - 1) * wide > 2 ** 31
+        y1 = paged.attend(pp, pq, kp, vp, pages, starts, lengths)
+        assert torch.equal(paged.attend(pp, pq, fk, fv, pages, starts, lengths), y1)
+        k1, v1 = (rand((pp.rows, 2, d), dtype, 60 + i) for i in range(2))
+        rp = rotary.RotaryParams.make(1, 4, 2, 1, d, dt, d, 150)
+        for a, b in ((kp, vp), (fk, fv)):
+            paged.write(pp, rp, pq, k1, v1, table, None, None, a, b, pages, starts, lengths)
+        assert torch.equal(kp, fk) and torch.equal(vp, fv)
+
+
+def test_training_step_in_a_graph(cuda_device):
+    """Forward and gradients of the training operators captured through autograd, replayed on new inputs."""
+    _, q, k, v, dy, _ = window_inputs((1, 4, 2, 200, 64, "bf16", 64, 2, None, False))
+    wq, wk = (1 + 0.1 * rand((64,), torch.float32, s) for s in (5, 6))
+    leaves = [t.requires_grad_() for t in (q, k, v, wq, wk)]
+    table = rotary.angle_table(200, 64, device=cuda_device)
+
+    def step():
+        qo, ko = rotary.norm_rotate(q, k, table, wq, wk)
+        y = window.window_attention(qo, ko, v, window=64, sinks=2)
+        return (y.detach(), *torch.autograd.grad(y, leaves, dy))   # (no autograd graph outlives the step)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    with torch.no_grad():
+        q.copy_(q.flip(2)), v.mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
 def test_refusals_on_the_device(cuda_device):
     p, q, k, v, dy, _ = window_inputs((1, 2, 2, 127, 64, "bf16", 16, 0, None, False))
     with pytest.raises(TypeError):
@@ -544,3 +637,6 @@ def test_refusals_on_the_device(cuda_device):
     assert e.value.code == 3
     with pytest.raises(ValueError):
         rotary.norm_rotate(q, k, rotary.angle_table(8, 64, device=cuda_device)[:, :, 0])
+    with pytest.raises(ValueError):       # rows that share memory
+        window.forward(p, q, k, v, y=torch.zeros(2 * 127 * 64, dtype=q.dtype, device=cuda_device)
+                       .as_strided((1, 2, 127, 64), (0, 64, 64, 1)))

@@ -105,7 +105,8 @@ def test_window_refusals():
         nbytes = window.workspace_bytes(p, False) if nbytes is None else nbytes
         return L.elsaa_window_forward(ctypes.byref(p), q, GOOD, GOOD, strides, NULL, y, lse, ws, nbytes, NULL)
 
-    for kw in (dict(q=NULL), dict(q=BAD), dict(y=NULL), dict(lse=NULL), dict(ws=NULL), dict(ws=BAD)):
+    for kw in (dict(q=NULL), dict(q=BAD), dict(y=NULL), dict(lse=NULL), dict(lse=GOOD + 2), dict(ws=NULL),
+               dict(ws=BAD)):
         assert fwd(**kw) == 1, kw
     assert fwd(nbytes=255) == 3
     s = [8 * 6400, 6400, 64, 2 * 6400, 6400, 64, 2 * 6400, 6400, 64, 8 * 6400, 6400, 64]
@@ -127,7 +128,7 @@ def test_paged_refusals():
         nbytes = paged.workspace_bytes(p) if nbytes is None else nbytes
         return L.elsaa_paged_attend(ctypes.byref(p), q, NULL, GOOD, GOOD, ps, pt, GOOD, GOOD, GOOD, ws, nbytes, NULL)
 
-    for kw in (dict(q=NULL), dict(q=BAD), dict(pt=NULL), dict(ws=NULL), dict(ws=BAD),
+    for kw in (dict(q=NULL), dict(q=BAD), dict(pt=NULL), dict(pt=GOOD + 2), dict(ws=NULL), dict(ws=BAD),
                dict(ps=i64(2048, 0, 64, 2048, 1024, 64))):
         assert attend(**kw) == 1, kw
     assert attend(nbytes=paged.workspace_bytes(p) - 1) == 3
@@ -149,6 +150,11 @@ def test_python_checks():
         assert layer.strided(t) == taken
     with pytest.raises(ValueError):
         layer.as_output("y", x[:, :1].expand(1, 4, 8, 32), (1, 4, 8, 32), torch.float32, x.device)
+    with pytest.raises(ValueError):          # heads of one token overlap tokens of one head
+        layer.as_output("y", torch.zeros(11 * 32).as_strided((1, 4, 8, 32), (0, 32, 32, 1)), (1, 4, 8, 32),
+                        torch.float32, x.device)
+    for t in (x, x.transpose(1, 2).contiguous().transpose(1, 2), torch.zeros(1, 4, 8, 64)[..., :32]):
+        assert layer.as_output("y", t, (1, 4, 8, 32), torch.float32, x.device) is t
     y = layer.as_input("q", x[:, :1].expand(1, 4, 8, 32), (1, 4, 8, 32), torch.float32, x.device)
     assert y.is_contiguous()
     with pytest.raises(TypeError):
