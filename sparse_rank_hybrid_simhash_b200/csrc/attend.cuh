@@ -13,6 +13,25 @@ ELSAA_DEV bool sees(int i, int j, int window, int sinks) {
   return j <= i && (i - j < window || j < sinks);
 }
 
+// How many keys the query at position i sees, and the x-th of them.
+ELSAA_DEV int seen_keys(int i, int window, int sinks) {
+  const int lo = max(i - window + 1, 0);
+  return i - lo + 1 + min(sinks, lo);
+}
+ELSAA_DEV int seen_key(int x, int i, int window, int sinks) {
+  const int lo = max(i - window + 1, 0), s = min(sinks, lo);
+  return x < s ? x : lo + x - s;
+}
+
+// The backward's delta_i = y_i . dy_i takes y as it was stored.  For rows that see few
+// keys that is a large part of dS = p (dy v - delta), a difference of like numbers: at
+// bf16 and two keys dq and dk were off by 0.004 to 0.007 of their norm, at 32 keys by no
+// more than the other roundings (0.0025).  So rows with up to this many keys take delta
+// from its other form, sum_j p_ij dy_i . v_j, in fp32 (0.0024 to 0.0030): all rows of
+// windows that short (2 x 12 heads of d = 64, 32768 tokens: the backward at window 16 893
+// us, at 17 542), else the first of each sequence.
+constexpr int kFewKeys = 16;
+
 // The key blocks (of `size` keys) of a tile whose rows lie at positions
 // p_lo .. p_hi: the sinks' blocks before the window, then the window's.
 struct KeyBlocks {

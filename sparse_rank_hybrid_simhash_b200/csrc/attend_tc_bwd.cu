@@ -30,7 +30,7 @@
 // elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
 // Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1316 us (784
 // TFLOP/s by the formulas' five products), d = 64 927 us; text-32k (2 x 12 heads of
-// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 44.
+// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 58.
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.
@@ -101,6 +101,54 @@ ELSAA_DEV int length_of(const AttendArgs& a, int b) {
 
 // ---- row statistics (and the zeros of empty tiles) ------------------------------------------------------------
 
+// -delta of row x from sum_j p_j dy . v_j where it sees at most kFewKeys keys, by its lane
+// group; the whole warp takes as many turns as one of its rows needs.  c: the lane's first
+// column.
+template <int D>
+ELSAA_DEV void few_delta(const AttendArgs& a, const Stats& st, int x, int rows, int c) {
+  constexpr int LANES = D / 8;
+  const int pad = (int)st.pad, bh = x / pad, n = x - bh * pad, b = bh / a.H, h = bh - b * a.H;
+  const bool mine = x < rows && n < length_of(a, b) && seen_keys(n, a.window, a.sinks) <= kFewKeys;
+  const int few = mine ? seen_keys(n, a.window, a.sinks) : 0;
+  const int turns = __reduce_max_sync(0xffffffffu, few);
+  if (turns == 0) return;
+  const auto at = [&](const void* base, const Strides& s, int head, int64_t j, bool in) {
+    return in ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + b * s.b +
+                                                head * s.h + j * s.n + c)
+              : make_uint4(0, 0, 0, 0);
+  };
+  const auto dot = [](const uint4& y, const uint4& z) {
+    const uint32_t ya[4] = {y.x, y.y, y.z, y.w}, za[4] = {z.x, z.y, z.z, z.w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s += __uint_as_float(ya[e] << 16) * __uint_as_float(za[e] << 16) +
+           __uint_as_float(ya[e] & 0xffff0000u) * __uint_as_float(za[e] & 0xffff0000u);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  };
+  const uint4 q = at(a.q, a.sq, h, n, mine), g = at(a.dy, a.sdy, h, n, mine);
+  const float nl = mine ? a.lse[(int64_t)bh * a.N + n] * -1.4426950408889634f : 0.f;
+  float sum = 0.f;
+  for (int t = 0; t < turns; t += 4) {
+    uint4 k[4], v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = t + e < few;
+      const int64_t j = in ? seen_key(t + e, n, a.window, a.sinks) : 0;
+      k[e] = at(a.k, a.sk, h / a.g, j, in);
+      v[e] = at(a.v, a.sv, h / a.g, j, in);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float s = dot(q, k[e]), r = dot(g, v[e]);
+      if (t + e < few) sum += ex2(s * (a.scale * 1.4426950408889634f) + nl) * r;
+    }
+  }
+  if (mine && c == 0) st.nd[x] = -sum;
+}
+
 // Four rows a lane group, all their loads in flight before the first sum.
 constexpr int kStatRows = 4;
 template <int D>
@@ -111,7 +159,7 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
   const int x0 = (int)blockIdx.x * (ROWS * kStatRows) + threadIdx.x / LANES;
   uint4 u[kStatRows], w[kStatRows];
   float nl[kStatRows];
-  bool empty[kStatRows];
+  bool empty[kStatRows], few = false;
 #pragma unroll
   for (int i = 0; i < kStatRows; ++i) {
     const int x = x0 + i * ROWS;
@@ -121,6 +169,7 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
     if (x < rows) {
       const int bh = x / pad, n = x - bh * pad, b = bh / a.H, h = bh - b * a.H, len = length_of(a, b);
       if (n < len) {
+        few |= seen_keys(n, a.window, a.sinks) <= kFewKeys;
         u[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) + b * a.sy.b +
                                                h * a.sy.h + n * a.sy.n + c);
         w[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy) + b * a.sdy.b +
@@ -160,6 +209,11 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
       }
     }
   }
+  // rows that see few keys, read anew (text-32k 58 us; 44 without them, 72 with them in the
+  // loop above)
+  if (!__any_sync(0xffffffffu, few)) return;
+#pragma unroll 1
+  for (int i = 0; i < kStatRows; ++i) few_delta<D>(a, st, x0 + i * ROWS, rows, c);
 }
 
 // ---- shared pieces ---------------------------------------------------------------

@@ -378,6 +378,25 @@ __global__ void __launch_bounds__(kThreads) window_delta_kernel(const AttendArgs
     for (int c = lane; c < a.d; c += 32) s += to_f32(y[c]) * to_f32(g[c]);
   }
   s = warp_sum(s);
+  // bf16 rows that see few keys (kFewKeys)
+  if (sizeof(T) == 2 && n < length_of(a, b) && seen_keys(n, a.window, a.sinks) <= kFewKeys) {
+    const int few = seen_keys(n, a.window, a.sinks), hk = h / a.g;
+    const T* q = static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h + n * a.sq.n;
+    const T* g = static_cast<const T*>(a.dy) + b * a.sdy.b + h * a.sdy.h + n * a.sdy.n;
+    const float lse = a.lse[row];
+    s = 0.f;
+    for (int x = 0; x < few; ++x) {
+      const int64_t j = seen_key(x, n, a.window, a.sinks);
+      const T* k = static_cast<const T*>(a.k) + b * a.sk.b + hk * a.sk.h + j * a.sk.n;
+      const T* v = static_cast<const T*>(a.v) + b * a.sv.b + hk * a.sv.h + j * a.sv.n;
+      float e = 0.f, r = 0.f;
+      for (int c = lane; c < a.d; c += 32) {
+        e += to_f32(q[c]) * to_f32(k[c]);
+        r += to_f32(g[c]) * to_f32(v[c]);
+      }
+      s += expf(warp_sum(e) * a.scale - lse) * warp_sum(r);
+    }
+  }
   if (lane == 0) a.delta[row] = s;
 }
 

@@ -26,9 +26,10 @@ def visible(n_q, n_k, first, window, sinks, device):
     return (j <= i) & (near | (j < sinks))
 
 
-def attention(q, k, v, see, scale, dt, dy=None):
+def attention(q, k, v, see, scale, dt, dy=None, few=0):
     """q [..., n, d], k, v [..., m, d] in fp64, see [..., n, m].  Values y, lse (and dq, dk, dv
-    of sum(y dy)) and their bounds, as two dicts."""
+    of sum(y dy)) and their bounds, as two dicts.  few: rows with up to so many keys sum
+    delta = y dy over their keys (the others' has y's rounding)."""
     d, m, n = q.shape[-1], k.shape[-2], q.shape[-2]
     u = unit(dt)
     up = u if dt == torch.bfloat16 else 0.0
@@ -55,6 +56,9 @@ def attention(q, k, v, see, scale, dt, dy=None):
     dp = dy @ v.transpose(-1, -2)
     ds = p * (dp - delta)
     tdelta = (dy.abs() * ty).sum(-1, keepdim=True) + (d + 2) * F32 * (dy * y).abs().sum(-1, keepdim=True)
+    tfew = (p * ((es + e_row + (m + 4) * F32) * dp.abs() + (d + 4) * F32 * (dy.abs() @ v.abs().transpose(-1, -2)))
+            ).sum(-1, keepdim=True)
+    tdelta = torch.where(see.sum(-1, keepdim=True) <= few, tfew, tdelta)
     tds = p * (e * (dp - delta).abs() + tdelta + (d + 4) * F32 * (dy.abs() @ v.abs().transpose(-1, -2))) \
         + up * ds.abs()
     val["dq"] = scale * (ds @ k)
@@ -66,7 +70,7 @@ def attention(q, k, v, see, scale, dt, dy=None):
     return val, tol
 
 
-def window(q, k, v, win, sinks, lengths=None, scale=0.0, dy=None):
+def window(q, k, v, win, sinks, lengths=None, scale=0.0, dy=None, few=0):
     """[B, H, N, d] and [B, Hkv, N, d] of the kernels' dtype: (values, bounds) of y, lse, dq, dk, dv."""
     B, H, N, d = q.shape
     Hkv, g, dt = k.shape[1], H // k.shape[1], q.dtype
@@ -83,7 +87,8 @@ def window(q, k, v, win, sinks, lengths=None, scale=0.0, dy=None):
     def keys(x):
         return torch.where(ok, x.double().view(B, Hkv, 1, N, d), 0.0)
 
-    val, tol = attention(grouped(q), keys(k), keys(v), see, scale, dt, None if dy is None else grouped(dy))
+    val, tol = attention(grouped(q), keys(k), keys(v), see, scale, dt, None if dy is None else grouped(dy),
+                         few)
     u = unit(dt)
     for x in val:
         if x in ("dk", "dv"):   # one sum over the group's heads, one rounding

@@ -188,6 +188,20 @@ def test_window(cuda_device, case):
     assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), again))
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("N,win,sinks", [(1, 0, 0), (2, 0, 0), (3, 9, 1), (16, 0, 0), (40, 2, 0), (150, 1, 0),
+                                         (200, 7, 9), (300, 16, 0), (33, 14, 2)])
+def test_window_few_keys(cuda_device, d, N, win, sinks):
+    """Rows that see at most 16 keys take no part of y's rounding into their gradients."""
+    for heads_, lens in (((2, 2), None), ((8, 1), (N, N // 2))):
+        case = (2, *heads_, N, d, "bf16", win, sinks, lens, lens is not None)
+        p, q, k, v, dy, n = window_inputs(case, seed=90)
+        val, tol = ref.window(q, k, v, win, sinks, n, dy=dy, few=16)
+        y, lse = window.forward(p, q, k, v, lengths=n)
+        for name, g in zip(("dq", "dk", "dv"), window.backward(p, q, k, v, y, lse, dy, lengths=n)):
+            ref.close(g, val[name], tol[name], name)
+
+
 def test_window_large_scores(cuda_device):
     """Row maxima that grow along the keys by far more than a rescaling threshold, and that fall."""
     for flip in (False, True):
