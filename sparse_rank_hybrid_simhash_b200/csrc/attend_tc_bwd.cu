@@ -30,7 +30,7 @@
 // elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
 // Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1316 us (784
 // TFLOP/s by the formulas' five products), d = 64 927 us; text-32k (2 x 12 heads of
-// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 58.
+// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 49.
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.
@@ -156,10 +156,14 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
   const int c = (threadIdx.x % LANES) * 8;
   const int pad = (int)st.pad, rows = a.B * a.H * pad;   // (below 2^31)
-  const int x0 = (int)blockIdx.x * (ROWS * kStatRows) + threadIdx.x / LANES;
+  // (a block's rows are one head's; the first blocks of all heads, which may hold rows that
+  // see few keys, go first)
+  static_assert(kBlock % (ROWS * kStatRows) == 0, "blocks within a head");
+  const int heads = a.B * a.H, n0 = (int)blockIdx.x / heads * (ROWS * kStatRows);
+  const int x0 = (int)blockIdx.x % heads * pad + n0 + threadIdx.x / LANES;
   uint4 u[kStatRows], w[kStatRows];
   float nl[kStatRows];
-  bool empty[kStatRows], few = false;
+  bool empty[kStatRows];
 #pragma unroll
   for (int i = 0; i < kStatRows; ++i) {
     const int x = x0 + i * ROWS;
@@ -169,7 +173,6 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
     if (x < rows) {
       const int bh = x / pad, n = x - bh * pad, b = bh / a.H, h = bh - b * a.H, len = length_of(a, b);
       if (n < len) {
-        few |= seen_keys(n, a.window, a.sinks) <= kFewKeys;
         u[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) + b * a.sy.b +
                                                h * a.sy.h + n * a.sy.n + c);
         w[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy) + b * a.sdy.b +
@@ -209,9 +212,9 @@ __global__ void __launch_bounds__(256) stats_kernel(const AttendArgs a, const St
       }
     }
   }
-  // rows that see few keys, read anew (text-32k 58 us; 44 without them, 72 with them in the
-  // loop above)
-  if (!__any_sync(0xffffffffu, few)) return;
+  // rows that see few keys, read anew (in the loop above: text-32k 72 us); later rows of a
+  // head see no fewer
+  if (seen_keys(n0, a.window, a.sinks) > kFewKeys) return;
 #pragma unroll 1
   for (int i = 0; i < kStatRows; ++i) few_delta<D>(a, st, x0 + i * ROWS, rows, c);
 }
