@@ -73,6 +73,11 @@ def rows_apart(t: torch.Tensor) -> bool:
     return True
 
 
+def like(t: torch.Tensor) -> torch.Tensor:
+    """A new dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
     """The checked tensor, or a dense copy of one the library does not take
     where it lies (a broadcast one, an odd stride or offset)."""
@@ -83,13 +88,8 @@ def as_input(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device,
-              like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The checked output, or a new dense one (``like``: of this shape and type)."""
-    if t is None:
-        if like is not None and like.is_contiguous():
-            return torch.empty_like(like)
-        return torch.empty(shape, dtype=dtype, device=device)
+def as_output(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
+    """The checked output, refused where the library does not take it where it lies."""
     check(where, t, shape, dtype, device)
     if not strided(t) or not rows_apart(t):
         raise ValueError(f"{where}: an output needs a contiguous last dimension, strides and a "
@@ -97,10 +97,8 @@ def as_output(where: str, t: Optional[torch.Tensor], shape, dtype, device,
     return t
 
 
-def as_small(where: str, t: Optional[torch.Tensor], shape, dtype, device) -> Optional[torch.Tensor]:
-    """An optional int32 / fp32 tensor, dense and on 16 bytes (copied where it is not)."""
-    if t is None:
-        return None
+def as_small(where: str, t: torch.Tensor, shape, dtype, device) -> torch.Tensor:
+    """The checked int32 / fp32 tensor, dense and on 16 bytes (copied where it is not)."""
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         check(where, t, shape, dtype, device)
     if t.is_contiguous() and not t.data_ptr() & 15:
@@ -119,6 +117,29 @@ def as_workspace(ws: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
     return ws
 
 
+def place(device: torch.device, dims: int, *specs):
+    """The addresses of a call's tensors, the strides of their first ``dims`` dimensions (None:
+    all are dense) and what has to live until the launch.  A spec is (name, tensor or None, shape,
+    dtype, how): ``how`` (as_input, as_output, ...) checks and places a tensor that is not dense
+    and on 16 bytes.  (One pass over the tensors: a call's host time is mostly these checks.)"""
+    at = []
+    for _, t, shape, dtype, _ in specs:
+        if t is None:
+            at.append(None)
+        elif t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+            p = t.data_ptr()
+            if p & 15:
+                break
+            at.append(p)
+        else:
+            break
+    else:
+        return at, None, None
+    held = [t if t is None else how(where, t, shape, dtype, device)
+            for where, t, shape, dtype, how in specs]
+    return [None if t is None else t.data_ptr() for t in held], strides_of(dims, *held), held
+
+
 def strides_of(dims: int, *tensors: Optional[torch.Tensor]):
     """Host array of the first `dims` strides of every tensor, or None where
     all are dense."""
@@ -131,10 +152,6 @@ def strides_of(dims: int, *tensors: Optional[torch.Tensor]):
     for t in tensors:
         flat += [0] * dims if t is None else t.stride()[:dims]
     return (ctypes.c_int64 * len(flat))(*flat)
-
-
-def ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 # the current stream's handle without a Stream object around it

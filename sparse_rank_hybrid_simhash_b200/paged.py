@@ -20,7 +20,7 @@ import torch
 
 from . import layer
 from .binding import lib
-from .rotary import RotaryParams
+from .rotary import RotaryParams, angles_and_weights
 
 
 class PagedParams(ctypes.Structure):
@@ -55,18 +55,14 @@ def alloc_pages(p: PagedParams, device) -> Tuple[torch.Tensor, torch.Tensor]:
     return tuple(torch.empty(shape, dtype=dt, device=device) for _ in range(2))
 
 
-def _cache(p: PagedParams, k_pages, v_pages, page_table, starts, lengths, dev):
-    dt = layer.torch_dtype(p.dtype)
+def _cache(p: PagedParams, k_pages, v_pages, page_table, starts, lengths, dt, dev):
     shape = (p.pages, p.Hkv, p.page_size, p.d)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        layer.check(name, t, shape, dt, dev)
-        if not layer.strided(t) or not layer.rows_apart(t):
-            raise ValueError(f"{name}: a contiguous last dimension, strides and a start that are "
-                             "multiples of 16 bytes, and no two elements in one place")
-    return (k_pages, v_pages,
-            layer.as_small("page_table", page_table, (p.seqs, p.table_width), torch.int32, dev),
-            layer.as_small("starts", starts, (p.seqs + 1,), torch.int32, dev),
-            layer.as_small("lengths", lengths, (p.seqs,), torch.int32, dev))
+    return (layer.place(dev, 3, ("k_pages", k_pages, shape, dt, layer.as_output),
+                        ("v_pages", v_pages, shape, dt, layer.as_output)),
+            layer.place(dev, 0, ("page_table", page_table, (p.seqs, p.table_width), torch.int32,
+                                 layer.as_small),
+                        ("starts", starts, (p.seqs + 1,), torch.int32, layer.as_small),
+                        ("lengths", lengths, (p.seqs,), torch.int32, layer.as_small)))
 
 
 @layer.on_device(2)
@@ -75,25 +71,19 @@ def write(p: PagedParams, rp: RotaryParams, q, k, v, table, q_weight, k_weight, 
     """qo [T, H, d], the new tokens' queries normed and rotated at their positions; their keys
     (likewise) and values [T, Hkv, d] go into the pages.  ``rp``: H, Hkv, d and dtype as in ``p``."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
-    q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
-    k = layer.as_input("k", k, (p.rows, p.Hkv, p.d), dt, dev)
-    v = layer.as_input("v", v, (p.rows, p.Hkv, p.d), dt, dev)
-    qo = layer.as_output("qo", qo, (p.rows, p.H, p.d), dt, dev, q)
-    if rp.rot_dim > 0:
-        if table is None:
-            raise ValueError("rot_dim > 0 needs a table")
-        table = layer.as_small("table", table, (rp.max_pos, rp.rot_dim // 2, 2), torch.float32, dev)
-    q_weight = layer.as_small("q_weight", q_weight, (p.d,), torch.float32, dev)
-    k_weight = layer.as_small("k_weight", k_weight, (p.d,), torch.float32, dev)
-    k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
-                                                           starts, lengths, dev)
+    sq, sk = (p.rows, p.H, p.d), (p.rows, p.Hkv, p.d)
+    if qo is None:
+        qo = layer.like(q)
+    (pq, pqo, pk, pv), strides, _held = layer.place(
+        dev, 2, ("q", q, sq, dt, layer.as_input), ("qo", qo, sq, dt, layer.as_output),
+        ("k", k, sk, dt, layer.as_input), ("v", v, sk, dt, layer.as_input))
+    (ptable, pwq, pwk), _small = angles_and_weights(rp, table, q_weight, k_weight, dev)
+    ((pkp, pvp), page_strides, _), ((ppt, pst, plen), _, _rows) = _cache(
+        p, k_pages, v_pages, page_table, starts, lengths, dt, dev)
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_paged_write", lib().elsaa_paged_write(
-        ctypes.byref(p), ctypes.byref(rp), ptr(q), ptr(k), ptr(v),
-        layer.strides_of(2, q, qo, k, v), ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo),
-        ptr(k_pages), ptr(v_pages), layer.strides_of(3, k_pages, v_pages), ptr(page_table),
-        ptr(starts), ptr(lengths), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), ctypes.byref(rp), pq, pk, pv, strides, ptable, pwq, pwk, pqo, pkp, pvp,
+        page_strides, ppt, pst, plen, ws.data_ptr(), ws.numel(), stream))
     return qo
 
 
@@ -103,14 +93,15 @@ def attend(p: PagedParams, q, k_pages, v_pages, page_table, starts, lengths, y=N
     """y [T, H, d]: attention of the new tokens q [T, H, d] over their sequences' cached keys and
     values (their own already written)."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
-    q = layer.as_input("q", q, (p.rows, p.H, p.d), dt, dev)
-    y = layer.as_output("y", y, (p.rows, p.H, p.d), dt, dev, q)
-    k_pages, v_pages, page_table, starts, lengths = _cache(p, k_pages, v_pages, page_table,
-                                                           starts, lengths, dev)
+    sq = (p.rows, p.H, p.d)
+    if y is None:
+        y = layer.like(q)
+    (pq, py), strides, _held = layer.place(dev, 2, ("q", q, sq, dt, layer.as_input),
+                                           ("y", y, sq, dt, layer.as_output))
+    ((pkp, pvp), page_strides, _), ((ppt, pst, plen), _, _rows) = _cache(
+        p, k_pages, v_pages, page_table, starts, lengths, dt, dev)
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_paged_attend", lib().elsaa_paged_attend(
-        ctypes.byref(p), ptr(q), layer.strides_of(2, q, y), ptr(k_pages), ptr(v_pages),
-        layer.strides_of(3, k_pages, v_pages), ptr(page_table), ptr(starts), ptr(lengths),
-        ptr(y), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), pq, strides, pkp, pvp, page_strides, ppt, pst, plen, py, ws.data_ptr(),
+        ws.numel(), stream))
     return y

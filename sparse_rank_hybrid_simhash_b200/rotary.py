@@ -58,15 +58,17 @@ def _shapes(p: RotaryParams):
     return (p.B, p.H, p.N, p.d), (p.B, p.Hkv, p.N, p.d)
 
 
-def _small(p: RotaryParams, table, q_weight, k_weight, positions, dev):
-    """The checked table, weights and positions."""
-    if p.rot_dim > 0 and table is None:
+def angles_and_weights(p: RotaryParams, table, q_weight, k_weight, dev):
+    """The addresses of the checked table and weights, and what holds them."""
+    if p.rot_dim == 0:
+        table = None
+    elif table is None:
         raise ValueError("rot_dim > 0 needs a table")
-    table = layer.as_small("table", table, (p.max_pos, p.rot_dim // 2, 2), torch.float32, dev) \
-        if p.rot_dim > 0 else None
-    return (table, layer.as_small("q_weight", q_weight, (p.d,), torch.float32, dev),
-            layer.as_small("k_weight", k_weight, (p.d,), torch.float32, dev),
-            layer.as_small("positions", positions, (p.B, p.N), torch.int32, dev))
+    at, _, held = layer.place(
+        dev, 0, ("table", table, (p.max_pos, p.rot_dim // 2, 2), torch.float32, layer.as_small),
+        ("q_weight", q_weight, (p.d,), torch.float32, layer.as_small),
+        ("k_weight", k_weight, (p.d,), torch.float32, layer.as_small))
+    return at, held
 
 
 @layer.on_device(1)
@@ -76,19 +78,23 @@ def forward(p: RotaryParams, q, k, table=None, q_weight=None, k_weight=None, pos
     other strides (heads of a fused projection) are read in place."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    q = layer.as_input("q", q, sq, dt, dev)
-    qo = layer.as_output("qo", qo, sq, dt, dev, q)
-    if k is not None:
-        k = layer.as_input("k", k, sk, dt, dev)
-        ko = layer.as_output("ko", ko, sk, dt, dev, k)
-    elif ko is not None:
-        raise ValueError("ko without k")
-    table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
+    if qo is None:
+        qo = layer.like(q)
+    if k is None:
+        if ko is not None:
+            raise ValueError("ko without k")
+    elif ko is None:
+        ko = layer.like(k)
+    (pq, pk, pqo, pko), strides, _held = layer.place(
+        dev, 3, ("q", q, sq, dt, layer.as_input), ("k", k, sk, dt, layer.as_input),
+        ("qo", qo, sq, dt, layer.as_output), ("ko", ko, sk, dt, layer.as_output))
+    (ptable, pwq, pwk), _small = angles_and_weights(p, table, q_weight, k_weight, dev)
+    (ppos,), _, _pos = layer.place(dev, 0, ("positions", positions, (p.B, p.N), torch.int32,
+                                            layer.as_small))
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_rotary_forward", lib().elsaa_rotary_forward(
-        ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, qo, ko), ptr(positions),
-        ptr(table), ptr(q_weight), ptr(k_weight), ptr(qo), ptr(ko), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), pq, pk, strides, ppos, ptable, pwq, pwk, pqo, pko, ws.data_ptr(),
+        ws.numel(), stream))
     return qo, ko
 
 
@@ -99,28 +105,34 @@ def backward(p: RotaryParams, q, k, table, q_weight, k_weight, dqo, dko, positio
     are None without the norm, dk's and dk_weight's without k."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    q = layer.as_input("q", q, sq, dt, dev)
-    dqo = layer.as_input("dqo", dqo, sq, dt, dev)
-    dq = layer.as_output("dq", dq, sq, dt, dev, q)
-    if k is not None:
-        k = layer.as_input("k", k, sk, dt, dev)
-        dko = layer.as_input("dko", dko, sk, dt, dev)
-        dk = layer.as_output("dk", dk, sk, dt, dev, k)
-    elif dko is not None or dk is not None:
-        raise ValueError("dko or dk without k")
-    if p.norm:
-        dq_weight = layer.as_output("dq_weight", dq_weight, (p.d,), torch.float32, dev)
-        if k is not None:
-            dk_weight = layer.as_output("dk_weight", dk_weight, (p.d,), torch.float32, dev)
-    else:
+    if dq is None:
+        dq = layer.like(q)
+    if k is None:
+        if dko is not None or dk is not None:
+            raise ValueError("dko or dk without k")
+        dk_weight = None
+    elif dk is None:
+        dk = layer.like(k)
+    if not p.norm:
         dq_weight = dk_weight = None
-    table, q_weight, k_weight, positions = _small(p, table, q_weight, k_weight, positions, dev)
+    else:
+        if dq_weight is None:
+            dq_weight = torch.empty(p.d, dtype=torch.float32, device=dev)
+        if k is not None and dk_weight is None:
+            dk_weight = torch.empty(p.d, dtype=torch.float32, device=dev)
+    into, out = layer.as_input, layer.as_output
+    (pq, pk, pdqo, pdko, pdq, pdk), strides, _held = layer.place(
+        dev, 3, ("q", q, sq, dt, into), ("k", k, sk, dt, into), ("dqo", dqo, sq, dt, into),
+        ("dko", dko, sk, dt, into), ("dq", dq, sq, dt, out), ("dk", dk, sk, dt, out))
+    (ptable, pwq, pwk), _small = angles_and_weights(p, table, q_weight, k_weight, dev)
+    (ppos, pdwq, pdwk), _, _pos = layer.place(
+        dev, 0, ("positions", positions, (p.B, p.N), torch.int32, layer.as_small),
+        ("dq_weight", dq_weight, (p.d,), torch.float32, out),
+        ("dk_weight", dk_weight, (p.d,), torch.float32, out))
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_rotary_backward", lib().elsaa_rotary_backward(
-        ctypes.byref(p), ptr(q), ptr(k), layer.strides_of(3, q, k, dqo, dko, dq, dk),
-        ptr(positions), ptr(table), ptr(q_weight), ptr(k_weight), ptr(dqo), ptr(dko), ptr(dq),
-        ptr(dk), ptr(dq_weight), ptr(dk_weight), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), pq, pk, strides, ppos, ptable, pwq, pwk, pdqo, pdko, pdq, pdk, pdwq, pdwk,
+        ws.data_ptr(), ws.numel(), stream))
     return dq, dk, dq_weight, dk_weight
 
 

@@ -46,6 +46,13 @@ def _shapes(p: WindowParams):
     return (p.B, p.H, p.N, p.d), (p.B, p.Hkv, p.N, p.d)
 
 
+def _as_lse(where, t, shape, dtype, device):
+    layer.check(where, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{where} must be contiguous")
+    return t
+
+
 @layer.on_device(1)
 def forward(p: WindowParams, q, k, v, lengths=None, y=None, lse=None, ws=None,
             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -53,21 +60,19 @@ def forward(p: WindowParams, q, k, v, lengths=None, y=None, lse=None, ws=None,
     in place."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    q = layer.as_input("q", q, sq, dt, dev)
-    k = layer.as_input("k", k, sk, dt, dev)
-    v = layer.as_input("v", v, sk, dt, dev)
-    y = layer.as_output("y", y, sq, dt, dev, q)
+    if y is None:
+        y = layer.like(q)
     if lse is None:
         lse = torch.empty(sq[:3], dtype=torch.float32, device=dev)
-    layer.check("lse", lse, sq[:3], torch.float32, dev)
-    if not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
-    lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+    (pq, pk, pv, py), strides, _held = layer.place(
+        dev, 3, ("q", q, sq, dt, layer.as_input), ("k", k, sk, dt, layer.as_input),
+        ("v", v, sk, dt, layer.as_input), ("y", y, sq, dt, layer.as_output))
+    (plse, plen), _, _small = layer.place(
+        dev, 0, ("lse", lse, sq[:3], torch.float32, _as_lse),
+        ("lengths", lengths, (p.B,), torch.int32, layer.as_small))
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p, False), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_window_forward", lib().elsaa_window_forward(
-        ctypes.byref(p), ptr(q), ptr(k), ptr(v), layer.strides_of(3, q, k, v, y), ptr(lengths),
-        ptr(y), ptr(lse), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), pq, pk, pv, strides, plen, py, plse, ws.data_ptr(), ws.numel(), stream))
     return y, lse
 
 
@@ -77,23 +82,21 @@ def backward(p: WindowParams, q, k, v, y, lse, dy, lengths=None, dq=None, dk=Non
     """(dq, dk, dv) of sum(y * dy), from the y and lse of ``forward`` on the same inputs."""
     dev, dt = q.device, layer.torch_dtype(p.dtype)
     sq, sk = _shapes(p)
-    q = layer.as_input("q", q, sq, dt, dev)
-    k = layer.as_input("k", k, sk, dt, dev)
-    v = layer.as_input("v", v, sk, dt, dev)
-    y = layer.as_input("y", y, sq, dt, dev)
-    dy = layer.as_input("dy", dy, sq, dt, dev)
-    layer.check("lse", lse, sq[:3], torch.float32, dev)
-    lse = lse.contiguous()
-    dq = layer.as_output("dq", dq, sq, dt, dev, q)
-    dk = layer.as_output("dk", dk, sk, dt, dev, k)
-    dv = layer.as_output("dv", dv, sk, dt, dev, v)
-    lengths = layer.as_small("lengths", lengths, (p.B,), torch.int32, dev)
+    dq = layer.like(q) if dq is None else dq
+    dk = layer.like(k) if dk is None else dk
+    dv = layer.like(v) if dv is None else dv
+    into, out = layer.as_input, layer.as_output
+    (pq, pk, pv, py, pdy, pdq, pdk, pdv), strides, _held = layer.place(
+        dev, 3, ("q", q, sq, dt, into), ("k", k, sk, dt, into), ("v", v, sk, dt, into),
+        ("y", y, sq, dt, into), ("dy", dy, sq, dt, into), ("dq", dq, sq, dt, out),
+        ("dk", dk, sk, dt, out), ("dv", dv, sk, dt, out))
+    (plse, plen), _, _small = layer.place(
+        dev, 0, ("lse", lse, sq[:3], torch.float32, layer.as_small),
+        ("lengths", lengths, (p.B,), torch.int32, layer.as_small))
     ws = layer.as_workspace(ws, lambda: workspace_bytes(p, True), dev)
-    ptr = layer.ptr
     layer.ok("elsaa_window_backward", lib().elsaa_window_backward(
-        ctypes.byref(p), ptr(q), ptr(k), ptr(v),
-        layer.strides_of(3, q, k, v, y, dy, dq, dk, dv), ptr(lengths), ptr(y), ptr(lse),
-        ptr(dy), ptr(dq), ptr(dk), ptr(dv), ptr(ws), ws.numel(), stream))
+        ctypes.byref(p), pq, pk, pv, strides, plen, py, plse, pdy, pdq, pdk, pdv, ws.data_ptr(),
+        ws.numel(), stream))
     return dq, dk, dv
 
 
