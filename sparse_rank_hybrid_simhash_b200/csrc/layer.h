@@ -81,12 +81,13 @@ struct AttendArgs {
   char* scratch;              // split partials
 };
 
-// CUDA-core kernels: every type and head dim.
+// CUDA-core kernels: fp32, and bf16 at d = 32.
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_fwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 // (a.delta: window_simt_scratch_bytes of workspace, row statistics and partials of shared tiles)
-size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int64_t N);
+// (window: INT32_MAX for no limit)
+size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int N, int window, int sinks);
 cudaError_t launch_paged_simt(const AttendArgs& a, bool bf16, cudaStream_t s);
 
 // tcgen05 kernels: bf16, d = 64 or 128.

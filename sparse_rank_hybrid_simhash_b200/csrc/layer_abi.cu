@@ -209,7 +209,8 @@ size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backwa
   if (!backward) return kHeadBytes;
   return kHeadBytes + (attend_tc_supported(p->d, p->dtype == ELSAA_BF16)
                            ? window_tc_scratch_bytes(p->d, p->B, p->H, p->N)
-                           : window_simt_scratch_bytes(p->d, p->B, p->H, p->Hkv, p->N));
+                           : window_simt_scratch_bytes(p->d, p->B, p->H, p->Hkv, p->N,
+                                                       p->window > 0 ? p->window : INT32_MAX, p->sinks));
 }
 
 static elsaa_status window_args(const elsaa_window_params* p, const void* const* tensors,

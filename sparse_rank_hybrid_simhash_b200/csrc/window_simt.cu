@@ -1,6 +1,6 @@
 // Causal attention over a sliding window with sinks, and over a paged cache, on
-// CUDA cores: every type and head dim (fp32 data keep fp32 products, which the
-// tensor cores do not have).
+// CUDA cores: fp32 at every head dim (fp32 data keep fp32 products, which the tensor
+// cores do not have), and d = 32.
 //
 // Query at position i sees the keys j <= i with i - j < window or j < sinks.
 // y_i = sum_j p_ij v_j, p = exp(scale q k - lse).  Backward, D_i = y_i . dy_i:
@@ -459,12 +459,17 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const AttendAr
   }
 }
 
-// `parts` CTAs share a key tile's (head of the group, query block) list; with more than
-// one, each leaves its sums in `partial` ([tile][part][2][ROWS][D]) and the last to
-// come adds them up in order.
+// How many CTAs share a key tile's (head of the group, query block) list: a head's first
+// `sinks` tiles, which every query behind them sees, `sink` each, the others `other`.
+struct Parts {
+  int sinks, sink, other;
+};
+
+// With more than one CTA a tile, each leaves its sums in `partial` ([tile][part][2][ROWS][D])
+// and the last to come adds them up in order.
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
-window_dkv_simt_kernel(const AttendArgs a, int tiles, int parts, float* partial) {
+window_dkv_simt_kernel(const AttendArgs a, int tiles, const Parts share, float* partial) {
   constexpr int RT = ROWS / 16;
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
@@ -475,9 +480,12 @@ window_dkv_simt_kernel(const AttendArgs a, int tiles, int parts, float* partial)
   float* Ds = Ps + ROWS * kPs;
   __shared__ int last;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int part = blockIdx.x % parts, item = blockIdx.x / parts;
-  const int bk = item / tiles, b = bk / a.Hkv, hk = bk % a.Hkv;
-  const int j0 = item % tiles * ROWS;   // the sinks' tile, the longest, first
+  const int lead = share.sinks * share.sink, per = lead + (tiles - share.sinks) * share.other;
+  const int bk = blockIdx.x / per, b = bk / a.Hkv, hk = bk % a.Hkv, at = blockIdx.x % per;
+  const bool sink = at < lead;
+  const int parts = sink ? share.sink : share.other, part = (sink ? at : at - lead) % parts;
+  const int tile = sink ? at / parts : share.sinks + (at - lead) / parts;
+  const int j0 = tile * ROWS;
   const int len = length_of(a, b);
   auto row = [&](const void* base, const Strides& s, int head, int n) -> const T* {
     return n < len ? static_cast<const T*>(base) + b * s.b + head * s.h + n * s.n : nullptr;
@@ -521,7 +529,12 @@ window_dkv_simt_kernel(const AttendArgs a, int tiles, int parts, float* partial)
     accumulate<D, RT>(Ds, Qs, ok);
   }
   if (parts > 1) {
-    float* base = partial + (int64_t)item * parts * 2 * ROWS * D;
+    // (the sinks' tiles of all heads, then the others)
+    const int heads = a.B * a.Hkv, most = heads * share.sinks;
+    const int item = sink ? bk * share.sinks + tile : most + bk * (tiles - share.sinks) + tile - share.sinks;
+    const int64_t slot = sink ? (int64_t)item * parts
+                              : (share.sink > 1 ? (int64_t)most * share.sink : 0) + (int64_t)(item - most) * parts;
+    float* base = partial + slot * 2 * ROWS * D;
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       store_cols<float, D>(base + ((int64_t)part * 2 * ROWS + RT * ty + x) * D, ov[x]);
@@ -591,17 +604,32 @@ cudaError_t dq(const AttendArgs& a, cudaStream_t s) {
   const int tiles = (a.N + R - 1) / R;
   return run(window_dq_simt_kernel<T, D, R>, (int64_t)a.B * a.H * tiles, bytes<D>(R, 2, 2, 1), s, a, tiles);
 }
-// CTAs that share a key tile: as many as give every SM two, at most 16.
-int dkv_parts(int64_t items) {
-  const int64_t p = (296 + items - 1) / items;
-  return (int)(p > 16 ? 16 : p);
+// CTAs that share a key tile: as many as give every SM two; for the sinks' tiles as many as
+// make their lists as short as the others' (fp32, 8 heads of d = 64, 8192 tokens, a window of
+// 512 and 4 sinks: the backward 2439 us with one CTA each, 1247 so).  At most 16, and no more
+// tiles than counters.
+Parts dkv_parts(int64_t heads, int N, int R, int window, int sinks) {
+  const int64_t tiles = (N + R - 1) / R, items = heads * tiles, p = (296 + items - 1) / items;
+  Parts s{0, 1, (int)(p > 16 ? 16 : p)};
+  if (sinks == 0 || window >= N) return s;
+  const int64_t most = ((int64_t)sinks + R - 1) / R, all = (N + kBlk - 1) / kBlk;
+  const int64_t few = ((int64_t)window + R - 1 + kBlk - 1) / kBlk + 1, n = all / few > 16 ? 16 : all / few;
+  if (n <= s.other || heads * most > 1024) return s;
+  s.sinks = (int)(most < tiles ? most : tiles);
+  s.sink = (int)n;
+  return s;
+}
+// Partial sums of the shared tiles, [2][R][d] each.
+int64_t dkv_slots(const Parts& s, int64_t heads, int64_t tiles) {
+  return (s.sink > 1 ? heads * s.sinks * s.sink : 0) + (s.other > 1 ? heads * (tiles - s.sinks) * s.other : 0);
 }
 template <typename T, int D, int R>
 cudaError_t dkv(const AttendArgs& a, cudaStream_t s) {
   const int tiles = (a.N + R - 1) / R;
-  const int64_t items = (int64_t)a.B * a.Hkv * tiles;
-  const int parts = dkv_parts(items);
-  return run(window_dkv_simt_kernel<T, D, R>, items * parts, bytes<D>(R, 2, 2, 2), s, a, tiles, parts,
+  const int64_t heads = (int64_t)a.B * a.Hkv;
+  const Parts p = dkv_parts(heads, a.N, R, a.window, a.sinks);
+  return run(window_dkv_simt_kernel<T, D, R>, heads * (p.sinks * p.sink + (int64_t)(tiles - p.sinks) * p.other),
+             bytes<D>(R, 2, 2, 2), s, a, tiles, p,
              a.delta + align_up((size_t)a.B * a.H * a.N * sizeof(float)) / sizeof(float));
 }
 
@@ -625,23 +653,20 @@ struct Launch {
   static cudaError_t paged(const AttendArgs& a, cudaStream_t s) { return pages<T, D>(a, s); }
 };
 
-// f<T, D> of the problem's type and head dim.
-#define ELSAA_BY_SHAPE(f)                                                                       \
-  (bf16 ? (a.d == 32   ? Launch<__nv_bfloat16, 32>::f(a, s)                                     \
-           : a.d == 64 ? Launch<__nv_bfloat16, 64>::f(a, s)                                     \
-                       : Launch<__nv_bfloat16, 128>::f(a, s))                                   \
-        : (a.d == 32   ? Launch<float, 32>::f(a, s)                                             \
-           : a.d == 64 ? Launch<float, 64>::f(a, s)                                             \
-                       : Launch<float, 128>::f(a, s)))
+// f<T, D> of the problem's type and head dim (bf16 at d = 64, 128 has the tensor cores).
+#define ELSAA_BY_SHAPE(f)                                \
+  (bf16        ? Launch<__nv_bfloat16, 32>::f(a, s)      \
+   : a.d == 32 ? Launch<float, 32>::f(a, s)              \
+   : a.d == 64 ? Launch<float, 64>::f(a, s)              \
+               : Launch<float, 128>::f(a, s))
 
 }  // namespace
 
-size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int64_t N) {
-  const int R = small_tiles(B * Hkv, (int)N) ? 16 : 64;
-  const int64_t items = B * Hkv * ((N + R - 1) / R);
-  const int parts = dkv_parts(items);
+size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int N, int window, int sinks) {
+  const int R = small_tiles(B * Hkv, N) ? 16 : 64;
+  const Parts p = dkv_parts(B * Hkv, N, R, window, sinks);
   return align_up((size_t)(B * H * N) * sizeof(float)) +
-         (parts > 1 ? (size_t)items * parts * 2 * R * d * sizeof(float) : 0);
+         (size_t)dkv_slots(p, B * Hkv, (N + R - 1) / R) * 2 * R * d * sizeof(float);
 }
 
 cudaError_t launch_window_delta(const AttendArgs& a, bool bf16, cudaStream_t s) {

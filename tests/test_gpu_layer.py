@@ -153,6 +153,11 @@ WINDOW = [
     (1, 8, 1, 700, 128, "f32", 0, 0, (650,), False),
     (1, 8, 1, 400, 32, "bf16", 90, 20, None, True),
     (2, 4, 2, 150, 32, "bf16", 40, 2, (150, 64), False),
+    # key tiles of the sinks, seen by far more queries than the others
+    (2, 6, 6, 1000, 32, "f32", 10, 3, (1000, 333), False),
+    (2, 12, 12, 1121, 32, "f32", 4, 1, None, False),
+    (2, 24, 12, 700, 32, "bf16", 5, 130, None, False),
+    (1, 4, 1, 900, 128, "f32", 20, 17, (771,), True),
 ]
 
 
