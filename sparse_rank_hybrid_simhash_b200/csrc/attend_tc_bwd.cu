@@ -28,9 +28,9 @@
 // Bound at d = 128: 2048 (dkv) and 1536 (dq) cycles of products a block against
 // 1024 of exponentials and about as many of other instructions; at d = 64 the
 // elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
-// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1316 us (784
+// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1306 us (790
 // TFLOP/s by the formulas' five products), d = 64 927 us; text-32k (2 x 12 heads of
-// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 521, stats 49.
+// d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 512, stats 49.
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.
@@ -1081,7 +1081,7 @@ window_dq_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const St
         if (n >= kItems && !mbar_wait(&bars->item_empty[n % kItems], (n / kItems - 1) & 1, a.err)) break;
         int32_t* it = bars->items[n % kItems];
         it[qB] = -1;
-        for (; x < items && it[qB] < 0; x += gridDim.x) {
+        for (; x < items && it[qB] < 0; x = next_item(a.counters, items)) {
           // the longest (last) tiles first, heads and batches inside
           const int t = tiles - 1 - (int)(x / bh), b = (int)(x % bh / a.H), h = (int)(x % a.H);
           const int len = length_of(a, b);

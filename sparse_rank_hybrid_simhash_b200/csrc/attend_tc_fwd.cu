@@ -42,8 +42,9 @@
 // exponentials (16 a cycle an SM) a stream, at d = 64 512 and 1024; one pair of
 // exponentials in four goes to the FMA pipe (attend_tc.cuh).  What is left over is the
 // chain of a half block: S read from TMEM, maximum, exponentials, P written, handed over.
-// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 413 us (1000
-// TFLOP/s), d = 64 369 us (560); text-32k (2 x 12 heads of d = 64, 32768 tokens) at window 1024 439 us (470).
+// Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 402 us (1026
+// TFLOP/s), d = 64 360 us (572); text-32k (2 x 12 heads of d = 64, 32768 tokens) at window
+// 1024 431 us (480).
 //
 // Every wait is bounded; one that gives up records ERR_TIMEOUT, every role leaves
 // its loop, and copies and products in flight end before TMEM is freed.
@@ -308,7 +309,7 @@ struct Walk {
       if (x >= items) return false;
       it = window_item(a, sh, x);
       it.order = order++;
-      x += gridDim.x;
+      x = next_item(a.counters, items);
       return true;
     }
     if (left <= 0) return false;

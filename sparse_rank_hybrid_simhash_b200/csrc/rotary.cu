@@ -16,7 +16,7 @@
 // and keeps what does not depend on the head in registers, weight and angle folded:
 //   y_i = r (x_i A_i + x_o B_i),  A_i = w_i cos,  B_i = -+ w_o sin  (o: i's partner)
 // (text-32k queries and keys, 2 x 12 heads of d = 64 over 32768 tokens: 74 us, issue
-// active 74 % of the time; backward 176 and the weights' sums 5).  Four heads' rows are
+// active 74 % of the time; backward 135 and the weights' sums 4).  Four heads' rows are
 // in flight at a time, the first of them while the angles are fetched (an output may be
 // its input, so the compiler must keep a later row's load behind an earlier store: 102 us
 // without); in the backward two heads' x and dy.
@@ -238,7 +238,8 @@ norm_rotate_back_kernel(const RotaryArgs a, int hp, int q_blocks) {
   for (int i = 0; i < V; ++i) dw[i] = 0.f;
   for (int it = first; it < items; it += step) {
     const int group = it / chunks, tok = group * ROWS + threadIdx.x / LANES;
-    const int h0 = (it - group * chunks) * hp, h1 = min(h0 + hp, heads);
+    const int chunk = it - group * chunks;   // (of equal size: a block may only ever get one of them)
+    const int h0 = chunk * heads / chunks, h1 = (chunk + 1) * heads / chunks;
     const bool live = tok < tokens;
     const int b = live ? tok / a.N : 0, n = live ? tok - b * a.N : 0;
     const T* in = static_cast<const T*>(is_q ? a.q : a.k) + b * si.b + n * si.n + col;
@@ -462,14 +463,13 @@ struct Backward {
     const int64_t tokens = (int64_t)a.B * a.N, groups = (tokens + ROWS - 1) / ROWS;
     const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
     const int64_t qi = groups * ((a.H + hp - 1) / hp), ki = groups * ((a.Hkv + hp - 1) / hp);
-    // blocks by the share of the items, all resident at once
+    // blocks by the share of the heads, all resident at once
     const int64_t cap = kRotaryPartials;
     int64_t qb = qi, kb = ki;
     if (qi + ki > cap) {
-      qb = cap * qi / (qi + ki);
-      qb = qb < 1 ? 1 : qb;
-      kb = a.Hkv ? (cap - qb < 1 ? 1 : cap - qb) : 0;
-      if (qb + kb > cap) qb = cap - kb;
+      kb = cap * a.Hkv / (a.H + a.Hkv);
+      kb = kb > ki ? ki : a.Hkv && kb < 1 ? 1 : kb;
+      qb = cap - kb > qi ? qi : cap - kb;
     }
     norm_rotate_back_kernel<T, D, IL><<<(unsigned)(qb + kb), kThreads, 0, s>>>(a, hp, (int)qb);
     cudaError_t e = cudaGetLastError();
