@@ -15,8 +15,8 @@
 // away and come over as the raw 16 bytes.  A group walks several heads of its token
 // and keeps what does not depend on the head in registers, weight and angle folded:
 //   y_i = r (x_i A_i + x_o B_i),  A_i = w_i cos,  B_i = -+ w_o sin  (o: i's partner)
-// (text-32k queries and keys, 2 x 12 heads of d = 64 over 32768 tokens: 74 us, issue
-// active 74 % of the time; backward 135 and the weights' sums 4).  Four heads' rows are
+// (text-32k queries and keys, 2 x 12 heads of d = 64 over 32768 tokens: 71 us, issue
+// active 71 % of the time; backward 135 and the weights' sums 4).  Four heads' rows are
 // in flight at a time, the first of them while the angles are fetched (an output may be
 // its input, so the compiler must keep a later row's load behind an earlier store: 102 us
 // without); in the backward two heads' x and dy.
@@ -416,11 +416,13 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
   }
 }
 
-// Heads that a lane group walks: as many as keep the card filled (148 SMs x
-// 2048 threads), at most 8.
-int head_chunk(int64_t tokens, int lanes, int heads) {
-  int hp = 8;
-  while (hp > 1 && tokens * lanes * ((heads + hp - 1) / hp) < (int64_t)148 * 2048) hp >>= 1;
+// Heads that a lane group walks: as many as leave the card (148 SMs x 1024 threads) filled,
+// at most `most`.  More of them share an angle and are loaded together; the forward on
+// text-32k 78 us with at most 8, 71 with 16, a fused projection of 32 and 8 heads over 4099
+// tokens 19.9, 17.8 (22.1 with 32), 24.4 where the card had to be filled four times.
+int head_chunk(int64_t tokens, int lanes, int heads, int most) {
+  int hp = most;
+  while (hp > 1 && tokens * lanes * ((heads + hp - 1) / hp) < (int64_t)148 * 1024) hp >>= 1;
   return hp;
 }
 
@@ -446,7 +448,7 @@ struct Forward {
   cudaError_t operator()() const {
     constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
     const int64_t tokens = (int64_t)a.B * a.N;
-    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
+    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv, 16);
     const int qc = (a.H + hp - 1) / hp, kc = (a.Hkv + hp - 1) / hp;
     const dim3 grid((unsigned)((tokens + ROWS - 1) / ROWS), qc + kc);
     norm_rotate_kernel<T, D, IL><<<grid, kThreads, 0, s>>>(a, hp, qc);
@@ -461,7 +463,7 @@ struct Backward {
   cudaError_t operator()() const {
     constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
     const int64_t tokens = (int64_t)a.B * a.N, groups = (tokens + ROWS - 1) / ROWS;
-    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv);
+    const int hp = head_chunk(tokens, LANES, a.H + a.Hkv, 8);
     const int64_t qi = groups * ((a.H + hp - 1) / hp), ki = groups * ((a.Hkv + hp - 1) / hp);
     // blocks by the share of the heads, all resident at once
     const int64_t cap = kRotaryPartials;
@@ -485,7 +487,7 @@ struct Write {
   template <typename T, int D, bool IL>
   cudaError_t operator()() const {
     constexpr int LANES = D / Vec<T>::V, ROWS = kThreads / LANES;
-    const int hp = head_chunk(a.N, LANES, a.H + 2 * a.Hkv);
+    const int hp = head_chunk(a.N, LANES, a.H + 2 * a.Hkv, 16);
     const int qc = (a.H + hp - 1) / hp, kc = (a.Hkv + hp - 1) / hp;
     const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS), qc + 2 * kc);
     paged_write_kernel<T, D, IL><<<grid, kThreads, 0, s>>>(a, hp, qc, kc);
