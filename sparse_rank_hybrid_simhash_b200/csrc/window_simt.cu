@@ -590,9 +590,24 @@ constexpr size_t bytes(int R, int tiles, int blocks, int scores) {
   return sizeof(float) * ((size_t)(tiles * R + blocks * kBlk) * pitch<D>() + (size_t)scores * R * kPs);
 }
 
-// 16-row tiles where 64-row tiles would be fewer than the SMs: a tile of 16 does a
-// quarter of the work of one of 64 at half its efficiency.
-bool small_tiles(int64_t heads, int N) { return heads * ((N + 63) / 64) < 148; }
+// 16-row query tiles where 64-row ones would leave two thirds of the SMs idle: a tile of 16
+// does a quarter of the work of one of 64 in two thirds of its time (fp32, d = 64, window 72:
+// forward of 20 tiles 17 against 25 us, of 80 tiles 28 against 25.5, of 120 39 against 26).
+bool small_tiles(int64_t heads, int N) { return heads * ((N + 63) / 64) < 50; }
+
+// Query blocks that see a key tile of 64 without sinks, and all of them.
+int64_t near_blocks(int N, int64_t window, int R) {
+  const int64_t all = (N + kBlk - 1) / kBlk, few = (window + R - 1 + kBlk - 1) / kBlk + 1;
+  return few < all ? few : all;
+}
+// 16-row key tiles where 64-row ones would not fill the card even with their lists (g heads x
+// query blocks) shared by up to 16 CTAs (fp32, d = 64, window 72, g = 1: 20 tiles 28 against 56
+// us, 40 tiles 34 against 42, 80 tiles 51 against 43; 24 tiles of a group of 8 over 1500 tokens
+// at d = 128 866 against 374).
+bool small_key_tiles(int64_t heads, int g, int N, int window) {
+  const int64_t list = g * near_blocks(N, window, 64);
+  return heads * ((N + 63) / 64) * (list < 16 ? list : 16) < 200;
+}
 
 template <typename T, int D, int R>
 cudaError_t forward(const AttendArgs& a, cudaStream_t s) {
@@ -612,8 +627,9 @@ Parts dkv_parts(int64_t heads, int N, int R, int window, int sinks) {
   const int64_t tiles = (N + R - 1) / R, items = heads * tiles, p = (296 + items - 1) / items;
   Parts s{0, 1, (int)(p > 16 ? 16 : p)};
   if (sinks == 0 || window >= N) return s;
-  const int64_t most = ((int64_t)sinks + R - 1) / R, all = (N + kBlk - 1) / kBlk;
-  const int64_t few = ((int64_t)window + R - 1 + kBlk - 1) / kBlk + 1, n = all / few > 16 ? 16 : all / few;
+  const int64_t most = ((int64_t)sinks + R - 1) / R;
+  int64_t n = (N + kBlk - 1) / kBlk / near_blocks(N, window, R);
+  n = n > 16 ? 16 : n;
   if (n <= s.other || heads * most > 1024) return s;
   s.sinks = (int)(most < tiles ? most : tiles);
   s.sink = (int)n;
@@ -648,7 +664,7 @@ struct Launch {
   static cudaError_t bwd(const AttendArgs& a, cudaStream_t s) {
     const cudaError_t e = small_tiles((int64_t)a.B * a.H, a.N) ? dq<T, D, 16>(a, s) : dq<T, D, 64>(a, s);
     if (e != cudaSuccess) return e;
-    return small_tiles((int64_t)a.B * a.Hkv, a.N) ? dkv<T, D, 16>(a, s) : dkv<T, D, 64>(a, s);
+    return small_key_tiles((int64_t)a.B * a.Hkv, a.g, a.N, a.window) ? dkv<T, D, 16>(a, s) : dkv<T, D, 64>(a, s);
   }
   static cudaError_t paged(const AttendArgs& a, cudaStream_t s) { return pages<T, D>(a, s); }
 };
@@ -663,7 +679,7 @@ struct Launch {
 }  // namespace
 
 size_t window_simt_scratch_bytes(int d, int64_t B, int64_t H, int64_t Hkv, int N, int window, int sinks) {
-  const int R = small_tiles(B * Hkv, N) ? 16 : 64;
+  const int R = small_key_tiles(B * Hkv, (int)(H / Hkv), N, window) ? 16 : 64;
   const Parts p = dkv_parts(B * Hkv, N, R, window, sinks);
   return align_up((size_t)(B * H * N) * sizeof(float)) +
          (size_t)dkv_slots(p, B * Hkv, (N + R - 1) / R) * 2 * R * d * sizeof(float);
