@@ -16,7 +16,7 @@
 // and keeps what does not depend on the head in registers, weight and angle folded:
 //   y_i = r (x_i A_i + x_o B_i),  A_i = w_i cos,  B_i = -+ w_o sin  (o: i's partner)
 // (text-32k queries and keys, 2 x 12 heads of d = 64 over 32768 tokens: 71 us, issue
-// active 71 % of the time; backward 135 and the weights' sums 4).  Four heads' rows are
+// active 69 % of the time; backward 135 and the weights' sums 4).  Four heads' rows are
 // in flight at a time, the first of them while the angles are fetched (an output may be
 // its input, so the compiler must keep a later row's load behind an earlier store: 102 us
 // without); in the backward two heads' x and dy.
