@@ -613,6 +613,27 @@ def test_offsets_past_32_bits(cuda_device, dt, d):
         assert torch.equal(kp, fk) and torch.equal(vp, fv)
 
 
+def test_workspace_head_is_left_clear(cuda_device):
+    """Error word and counters are zero after every call, whatever it shared between CTAs."""
+    def clear(ws):
+        torch.cuda.synchronize()
+        assert not ws[:8192].any()
+
+    for case in ((4, 16, 4, 1100, 64, "bf16", 300, 3, (1100, 0, 100, 1), False), (1, 2, 2, 90, 128, "bf16", 0, 0, None, False),
+                 (2, 6, 6, 1000, 32, "f32", 10, 3, (1000, 333), False), (1, 8, 1, 700, 128, "f32", 0, 0, None, False)):
+        p, q, k, v, dy, n = window_inputs(case)
+        ws = window.alloc_workspace(p, cuda_device)
+        y, lse = window.forward(p, q, k, v, lengths=n, ws=ws)
+        clear(ws)
+        window.backward(p, q, k, v, y, lse, dy, lengths=n, ws=ws)
+        clear(ws)
+    for case in (PAGED[6], PAGED[2], PAGED[12], PAGED[16]):
+        p, *args = paged_inputs(case)
+        ws = paged.alloc_workspace(p, cuda_device)
+        paged.attend(p, *args, ws=ws)
+        clear(ws)
+
+
 def test_training_step_in_a_graph(cuda_device):
     """Forward and gradients of the training operators captured through autograd, replayed on new inputs."""
     _, q, k, v, dy, _ = window_inputs((1, 4, 2, 200, 64, "bf16", 64, 2, None, False))
