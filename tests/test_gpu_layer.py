@@ -79,6 +79,24 @@ def test_rotary(cuda_device, case, far):
     assert none is None and torch.equal(alone, qo)
 
 
+@pytest.mark.parametrize("case", [(2, 9, 3, 70, 64, "bf16"), (1, 12, 3, 900, 128, "bf16"), (3, 20, 1, 40, 32, "f32")])
+def test_rotary_backward_alone_and_in_place(cuda_device, case):
+    """Gradients of the queries alone, and gradients written over the incoming ones."""
+    B_, H, Hkv, N, d, dt = case
+    q, k, gq, gk = (rand((B_, h, N, d), DT[dt], 20 + i) for i, h in enumerate((H, Hkv, H, Hkv)))
+    tab, w = rotary.angle_table(N, d, device=cuda_device), 1 + rand((d,), torch.float32, 9, 0.2)
+    p = rotary.RotaryParams.make(B_, H, Hkv, N, d, dt, d, N)
+    want = rotary.backward(p, q, k, tab, w, w, gq, gk)
+    at = torch.arange(N, device=cuda_device).expand(B_, H, N)
+    dq, dk, dwq, dwk = rotary.backward(p, q, None, tab, w, None, gq, None)
+    val, tol = ref.rotary(q, w, at, tab, False, True, 1e-6, dy=gq)
+    assert dk is None and dwk is None and torch.equal(dq, want[0])
+    ref.close(dwq, val["dw"], tol["dw"], "dw")
+    a, b = gq.clone(), gk.clone()
+    got = rotary.backward(p, q, k, tab, w, w, a, b, dq=a, dk=b)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(a, want[0])
+
+
 def test_rotary_positions_outside_the_table(cuda_device):
     p = rotary.RotaryParams.make(1, 2, 1, 5, 64, "bf16", 64, 8)
     q, k = rand((1, 2, 5, 64), torch.bfloat16, 1), rand((1, 1, 5, 64), torch.bfloat16, 2)
