@@ -440,9 +440,11 @@ size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p);
  * page page_table[b][j / page_size] (device int32 [S, table_width]), slot
  * j % page_size.  Entries that no token of the call needs are not read: behind
  * the length, and before every new token's window and behind the sinks.  A
- * needed entry that is no page, or a length that does not fit, is recorded
- * (DEVICE_CHECK); such a page reads as zeros and is never written.  Rows of q
- * before starts[0] and from starts[S] on belong to no sequence.
+ * needed entry that is no page is recorded (DEVICE_CHECK), reads as zeros and
+ * is never written.  A sequence that does not fit (starts that fall or leave
+ * q's rows, a length below its new tokens or beyond its page table) is recorded
+ * and left out whole: its rows of y and q_out and every page stay as they were.
+ * Rows of q before starts[0] and from starts[S] on belong to no sequence.
  * strides: q, q_out, k, v as (row, head); page_strides: k_pages, v_pages as
  * (page, head, slot); host arrays of element strides or NULL for dense. */
 

@@ -58,15 +58,19 @@ ELSAA_DEV int64_t div64(int64_t x, int64_t y) {
 
 // ---- pages -----------------------------------------------------------------
 
-// New tokens of sequence b: clamped to what q holds and the context has
-// (anything else is recorded and left out).
+// Whether a sequence's new tokens, rows s0 .. s1 - 1 of q, lie in q's rows and its length holds
+// them and fits its page table.  A sequence that does not fit is recorded and left out whole, by
+// the write as by the attention: following part of it would put tokens into other tokens' slots.
+ELSAA_DEV bool tokens_fit(int s0, int s1, int len, int rows, int64_t context) {
+  return s0 >= 0 && s1 >= s0 && s1 <= rows && len >= s1 - s0 && len <= context;
+}
+
+// New tokens of sequence b; none (recorded) where they do not fit.
 ELSAA_DEV int new_tokens(const AttendArgs& a, int b, int* start, int* len, bool lead) {
   const int s0 = a.starts[b], s1 = a.starts[b + 1], l = a.lengths[b];
   *start = s0;
   *len = l;
-  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.rows && l >= s1 - s0 &&
-                  l <= (int64_t)a.page_size * a.table_width;
-  if (ok) return s1 - s0;
+  if (tokens_fit(s0, s1, l, a.rows, (int64_t)a.page_size * a.table_width)) return s1 - s0;
   if (lead) raise_error(a.err, ERR_CHECK);
   return 0;
 }

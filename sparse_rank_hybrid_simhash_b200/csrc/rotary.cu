@@ -20,6 +20,7 @@
 // in flight at a time, the first of them while the angles are fetched (an output may be
 // its input, so the compiler must keep a later row's load behind an earlier store: 102 us
 // without); in the backward two heads' x and dy.
+#include "attend.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "layer.h"
@@ -347,23 +348,28 @@ paged_write_kernel(const RotaryArgs a, int hp, int q_chunks, int k_chunks) {
   const int32_t* st = cached ? first : a.starts;
   const int col = (threadIdx.x % LANES) * V;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
-  const int end = min(st[a.seqs], a.N);
-  const bool live = row >= st[0] && row < end;
+  const int64_t context = (int64_t)a.page_size * a.table_width;
+  // sequences that do not fit are recorded by one block, whether they have rows here or not
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.seqs; i += kThreads)
+      if (!tokens_fit(st[i], st[i + 1], a.lengths[i], a.N, context)) raise_error(a.err, ERR_CHECK);
   // the last sequence that starts at or before the row (empty ones share a start)
   int lo = 0, hi = a.seqs - 1;
-  while (live && lo < hi) {
+  while (row < a.N && lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (st[mid] <= row) lo = mid; else hi = mid - 1;
   }
-  const int seq = lo;
-  const int len = live ? a.lengths[seq] : 0;
-  const int pos = live ? len - st[seq + 1] + (int)row : 0;
+  const int seq = lo, s0 = st[seq], s1 = st[seq + 1];
+  const bool mine = row < a.N && row >= s0 && row < s1;
+  const int len = mine ? a.lengths[seq] : 0;
+  const bool live = mine && tokens_fit(s0, s1, len, a.N, context);   // (else the row stays as it was)
+  const int pos = live ? len - s1 + (int)row : 0;
   const int kind = (int)blockIdx.y < q_chunks ? 0 : (int)blockIdx.y < q_chunks + k_chunks ? 1 : 2;
   const int y = blockIdx.y - (kind == 0 ? 0 : kind == 1 ? q_chunks : q_chunks + k_chunks);
   const int h0 = y * hp, h1 = min(h0 + hp, kind == 0 ? a.H : a.Hkv);
   // keys and values: the token's page and slot, checked before anything is written
   int64_t page = -1;
-  bool ok = live && pos >= 0 && pos < len && len <= (int64_t)a.page_size * a.table_width;
+  bool ok = live;
   if (ok && kind != 0) {
     page = a.page_table[(int64_t)seq * a.table_width + pos / a.page_size];
     ok = page >= 0 && page < a.pages;

@@ -1,0 +1,65 @@
+"""Calls of the operators next to ELSAA that their documentation allows or refuses and
+that test_gpu_layer.py does not make, and the code paths of larger sizes."""
+
+import pytest
+import torch
+
+import layer_reference as ref
+from sparse_rank_hybrid_simhash_b200 import binding as B
+from sparse_rank_hybrid_simhash_b200 import paged, rotary, window
+from test_gpu_layer import DT, paged_inputs, rand
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- sequences that do not fit ---------------------------------------------------
+
+def starts_of(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("starts,lengths,good", [
+    ((0, 3, 5, 6), (20, 1, 30), (0, 2)),           # fewer tokens than new ones
+    ((0, 3, 5, 6), (20, 0, 30), (0, 2)),
+    ((0, 3, 5, 6), (20, -7, 30), (0, 2)),
+    ((0, 3, 5, 6), (20, 49, 30), (0, 2)),          # more than the page table holds
+    ((0, 3, 5, 9), (20, 40, 30), (0, 1)),          # rows past q's
+    ((0, 3, 5, 1 << 30), (20, 40, 30), (0, 1)),
+    ((-2, 3, 5, 6), (20, 40, 30), (1, 2)),         # rows before q's
+    ((-2, -1, 5, 6), (20, 40, 30), (2,)),
+    ((0, 3, 3, 1), (20, 40, 30), (0, 1)),          # starts that fall behind a sequence without new tokens
+], ids=str)
+def test_sequences_that_do_not_fit_are_left_out_whole(cuda_device, dt, starts, lengths, good):
+    """The write, like the attention, records such a sequence and touches nothing of it."""
+    p, q, kp, vp, table, _, _ = paged_inputs((4, 2, 64, dt, 16, 0, 0, [(3, 48), (2, 48), (1, 48)]), slack=1)
+    kp, vp = rand(kp.shape, DT[dt], 1), rand(vp.shape, DT[dt], 2)
+    k, v = (rand((p.rows, 2, 64), DT[dt], s) for s in (3, 4))
+    tab = rotary.angle_table(64, 64, device=cuda_device)
+    rp = rotary.RotaryParams.make(1, 4, 2, 1, 64, dt, 64, 64)
+    st, ln = starts_of(*starts), starts_of(*lengths)
+    ws = paged.alloc_workspace(p, cuda_device)
+    k0, v0 = kp.clone(), vp.clone()
+    qo, y = torch.full_like(q, 5.0), torch.full_like(q, 5.0)
+    paged.write(p, rp, q, k, v, tab, None, None, kp, vp, table, st, ln, qo=qo, ws=ws)
+    with pytest.raises(B.ElsaaError) as e:
+        B.check(ws)
+    assert e.value.code == 6
+    paged.attend(p, q, kp, vp, table, st, ln, y=y, ws=ws)
+    with pytest.raises(B.ElsaaError) as e:
+        B.check(ws)
+    assert e.value.code == 6
+    touched = torch.zeros(p.rows, dtype=torch.bool, device=cuda_device)
+    for b in good:
+        rows = torch.arange(starts[b], starts[b + 1], device=cuda_device)
+        pos = rows + lengths[b] - starts[b + 1]
+        touched[rows] = True
+        at = (table.long()[b, pos // 16], slice(None), pos % 16)
+        for x, got in ((q, qo[rows]), (k, kp[at])):
+            val, tol = ref.rotary(x[rows], None, pos[:, None].expand(x[rows].shape[:2]), tab, False, True, 1e-6)
+            ref.close(got, val["y"], tol["y"])
+        assert torch.equal(vp[at], v[rows])
+        kp[at], vp[at] = k0[at], v0[at]
+    assert torch.equal(kp, k0) and torch.equal(vp, v0)     # nothing else in the pools has changed
+    assert (qo[~touched] == 5.0).all() and (y[~touched] == 5.0).all()
+    assert torch.isfinite(y).all() and (y[touched] != 5.0).any(-1).all()
