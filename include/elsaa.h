@@ -363,8 +363,9 @@ size_t elsaa_rotary_workspace_bytes(const elsaa_rotary_params* p);
  *   (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin) for its pairs (a, b),
  * with the angles of table[position].  table: device fp32
  * [max_pos, rot_dim / 2, 2] of (cos, sin).  positions: device int32 [B, N], or
- * NULL for 0..N-1; a position outside the table is recorded (DEVICE_CHECK) and
- * its row is written as zeros.  q_weight, k_weight: device fp32 [d], or NULL
+ * NULL for 0..N-1, which max_pos must hold (N <= max_pos where rot_dim > 0); a
+ * position outside the table is recorded (DEVICE_CHECK) and its row is written
+ * as zeros.  q_weight, k_weight: device fp32 [d], or NULL
  * for ones.  strides: q, k, qo, ko.  Sums in fp32, one rounding at the end.  k
  * and ko may be NULL (queries only).  qo may be q and ko may be k, with the same
  * strides. */

@@ -135,6 +135,12 @@ static elsaa_status rotary_args(const elsaa_rotary_params* p, const float* table
   return ELSAA_OK;
 }
 
+// Without positions the tokens are 0 .. N - 1: the table has to hold them all (positions are
+// known to the device alone, which records those outside).
+static bool token_order_ok(const elsaa_rotary_params* p, const int32_t* positions) {
+  return positions || p->rot_dim == 0 || p->N <= p->max_pos;
+}
+
 elsaa_status elsaa_rotary_forward(const elsaa_rotary_params* p, const void* q, const void* k,
                                   const int64_t* strides, const int32_t* positions,
                                   const float* table, const float* q_weight,
@@ -143,6 +149,7 @@ elsaa_status elsaa_rotary_forward(const elsaa_rotary_params* p, const void* q, c
   RotaryArgs a = {};
   const elsaa_status st = rotary_args(p, table, q_weight, k_weight, ws, ws_bytes, &a);
   if (st != ELSAA_OK) return st;
+  if (!token_order_ok(p, positions)) return ELSAA_ERR_INVALID_ARG;
   if (!q || !qo || (k == nullptr) != (ko == nullptr) || !aligned4(positions)) return ELSAA_ERR_INVALID_ARG;
   for (const void* x : {q, k, (const void*)qo, (const void*)ko})
     if (!aligned16(x)) return ELSAA_ERR_INVALID_ARG;
@@ -172,6 +179,7 @@ elsaa_status elsaa_rotary_backward(const elsaa_rotary_params* p, const void* q, 
   RotaryArgs a = {};
   const elsaa_status st = rotary_args(p, table, q_weight, k_weight, ws, ws_bytes, &a);
   if (st != ELSAA_OK) return st;
+  if (!token_order_ok(p, positions)) return ELSAA_ERR_INVALID_ARG;
   if (!q || !dqo || !dq || (k == nullptr) != (dko == nullptr) || (k == nullptr) != (dk == nullptr))
     return ELSAA_ERR_INVALID_ARG;
   if (!p->norm && (dq_weight || dk_weight)) return ELSAA_ERR_INVALID_ARG;

@@ -159,7 +159,8 @@ class NormRotateFunction(torch.autograd.Function):
 def norm_rotate(q, k, table=None, q_weight=None, k_weight=None, positions=None, rot_dim=None,
                 interleaved=False, norm=True, eps=1e-6):
     """Differentiable norm and rotation of q [B, H, N, d] and k [B, Hkv, N, d]; ``table`` as
-    ``angle_table`` makes it (None: norm only).  In a captured step as ``window.window_attention``."""
+    ``angle_table`` makes it (None: norm only), with a row for every token where there are no
+    ``positions``.  In a captured step as ``window.window_attention``."""
     B, H, N, d = q.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")

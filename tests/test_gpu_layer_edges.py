@@ -63,3 +63,24 @@ def test_sequences_that_do_not_fit_are_left_out_whole(cuda_device, dt, starts, l
     assert torch.equal(kp, k0) and torch.equal(vp, v0)     # nothing else in the pools has changed
     assert (qo[~touched] == 5.0).all() and (y[~touched] == 5.0).all()
     assert torch.isfinite(y).all() and (y[touched] != 5.0).any(-1).all()
+
+
+# ---- positions -------------------------------------------------------------------
+
+def test_a_short_angle_table_is_refused(cuda_device):
+    """Through every entry point that takes tokens in order; a table of N rows, or positions, or no rotation serve."""
+    q, k = rand((1, 2, 20, 64), torch.bfloat16, 1), rand((1, 1, 20, 64), torch.bfloat16, 2)
+    short = rotary.angle_table(19, 64, device=cuda_device)
+    p = rotary.RotaryParams.make(1, 2, 1, 20, 64, "bf16", 64, 19)
+    for call in (lambda: rotary.norm_rotate(q, k, short), lambda: rotary.QkRotary(short).apply(q, k),
+                 lambda: rotary.forward(p, q, k, short), lambda: rotary.forward(p, q, None, short),
+                 lambda: rotary.backward(p, q, k, short, None, None, q, k)):
+        with pytest.raises(B.ElsaaError) as e:
+            call()
+        assert e.value.code == 1
+    pos = torch.arange(20, dtype=torch.int32, device=cuda_device).clamp(max=18)[None]
+    some = rotary.norm_rotate(q, k, short, positions=pos)
+    whole = rotary.norm_rotate(q, k, rotary.angle_table(20, 64, device=cuda_device))
+    for a, b in zip(some, whole):
+        assert torch.equal(a[:, :, :19], b[:, :, :19]) and a[:, :, 19].any()
+    rotary.norm_rotate(q, k)                   # norm only

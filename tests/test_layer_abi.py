@@ -97,6 +97,16 @@ def test_rotary_refusals():
     assert code == 1
 
 
+@pytest.mark.parametrize("N,max_pos,rot_dim,code", [(100, 99, 32, 1), (8192, 4096, 64, 1), (2, 1, 16, 1)])
+def test_rotary_refuses_a_table_without_a_row_for_every_token(N, max_pos, rot_dim, code):
+    """Tokens in order 0 .. N - 1 (no positions) need N rows of the table, forward and backward."""
+    p = rot(N=N, max_pos=max_pos, rot_dim=rot_dim)
+    assert rotary.validate(p) == 0             # (with positions it is a valid problem)
+    assert rotary_call(p) == code
+    assert B.lib().elsaa_rotary_backward(ctypes.byref(p), GOOD, GOOD, NULL, NULL, GOOD, NULL, NULL, GOOD, GOOD, GOOD,
+                                         GOOD, NULL, NULL, GOOD, rotary.workspace_bytes(p), NULL) == code
+
+
 def test_window_refusals():
     p = win()
     L = B.lib()
