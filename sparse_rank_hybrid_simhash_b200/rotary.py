@@ -140,9 +140,9 @@ class NormRotateFunction(torch.autograd.Function):
     """Autograd wrapper: forward and backward both run in libelsaa."""
 
     @staticmethod
-    def forward(ctx, q, k, table, q_weight, k_weight, positions, params: RotaryParams):
-        qo, ko = forward(params, q, k, table, q_weight, k_weight, positions)
-        ctx.params = params
+    def forward(ctx, q, k, table, q_weight, k_weight, positions, params: RotaryParams, ws=None):
+        qo, ko = forward(params, q, k, table, q_weight, k_weight, positions, ws=ws)
+        ctx.params, ctx.ws = params, ws
         ctx.save_for_backward(q, k, table, q_weight, k_weight, positions)
         return qo, ko
 
@@ -151,16 +151,19 @@ class NormRotateFunction(torch.autograd.Function):
     def backward(ctx, dqo, dko):
         q, k, table, q_weight, k_weight, positions = ctx.saved_tensors
         dq, dk, dwq, dwk = backward(ctx.params, q, k, table, q_weight, k_weight, dqo, dko,
-                                    positions)
+                                    positions, ws=ctx.ws)
         return (dq, dk, None, dwq if q_weight is not None else None,
-                dwk if k_weight is not None else None, None, None)
+                dwk if k_weight is not None else None, None, None, None)
 
 
 def norm_rotate(q, k, table=None, q_weight=None, k_weight=None, positions=None, rot_dim=None,
-                interleaved=False, norm=True, eps=1e-6):
+                interleaved=False, norm=True, eps=1e-6, ws=None):
     """Differentiable norm and rotation of q [B, H, N, d] and k [B, Hkv, N, d]; ``table`` as
     ``angle_table`` makes it (None: norm only), with a row for every token where there are no
-    ``positions``.  In a captured step as ``window.window_attention``."""
+    ``positions``.  ``ws`` (``alloc_workspace``) serves the forward and the backward; what they
+    record on the device (positions outside the table, whose rows are zeros) is read with
+    ``binding.check(ws)``.  Without it each makes its own, and the record is lost with it.  In a
+    captured step as ``window.window_attention``."""
     B, H, N, d = q.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")
@@ -168,7 +171,7 @@ def norm_rotate(q, k, table=None, q_weight=None, k_weight=None, positions=None, 
         rot_dim = 0 if table is None else 2 * table.shape[1]
     p = RotaryParams.make(B, H, k.shape[1], N, d, q.dtype, rot_dim,
                           0 if table is None else table.shape[0], interleaved, norm, eps)
-    return NormRotateFunction.apply(q, k, table, q_weight, k_weight, positions, p)
+    return NormRotateFunction.apply(q, k, table, q_weight, k_weight, positions, p, ws)
 
 
 class QkRotary(NamedTuple):
@@ -180,7 +183,8 @@ class QkRotary(NamedTuple):
     interleaved: bool = False
     norm: bool = True
     eps: float = 1e-6
+    ws: Optional[torch.Tensor] = None
 
     def apply(self, q, k):
         return norm_rotate(q, k, self.table, self.q_weight, self.k_weight, self.positions,
-                           interleaved=self.interleaved, norm=self.norm, eps=self.eps)
+                           interleaved=self.interleaved, norm=self.norm, eps=self.eps, ws=self.ws)

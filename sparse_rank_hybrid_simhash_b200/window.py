@@ -104,9 +104,9 @@ class WindowFunction(torch.autograd.Function):
     """Autograd wrapper: forward and backward both run in libelsaa."""
 
     @staticmethod
-    def forward(ctx, q, k, v, lengths, params: WindowParams):
-        y, lse = forward(params, q, k, v, lengths)
-        ctx.params = params
+    def forward(ctx, q, k, v, lengths, params: WindowParams, ws=None):
+        y, lse = forward(params, q, k, v, lengths, ws=ws)
+        ctx.params, ctx.ws = params, ws
         ctx.save_for_backward(q, k, v, y, lse, lengths)
         return y
 
@@ -114,11 +114,15 @@ class WindowFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         q, k, v, y, lse, lengths = ctx.saved_tensors
-        return (*backward(ctx.params, q, k, v, y, lse, dy, lengths), None, None)
+        return (*backward(ctx.params, q, k, v, y, lse, dy, lengths, ws=ctx.ws), None, None, None)
 
 
-def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0):
+def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0, ws=None):
     """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d].
+
+    ``ws`` (``alloc_workspace``) serves the forward and the backward; what they record on the
+    device (a wait that gave up) is read with ``binding.check(ws)``.  Without it each makes its
+    own, and the record is lost with it.
 
     A step captured in a CUDA graph must find no eager autograd graph of the same leaves alive
     (an output not yet dropped or detached): autograd would sum their gradients on that graph's
@@ -127,4 +131,4 @@ def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0):
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")
     p = WindowParams.make(B, H, k.shape[1], N, d, q.dtype, window, sinks, scale)
-    return WindowFunction.apply(q, k, v, lengths, p)
+    return WindowFunction.apply(q, k, v, lengths, p, ws)

@@ -84,3 +84,41 @@ def test_a_short_angle_table_is_refused(cuda_device):
     for a, b in zip(some, whole):
         assert torch.equal(a[:, :, :19], b[:, :, :19]) and a[:, :, 19].any()
     rotary.norm_rotate(q, k)                   # norm only
+
+
+def test_records_of_the_autograd_functions_can_be_read(cuda_device):
+    """With a workspace of the caller's: positions outside the table, in the forward and the backward."""
+    q, k = (rand((1, h, 20, 64), torch.bfloat16, h).requires_grad_() for h in (2, 1))
+    tab = rotary.angle_table(20, 64, device=cuda_device)
+    ws = rotary.alloc_workspace(rotary.RotaryParams.make(1, 2, 1, 20, 64, "bf16", 64, 20), cuda_device)
+    pos = torch.arange(20, dtype=torch.int32, device=cuda_device)[None]
+    for at, bad in ((pos, False), (pos + 1, True), (pos - 1, True)):
+        qo, ko = rotary.norm_rotate(q, k, tab, positions=at, ws=ws)
+        for _ in range(2):                     # the forward's record, then the backward's
+            if bad:
+                with pytest.raises(B.ElsaaError) as e:
+                    B.check(ws)
+                assert e.value.code == 6
+            B.check(ws)
+            (qo.float().sum() + ko.float().sum()).backward(retain_graph=True)
+        q.grad = k.grad = None
+    # through ELSAA's own call, and through the attention (its error word set by hand)
+    qo, ko = rotary.QkRotary(tab, positions=pos + 1, ws=ws).apply(q, k)
+    with pytest.raises(B.ElsaaError):
+        B.check(ws)
+    ws = window.alloc_workspace(window.WindowParams.make(1, 2, 1, 20, 64, "bf16", 8), cuda_device)
+    y = window.window_attention(q, k, k, window=8, ws=ws)
+    want = window.window_attention(q, k, k, window=8)
+    assert torch.equal(y, want)
+    ws[0] = 1
+    a, b = torch.autograd.grad(y.float().sum(), (q, k)), torch.autograd.grad(want.float().sum(), (q, k))
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    with pytest.raises(B.ElsaaError) as e:     # the calls only ever set it
+        B.check(ws)
+    assert e.value.code == 5
+    # one for the forward alone is too small for the backward
+    small = window.alloc_workspace(window.WindowParams.make(1, 2, 1, 20, 64, "bf16", 8), cuda_device, backward=False)
+    y = window.window_attention(q, k, k, window=8, ws=small)
+    with pytest.raises(B.ElsaaError) as e:
+        y.float().sum().backward()
+    assert e.value.code == 3
