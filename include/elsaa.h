@@ -402,9 +402,10 @@ size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backwa
 /* y = softmax(scale q k^T) v over the keys j <= i with i - j < window or
  * j < sinks.  lengths: device int32 [B] of a padded batch's token counts
  * (clamped to [0, N]), or NULL for N: rows at or behind a length are read into
- * no result, whatever they hold, and their y is zero and lse -inf.  Values that
- * are not finite within a length are outside the contract (0 * inf in a masked
- * place).  lse: device fp32 [B, H, N] dense, the log of the row's sum of
+ * no result, whatever they hold, and their y is zero and lse -inf.  A key that a
+ * row does not see enters it with exactly zero, whatever finite value it has;
+ * values that are not finite within a length are outside the contract (0 * inf
+ * in a masked place).  lse: device fp32 [B, H, N] dense, the log of the row's sum of
  * exponentials.  strides: q, k, v, y. */
 elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, const void* k,
                                   const void* v, const int64_t* strides, const int32_t* lengths,

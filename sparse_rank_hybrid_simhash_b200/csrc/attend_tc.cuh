@@ -35,12 +35,15 @@ ELSAA_DEV float ex2(float x) {
 // 2^x of a pair on the FMA pipe, relative error below 2.4e-7 (ex2.approx: 2^-22):
 // x = n + f with n the nearest whole number (Cody and Waite's reduction, by adding
 // and taking off 1.5 2^23) and a degree-5 polynomial of f in [-1/2, 1/2], minimax in
-// the relative error (Remez exchange).  x below -125 counts as -125: a masked score
-// gives 2^-125, nothing next to a row's sum.  NaN does not come out finite and small.
+// the relative error (Remez exchange).  x below -127 counts as -127, where n = x and f = 0:
+// the last coefficient's bits (one unit over 1) less 127 in the exponent are 2^-149, so a
+// masked score's probability is zero once it is bf16 and no value behind it enters the row,
+// however large (at -125 a value of 2^127 came through as 4).  Between -127 and -126 the
+// result is off by up to 2^-127.  NaN does not come out finite and small.
 ELSAA_DEV void exp2_fma(float& x0, float& x1) {
   constexpr float kMagic = 12582912.0f;
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x0));   // -125
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x1));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));   // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
   float t0 = x0, t1 = x1;
   add2(t0, t1, kMagic, kMagic);
   float n0 = t0, n1 = t1;

@@ -122,3 +122,40 @@ def test_records_of_the_autograd_functions_can_be_read(cuda_device):
     with pytest.raises(B.ElsaaError) as e:
         y.float().sum().backward()
     assert e.value.code == 3
+
+
+# ---- masked keys --------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,N,d,dt,win,sinks", [
+    (2, 1, 260, 64, "bf16", 40, 0), (3, 3, 260, 128, "bf16", 40, 0), (4, 2, 330, 128, "bf16", 0, 0),
+    (2, 2, 260, 64, "bf16", 33, 2), (2, 1, 200, 32, "bf16", 40, 0), (2, 1, 260, 64, "f32", 40, 2)])
+def test_window_values_of_masked_keys_are_in_no_row(cuda_device, H, Hkv, N, d, dt, win, sinks):
+    """A key that a row does not see leaves the row's bits alone, however large its value."""
+    q, k, v = (rand((1, h, N, d), DT[dt], 40 + i) for i, h in enumerate((H, Hkv, Hkv)))
+    p = window.WindowParams.make(1, H, Hkv, N, d, dt, win, sinks)
+    y, lse = window.forward(p, q, k, v)
+    for j in (2, 66, 67, 74, 107, 130, 203):    # (every eighth pair of keys takes another exponential)
+        if j >= N:
+            continue
+        v2 = v.clone()
+        v2[:, :, j] = 1e38
+        y2, lse2 = window.forward(p, q, k, v2)
+        blind = ~ref.visible(N, N, 0, win, sinks, cuda_device)[:, j]
+        assert blind.any() and torch.equal(y[:, :, blind], y2[:, :, blind]) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("H,Hkv,d,dt,seqs,win", [
+    (8, 2, 64, "bf16", [(60, 300), (33, 200)], 50), (8, 2, 128, "bf16", [(200, 300)], 0),
+    (4, 2, 128, "bf16", [(1, 200), (4, 170)], 40), (4, 2, 32, "bf16", [(60, 300)], 50), (4, 2, 64, "f32", [(60, 300)], 50)])
+def test_paged_values_of_masked_keys_are_in_no_row(cuda_device, H, Hkv, d, dt, seqs, win):
+    p, q, kp, vp, table, starts, lengths = paged_inputs((H, Hkv, d, dt, 16, win, 0, seqs), slack=0)
+    y = paged.attend(p, q, kp, vp, table, starts, lengths)
+    n, x = seqs[0]
+    for j in (106, 130, 131, 162, 234, 251):
+        if j >= x:
+            continue
+        v2 = vp.clone()
+        v2[table[0, j // 16].long(), :, j % 16] = 1e38
+        y2 = paged.attend(p, q, kp, v2, table, starts, lengths)
+        blind = ~ref.visible(n, x, x - n, win, 0, cuda_device)[:, j]
+        assert torch.equal(y[:n][blind], y2[:n][blind]) and torch.equal(y[n:], y2[n:])
