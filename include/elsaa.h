@@ -404,8 +404,9 @@ size_t elsaa_window_workspace_bytes(const elsaa_window_params* p, int32_t backwa
  * (clamped to [0, N]), or NULL for N: rows at or behind a length are read into
  * no result, whatever they hold, and their y is zero and lse -inf.  A key that a
  * row does not see enters it with exactly zero, whatever finite value it has;
- * values that are not finite within a length are outside the contract (0 * inf
- * in a masked place).  lse: device fp32 [B, H, N] dense, the log of the row's sum of
+ * a NaN within a length leaves the rows that see it not finite (their gradients
+ * too); otherwise values that are not finite there are outside the contract
+ * (0 * inf in a masked place).  lse: device fp32 [B, H, N] dense, the log of the row's sum of
  * exponentials.  strides: q, k, v, y. */
 elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, const void* k,
                                   const void* v, const int64_t* strides, const int32_t* lengths,

@@ -611,7 +611,9 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
       }
       // rows of the result: final (the item is whole in this CTA) or partial
       const bool whole = !PAGED || (it.n0 == 0 && it.n1 == it.nblk);
-      float w0 = any ? 1.f : 0.f, w1 = 0.f;   // weights of O of this stream and of stream 1
+      // weights of O of this stream and of stream 1 (0: no keys seen there, O not read; a row
+      // whose scores were all NaN has no maximum either, but a NaN sum, and stays NaN)
+      float w0 = any ? 1.f : 0.f, w1 = 0.f;
       if (PAGED && it.split) {
         // stream 0 reads both O (a row's lane is the same in both)
         if (st == 1) {
@@ -624,15 +626,15 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           if (!ok) break;
           fence_after();
           const float m1 = ml1[row], l1 = ml1[128 + row], mm = fmaxf(m, m1);
-          w0 = m > -INFINITY ? ex2(m - mm) : 0.f;
-          w1 = m1 > -INFINITY ? ex2(m1 - mm) : 0.f;
+          w0 = m > -INFINITY ? ex2(m - mm) : 0.f * l;
+          w1 = m1 > -INFINITY ? ex2(m1 - mm) : 0.f * l1;
           l = l * w0 + l1 * w1;
           m = mm;
         }
       }
       const bool out = !(PAGED && it.split && st == 1);
       if (out && PAGED && warp_live) {
-        const bool two = it.split && __any_sync(0xffffffffu, w1 > 0.f);
+        const bool two = it.split && __any_sync(0xffffffffu, w1 != 0.f);
         const int slot = ((int)blockIdx.x * 2 + (it.order > 0 ? 1 : 0)) * 2 + st;
         const float inv = !whole ? 1.f : l > 0.f ? 1.0f / l : 0.f;
         __nv_bfloat16* yrow = nullptr;
@@ -653,8 +655,8 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            ov[e] = w0 > 0.f ? ov[e] * (w0 * inv) : 0.f;
-            if (two && w1 > 0.f) ov[e] += ow[e] * (w1 * inv);
+            ov[e] = w0 != 0.f ? ov[e] * (w0 * inv) : 0.f;
+            if (two && w1 != 0.f) ov[e] += ow[e] * (w1 * inv);
           }
           if (yrow != nullptr) store32(yrow + 32 * c, ov);
           if (prow != nullptr) {
@@ -680,12 +682,12 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         }
       }
       if (!PAGED) {
-        // rows at and behind the length: zeros
-        const float inv = live && l > 0.f ? 1.0f / l : 0.f;
+        // rows at and behind the length: zeros (a live row sees its own key: l > 0, or NaN)
+        const float inv = live ? 1.0f / l : 0.f;
         const bool store = r < a.N;
         if (store)
           a.lse[((int64_t)it.b * a.H + pick(it.h, st)) * a.N + r] =
-              live && l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+              live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         __nv_bfloat16* yrow = static_cast<__nv_bfloat16*>(a.y) + (int64_t)it.b * a.sy.b +
                               (int64_t)pick(it.h, st) * a.sy.h + (int64_t)r * a.sy.n;
 #pragma unroll
@@ -696,7 +698,7 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = inv > 0.f ? ov[e] * inv : 0.f;
+          for (int e = 0; e < 32; ++e) ov[e] = live ? ov[e] * inv : 0.f;
           if (store) store32(yrow + 32 * c, ov);
         }
       }

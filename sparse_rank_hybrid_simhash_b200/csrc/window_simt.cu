@@ -233,12 +233,13 @@ window_fwd_simt_kernel(const AttendArgs a, int tiles) {
   for (int x = 0; x < RT; ++x) {
     const int n = r0 + RT * ty + x;
     if (n >= a.N) continue;
-    const float inv = st.l[x] > 0.f ? 1.0f / st.l[x] : 0.f;
+    const bool some = st.l[x] != 0.f;   // (NaN too: a score was)
+    const float inv = some ? 1.0f / st.l[x] : 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) st.o[x][c] *= inv;
     store_cols<T, D>(static_cast<T*>(a.y) + b * a.sy.b + h * a.sy.h + n * a.sy.n, st.o[x]);
     if (tx == 0)
-      a.lse[(int64_t)bh * a.N + n] = st.l[x] > 0.f ? st.m[x] + logf(st.l[x]) : -INFINITY;
+      a.lse[(int64_t)bh * a.N + n] = some ? st.m[x] + logf(st.l[x]) : -INFINITY;
   }
 }
 

@@ -159,3 +159,51 @@ def test_paged_values_of_masked_keys_are_in_no_row(cuda_device, H, Hkv, d, dt, s
         y2 = paged.attend(p, q, kp, v2, table, starts, lengths)
         blind = ~ref.visible(n, x, x - n, win, 0, cuda_device)[:, j]
         assert torch.equal(y[:n][blind], y2[:n][blind]) and torch.equal(y[n:], y2[n:])
+
+
+# ---- NaN is not lost ------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,N,d,dt,win", [(2, 1, 260, 64, "bf16", 40), (3, 3, 260, 128, "bf16", 0),
+                                              (2, 2, 200, 32, "bf16", 40), (2, 1, 260, 64, "f32", 40)])
+def test_window_nan_stays(cuda_device, H, Hkv, N, d, dt, win):
+    """Rows of a NaN query, and rows that see a NaN key, are not finite, in y, lse and the gradients."""
+    q, k, v, dy = (rand((1, h, N, d), DT[dt], 50 + i) for i, h in enumerate((H, Hkv, Hkv, H)))
+    p = window.WindowParams.make(1, H, Hkv, N, d, dt, win, 0)
+    y0, _ = window.forward(p, q, k, v)
+    rows = torch.tensor([0, 5, 130, N - 1], device=cuda_device)
+    q2 = q.clone()
+    q2[:, :, rows] = float("nan")
+    y, lse = window.forward(p, q2, k, v)
+    assert y[:, :, rows].isnan().all() and lse[:, :, rows].isnan().all()
+    rest = torch.ones(N, dtype=torch.bool, device=cuda_device)
+    rest[rows] = False
+    assert torch.equal(y[:, :, rest], y0[:, :, rest]) and lse[:, :, rest].isfinite().all()
+    dq, dk, dv = window.backward(p, q2, k, v, y, lse, dy)
+    assert not dq[:, :, rows].isfinite().any() and dq[:, :, rest].isfinite().all()
+    assert not dk[:, :, rows].isfinite().all(-1).any() and not dv[:, :, rows].isfinite().all(-1).any()
+    for j in (3, 64, 99):
+        k2 = k.clone()
+        k2[:, :, j] = float("nan")
+        y, lse = window.forward(p, q, k2, v)
+        sees = ref.visible(N, N, 0, win, 0, cuda_device)[:, j]
+        assert not y[:, :, sees].isfinite().any() and torch.equal(y[:, :, ~sees], y0[:, :, ~sees])
+        dq, dk, _ = window.backward(p, q, k2, v, y, lse, dy)
+        assert not dq[:, :, sees].isfinite().all(-1).any() and not dk[:, :, j].isfinite().all(-1).any()
+
+
+@pytest.mark.parametrize("H,Hkv,d,dt,seqs", [
+    (8, 2, 64, "bf16", [(60, 700), (33, 200)]), (4, 4, 128, "bf16", [(100, 900)]), (8, 2, 128, "bf16", [(1, 900), (2, 60)]),
+    (4, 2, 32, "bf16", [(1, 2000)]), (4, 2, 64, "f32", [(60, 300), (1, 2000)])])
+def test_paged_nan_stays(cuda_device, H, Hkv, d, dt, seqs):
+    p, q, kp, vp, table, starts, lengths = paged_inputs((H, Hkv, d, dt, 16, 0, 0, seqs), slack=0)
+    y0 = paged.attend(p, q, kp, vp, table, starts, lengths)
+    assert y0.isfinite().all()
+    q2 = q.clone()
+    q2[0] = float("nan")
+    y = paged.attend(p, q2, kp, vp, table, starts, lengths)
+    assert y[0].isnan().all() and torch.equal(y[1:], y0[1:])
+    n = seqs[0][0]
+    k2 = kp.clone()
+    k2[table[0, 1].long(), :, 7] = float("nan")
+    y = paged.attend(p, q, k2, vp, table, starts, lengths)
+    assert not y[:n].isfinite().any() and torch.equal(y[n:], y0[n:])
