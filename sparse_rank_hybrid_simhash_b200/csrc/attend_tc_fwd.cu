@@ -52,6 +52,7 @@
 
 #include "attend_tc.cuh"
 #include "internal.h"
+#include "ring_drain.h"
 
 namespace elsaa {
 namespace {
@@ -150,6 +151,7 @@ struct Bars {
   uint64_t x_full, x_done;      // a split item: O of stream 1 given, and read
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
+  uint32_t loads[2];            // copies into the ring that K's and V's warp have started
   uint32_t tmem;
   Cut cut;                      // a paged CTA's first item
   int64_t per;                  // units of a run
@@ -819,16 +821,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
         if (!ok) break;
         give_back();
       }
-      // every copy this warp started has landed before the CTA may exit
       if (lane == 0) {
-        for (uint32_t m = loads > SL / 2 ? loads - SL / 2 : 0; m < loads; ++m) {
-          const uint32_t i = 2 * m + kv;
-          mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
-        }
+        bars->loads[kv] = loads;
         if (nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, a.err);
       }
       __syncwarp();
-
     } else {
       // ------------------------------------------------------------------ products
       // a warp a stream: one's waits and bookkeeping run under the other's products
@@ -925,6 +922,11 @@ attend_fwd_kernel(const __grid_constant__ Maps maps, const AttendArgs a, const S
   }
   fence_before();
   __syncthreads();
+  if (tid == 32 * kKWarp) {   // every copy has landed before the CTA exits, after a wait that gave up too
+    const RingDrain ring{SL, bars->loads[0], bars->loads[1]};
+    for (uint32_t i = ring.begin(); i < ring.end(); ++i)
+      if (ring.open(i)) mbar_wait(&bars->full[i % SL], (i / SL) & 1, a.err);
+  }
   if (warp == kMmaWarp) {
     fence_after();
     tmem_dealloc(tmem, kTmemCols);
