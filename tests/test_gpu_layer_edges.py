@@ -7,7 +7,7 @@ import torch
 import layer_reference as ref
 from sparse_rank_hybrid_simhash_b200 import binding as B
 from sparse_rank_hybrid_simhash_b200 import paged, rotary, window
-from test_gpu_layer import DT, paged_inputs, rand
+from test_gpu_layer import DT, heads, paged_inputs, rand, window_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +207,125 @@ def test_paged_nan_stays(cuda_device, H, Hkv, d, dt, seqs):
     k2[table[0, 1].long(), :, 7] = float("nan")
     y = paged.attend(p, q, k2, vp, table, starts, lengths)
     assert not y[:n].isfinite().any() and torch.equal(y[n:], y0[n:])
+
+
+# ---- the paths of larger sizes ----------------------------------------------------------
+
+@pytest.mark.parametrize("case", [
+    # many heads a lane group, not a multiple of what is loaded together
+    (2, 15, 5, 10000, 64, "bf16", 64, False, True), (1, 21, 7, 9700, 128, "bf16", 96, True, False),
+    (2, 15, 5, 10000, 32, "f32", 32, False, False), (1, 18, 3, 4800, 128, "f32", 128, True, True)], ids=str)
+def test_rotary_many_heads_a_group(cuda_device, case):
+    B_, H, Hkv, N, d, dt, rot, il, fused = case
+    q, k, gq, gk = (heads(B_, h, N, d, DT[dt], 60 + i, fused) for i, h in enumerate((H, Hkv, H, Hkv)))
+    wq, wk = (1 + rand((d,), torch.float32, s, 0.2) for s in (64, 65))
+    tab = rotary.angle_table(N, rot, device=cuda_device)
+    p = rotary.RotaryParams.make(B_, H, Hkv, N, d, dt, rot, N, il, True, 1e-5)
+    ws = rotary.alloc_workspace(p, cuda_device)
+    qo, ko = rotary.forward(p, q, k, tab, wq, wk, ws=ws)
+    dq, dk, dwq, dwk = rotary.backward(p, q, k, tab, wq, wk, gq, gk, ws=ws)
+    B.check(ws)
+    at = torch.arange(N, device=cuda_device).expand(B_, 1, N)
+    for x, w, g, o, dx, dw in ((q, wq, gq, qo, dq, dwq), (k, wk, gk, ko, dk, dwk)):
+        val, tol = ref.rotary(x, w, at.expand(x.shape[:3]), tab, il, True, 1e-5, dy=g)
+        for name, got in (("y", o), ("dx", dx), ("dw", dw)):
+            ref.close(got, val[name], tol[name], name)
+    # in place, both ways
+    rotary.forward(p, q, k, tab, wq, wk, qo=(a := q.clone()), ko=(b := k.clone()), ws=ws)
+    assert torch.equal(a, qo) and torch.equal(b, ko)
+    a, b = q.clone(), k.clone()
+    rotary.forward(p, a, b, tab, wq, wk, qo=a, ko=b, ws=ws)
+    assert torch.equal(a, qo) and torch.equal(b, ko)
+    a, b = gq.clone(), gk.clone()
+    got = rotary.backward(p, q, k, tab, wq, wk, a, b, dq=a, dk=b, ws=ws)
+    assert all(torch.equal(x, y) for x, y in zip(got, (dq, dk, dwq, dwk)))
+
+
+@pytest.mark.parametrize("H,Hkv,d,dt,seqs", [
+    (13, 13, 128, "bf16", [(1700, 1800), (0, 5), (3300, 3301)]), (12, 6, 64, "f32", [(2600, 2600), (2500, 2501)]),
+    # more sequences than a block keeps the starts of, some of them without new tokens
+    (4, 2, 64, "bf16", [(b % 3, 20 + b % 40) for b in range(2500)])], ids=["heads-bf16", "heads-f32", "2500-sequences"])
+def test_paged_write_of_many_rows(cuda_device, H, Hkv, d, dt, seqs):
+    p, q, kp, vp, table, starts, lengths = paged_inputs((H, Hkv, d, dt, 16, 0, 0, seqs))
+    kp, vp = rand(kp.shape, DT[dt], 70), rand(vp.shape, DT[dt], 71)
+    k, v = (rand((p.rows, Hkv, d), DT[dt], s) for s in (72, 73))
+    wq, wk = (1 + rand((d,), torch.float32, s, 0.2) for s in (74, 75))
+    most = max(x for _, x in seqs)
+    tab = rotary.angle_table(most, d, device=cuda_device)
+    rp = rotary.RotaryParams.make(1, H, Hkv, 1, d, dt, d, most)
+    ws = paged.alloc_workspace(p, cuda_device)
+    k0, v0 = kp.clone(), vp.clone()
+    qo = torch.full_like(q, 5.0)
+    paged.write(p, rp, q, k, v, tab, wq, wk, kp, vp, table, starts, lengths, qo=qo, ws=ws)
+    B.check(ws)
+    end = int(starts[-1])
+    pos = torch.cat([torch.arange(x - n, x) for n, x in seqs]).to(cuda_device)
+    seq = torch.repeat_interleave(torch.arange(len(seqs)), torch.tensor([n for n, _ in seqs])).to(cuda_device)
+    at = (table.long()[seq, pos // 16], slice(None), pos % 16)
+    for x, w, got in ((q[:end], wq, qo[:end]), (k[:end], wk, kp[at])):
+        val, tol = ref.rotary(x, w, pos[:, None].expand(x.shape[:2]), tab, False, True, 1e-6)
+        ref.close(got, val["y"], tol["y"])
+    assert (qo[end:] == 5.0).all() and torch.equal(vp[at], v[:end])
+    kp[at], vp[at] = k0[at], v0[at]
+    assert torch.equal(kp, k0) and torch.equal(vp, v0)
+
+
+@pytest.mark.parametrize("case", [
+    # more sequences than lanes for the tensor-core kernel's walk, some of them without new tokens
+    (8, 2, 64, "bf16", 16, 0, 0, [(0 if b % 7 == 3 else 6 + b % 20, 30 + 11 * b) for b in range(40)]),
+    (4, 1, 128, "bf16", 32, 100, 3, [(0 if b % 5 == 0 else 1 + 7 * b % 60, 60 + 5 * b) for b in range(70)]),
+    (2, 2, 64, "bf16", 16, 0, 0, [(0, 9)] * 33 + [(600, 700)] + [(0, 5)] * 3),
+    # the CUDA-core kernel's
+    (8, 2, 64, "f32", 16, 0, 0, [(0 if b % 7 == 3 else 6 + b % 20, 30 + 11 * b) for b in range(40)]),
+    # a long chunk among single tokens; as many sequences as a large server decodes
+    (2, 2, 64, "bf16", 16, 0, 0, [(1, 40 + b) for b in range(63)] + [(900, 1200)]),
+    (4, 2, 128, "bf16", 16, 0, 0, [(b % 2, 1 + b % 90) for b in range(2100)])],
+    ids=["tc-40", "tc-70", "tc-one-of-37", "f32-40", "chunk-among-tokens", "decode-2100"])
+def test_paged_attend_many_sequences(cuda_device, case):
+    p, q, kp, vp, table, starts, lengths = paged_inputs(case)
+    want, tol = ref.paged(q, kp, vp, table, starts, lengths, p.window, p.sinks)
+    ws = paged.alloc_workspace(p, cuda_device)
+    y = torch.full_like(q, 5.0)
+    paged.attend(p, q, kp, vp, table, starts, lengths, y=y, ws=ws)
+    B.check(ws)
+    end = int(starts[-1])
+    ref.close(y[:end], want[:end], tol[:end], "y")
+    assert (y[end:] == 5.0).all() and not ws[:8192].any()
+
+
+@pytest.mark.parametrize("case", [
+    # 64-row query and key tiles in fp32
+    (2, 8, 4, 500, 64, "f32", 100, 0, None, False), (2, 8, 4, 500, 128, "f32", 70, 3, (500, 321), True),
+    (1, 12, 12, 600, 64, "f32", 0, 0, None, True), (1, 12, 3, 900, 128, "f32", 20, 1, (850,), False),
+    (2, 12, 12, 1300, 64, "f32", 30, 5, (1300, 700), False)], ids=str)
+def test_window_large_tiles_in_fp32(cuda_device, case):
+    p, q, k, v, dy, lens = window_inputs(case, seed=110)
+    val, tol = ref.window(q, k, v, p.window, p.sinks, lens, dy=dy)
+    ws = window.alloc_workspace(p, cuda_device)
+    y, lse = window.forward(p, q, k, v, lengths=lens, ws=ws)
+    grads = window.backward(p, q, k, v, y, lse, dy, lengths=lens, ws=ws)
+    B.check(ws)
+    for name, g in zip(("y", "lse", "dq", "dk", "dv"), (y, lse, *grads)):
+        ref.close(g, val[name], tol[name], name)
+    assert not ws[:8192].any()
+
+
+def test_calls_at_the_same_time(cuda_device):
+    """Two streams with a workspace each, window steps on one and decoding on the other."""
+    p, q, k, v, dy, lens = window_inputs((4, 16, 4, 1100, 64, "bf16", 300, 3, (1100, 0, 100, 1), False))
+    y, lse = window.forward(p, q, k, v, lengths=lens)
+    want = (y, lse, *window.backward(p, q, k, v, y, lse, dy, lengths=lens))
+    pp, *args = paged_inputs((8, 2, 128, "bf16", 16, 0, 0, [(1, 900 + 13 * b) for b in range(9)]), slack=0)
+    pwant = paged.attend(pp, *args)
+    ws, pws = window.alloc_workspace(p, cuda_device), paged.alloc_workspace(pp, cuda_device)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got, pgot = [], []
+    for _ in range(5):
+        y, lse = window.forward(p, q, k, v, lengths=lens, ws=ws, stream=s)
+        got.append((y, lse, *window.backward(p, q, k, v, y, lse, dy, lengths=lens, ws=ws, stream=s)))
+        pgot += [paged.attend(pp, *args, ws=pws, stream=t) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    assert all(torch.equal(g, pwant) for g in pgot)
+    B.check(ws), B.check(pws)
