@@ -26,11 +26,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+// The encoder wants a context current on the calling thread.  A thread whose first call into
+// CUDA this is (a server's worker, the thread that autograd runs a backward on) has none until
+// the runtime is initialised there, which setting its device does (once a thread and device;
+// no work on a stream, so captures go on).
+cudaError_t bind_thread() {
+  static thread_local int bound = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != bound && (e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
+  return e;
+}
+
+// The encoder, or null where there is none (*e: why).
+PFN_cuTensorMapEncodeTiled_v12000 encoder(cudaError_t* e) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  *e = fn == nullptr ? cudaErrorNotSupported : bind_thread();
+  return *e == cudaSuccess ? fn : nullptr;
+}
 }  // namespace
 
 cudaError_t make_row_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t width) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return cudaErrorNotSupported;
+  cudaError_t e;
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder(&e);
+  if (fn == nullptr) return e;
   const cuuint64_t dims[2] = {width, rows};
   const cuuint64_t strides[1] = {width * 2};
   const cuuint32_t box[2] = {64, 1};
@@ -44,8 +64,9 @@ cudaError_t make_row_map(CUtensorMap* map, const void* base, uint64_t rows, uint
 
 cudaError_t make_slab_map(CUtensorMap* map, const void* base, uint64_t units, uint64_t n,
                           uint64_t d, uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return cudaErrorNotSupported;
+  cudaError_t e;
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder(&e);
+  if (fn == nullptr) return e;
   const cuuint64_t dims[3] = {d, n, units};
   const cuuint64_t strides[2] = {d * 2, n * d * 2};
   const cuuint32_t box[3] = {8, box_rows, 1};
@@ -59,8 +80,9 @@ cudaError_t make_slab_map(CUtensorMap* map, const void* base, uint64_t units, ui
 
 cudaError_t make_map_4d(CUtensorMap* map, const void* base, uint64_t d, uint64_t n1, uint64_t n2,
                         uint64_t n3, int64_t s1, int64_t s2, int64_t s3, const uint32_t* box) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return cudaErrorNotSupported;
+  cudaError_t e;
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder(&e);
+  if (fn == nullptr) return e;
   const cuuint64_t dims[4] = {d, n1, n2, n3};
   const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
   const cuuint32_t elem[4] = {1, 1, 1, 1};

@@ -1,6 +1,8 @@
 """Calls of the operators next to ELSAA that their documentation allows or refuses and
 that test_gpu_layer.py does not make, and the code paths of larger sizes."""
 
+import threading
+
 import pytest
 import torch
 
@@ -329,3 +331,56 @@ def test_calls_at_the_same_time(cuda_device):
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
     assert all(torch.equal(g, pwant) for g in pgot)
     B.check(ws), B.check(pws)
+
+
+def in_a_new_thread(f):
+    """f's result from a thread that has made no CUDA call."""
+    got = []
+
+    def run():
+        try:
+            got.append(f())
+        except Exception as e:
+            got.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    if isinstance(got[0], Exception):
+        raise got[0]
+    return got[0]
+
+
+def test_first_call_of_a_thread(cuda_device):
+    """With every buffer the caller's, so that nothing before the call has set the thread up."""
+    p, q, k, v, dy, _ = window_inputs((1, 4, 2, 200, 64, "bf16", 64, 2, None, False))
+    ws = window.alloc_workspace(p, cuda_device)
+    y, lse = window.forward(p, q, k, v, ws=ws)
+    grads = window.backward(p, q, k, v, y, lse, dy, ws=ws)
+    out = [torch.zeros_like(t) for t in (y, lse, *grads)]
+    torch.cuda.synchronize()
+    in_a_new_thread(lambda: window.forward(p, q, k, v, y=out[0], lse=out[1], ws=ws))
+    in_a_new_thread(lambda: window.backward(p, q, k, v, y, lse, dy, dq=out[2], dk=out[3], dv=out[4], ws=ws))
+    assert all(torch.equal(a, b) for a, b in zip(out, (y, lse, *grads)))
+    for new in (1, 40):
+        pp, *args = paged_inputs((8, 2, 128, "bf16", 16, 0, 0, [(new, 300)]), slack=0)
+        ws = paged.alloc_workspace(pp, cuda_device)
+        want, got = paged.attend(pp, *args, ws=ws), torch.zeros_like(args[0])
+        torch.cuda.synchronize()
+        in_a_new_thread(lambda: paged.attend(pp, *args, y=got, ws=ws))
+        assert torch.equal(got, want)
+
+
+def test_first_call_of_a_thread_elsaa(cuda_device):
+    from sparse_rank_hybrid_simhash_b200.workloads import WORKLOADS, make_inputs, small
+    w = small(WORKLOADS["text-32k"], B=1, H=2, N=1024)
+    p = B.Params.from_workload(w)
+    d = {n: t.to(cuda_device) for n, t in make_inputs(w, with_dy=True).items()}
+    args = [d[n] for n in ("q", "k", "v", "r_sort", "r_race", "gate_w", "gate_b", "lam")]
+    saved, ws = B.alloc_saved(p, cuda_device), B.alloc_workspace(p, cuda_device)
+    y = B.forward(p, *args, saved=saved, ws=ws)
+    grads = B.backward(p, *args, saved, d["dy"], ws=ws)
+    torch.cuda.synchronize()
+    again = in_a_new_thread(lambda: B.backward(p, *args, saved, d["dy"], ws=ws))
+    assert torch.equal(in_a_new_thread(lambda: B.forward(p, *args, saved=saved, ws=ws)), y)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
