@@ -342,8 +342,9 @@ int32_t elsaa_path_flags(const elsaa_params* p);
  *     after ELSAA_ERR_DEVICE_TIMEOUT).
  *   - Two calls that may run at the same time (two streams, two captured
  *     graphs) need a workspace each.
- *   - Outputs overlap no input where this header does not say that they may,
- *     and no two elements of an output share memory. */
+ *   - Outputs overlap no input and no other output where this header does not
+ *     say that they may (one that starts where another tensor does is an
+ *     invalid argument), and no two elements of an output share memory. */
 
 typedef struct {
   int32_t B, H, Hkv, N, d;   /* d in {32, 64, 128} */
@@ -454,7 +455,7 @@ size_t elsaa_paged_workspace_bytes(const elsaa_paged_params* p);
 /* The serving form of elsaa_rotary_forward: norms and rotates the new tokens'
  * q into q_out and k into the pages, and copies v into the pages (r->H, r->Hkv,
  * r->d and r->dtype equal p's; r->B and r->N are not used).  Two tokens of one
- * call must not share a slot. */
+ * call must not share a slot.  q_out may be q, with the same strides. */
 elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_params* r,
                                const void* q, const void* k, const void* v,
                                const int64_t* strides, const float* table,

@@ -95,6 +95,16 @@ bool take_row_strides(const int64_t* given, int64_t rows, int64_t h, int64_t d, 
   return take_strides(x, 1, h, rows, d, esz, out);
 }
 
+// Whether one of the `outs` last of n tensors starts where another tensor does.  (Views of one
+// buffer may lie inside one another's range without sharing an element, so that is all that is
+// refused of what the contract rules out.)
+bool shared_start(const void* const* t, int n, int outs) {
+  for (int o = n - outs; o < n; ++o)
+    for (int i = 0; i < o; ++i)
+      if (t[i] == t[o]) return true;
+  return false;
+}
+
 inline int esize(int dtype) { return dtype == ELSAA_BF16 ? 2 : 4; }
 
 elsaa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ELSAA_OK : ELSAA_ERR_CUDA; }
@@ -263,7 +273,7 @@ elsaa_status elsaa_window_forward(const elsaa_window_params* p, const void* q, c
   const void* t[4] = {q, k, v, y};
   const elsaa_status st = window_args(p, t, 4, strides, lengths, ws, ws_bytes, false, &a);
   if (st != ELSAA_OK) return st;
-  if (!lse || !aligned4(lse) || !aligned4(lengths)) return ELSAA_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse) || !aligned4(lengths) || shared_start(t, 4, 1)) return ELSAA_ERR_INVALID_ARG;
   a.lse = lse;
   const bool bf16 = p->dtype == ELSAA_BF16;
   return cuda_status(attend_tc_supported(p->d, bf16)
@@ -279,7 +289,7 @@ elsaa_status elsaa_window_backward(const elsaa_window_params* p, const void* q, 
   const void* t[8] = {q, k, v, y, dy, dq, dk, dv};
   const elsaa_status st = window_args(p, t, 8, strides, lengths, ws, ws_bytes, true, &a);
   if (st != ELSAA_OK) return st;
-  if (!lse || !aligned4(lse) || !aligned4(lengths)) return ELSAA_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse) || !aligned4(lengths) || shared_start(t, 8, 3)) return ELSAA_ERR_INVALID_ARG;
   a.lse = const_cast<float*>(lse);
   a.dy = dy;
   a.dq = dq;
@@ -338,6 +348,8 @@ elsaa_status elsaa_paged_write(const elsaa_paged_params* p, const elsaa_rotary_p
   for (const void* x : {page_table, starts, lengths})
     if (!aligned4(x)) return ELSAA_ERR_INVALID_ARG;
   if (ws_bytes < kHeadBytes) return ELSAA_ERR_WORKSPACE;
+  const void* const out[5] = {k, v, q_out, k_pages, v_pages};
+  if (shared_start(out, 5, 3) || k_pages == q || v_pages == q) return ELSAA_ERR_INVALID_ARG;
   const int e = esize(p->dtype);
   auto take = [&](int i, int h, Strides* to) {
     return take_row_strides(strides ? strides + 2 * i : nullptr, p->rows, h, p->d, e, to);
@@ -377,6 +389,7 @@ elsaa_status elsaa_paged_attend(const elsaa_paged_params* p, const void* q,
     if (!aligned4(x)) return ELSAA_ERR_INVALID_ARG;
   if (((uintptr_t)ws & 255) != 0) return ELSAA_ERR_INVALID_ARG;
   if (ws_bytes < elsaa_paged_workspace_bytes(p)) return ELSAA_ERR_WORKSPACE;
+  if (y == q || y == k_pages || y == v_pages) return ELSAA_ERR_INVALID_ARG;
   AttendArgs a = {};
   const int e = esize(p->dtype);
   if (!take_row_strides(strides, p->rows, p->H, p->d, e, &a.sq) ||

@@ -384,3 +384,22 @@ def test_first_call_of_a_thread_elsaa(cuda_device):
     again = in_a_new_thread(lambda: B.backward(p, *args, saved, d["dy"], ws=ws))
     assert torch.equal(in_a_new_thread(lambda: B.forward(p, *args, saved=saved, ws=ws)), y)
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_paged_write_in_place(cuda_device):
+    """The new queries normed and rotated where they are; an output in an input's place is refused elsewhere."""
+    p, q, kp, vp, table, starts, lengths = paged_inputs((12, 4, 64, "bf16", 16, 0, 0, [(30, 40), (1, 70)]), slack=0)
+    k, v = (rand((p.rows, 4, 64), torch.bfloat16, s) for s in (1, 2))
+    tab = rotary.angle_table(70, 64, device=cuda_device)
+    rp = rotary.RotaryParams.make(1, 12, 4, 1, 64, "bf16", 64, 70)
+    want = paged.write(p, rp, q, k, v, tab, None, None, kp, vp, table, starts, lengths)
+    wide = torch.zeros(p.rows, 20, 64, dtype=q.dtype, device=cuda_device)
+    wide[:, :12], wide[:, 12:16], wide[:, 16:] = q, k, v
+    parts = wide.split([12, 4, 4], dim=1)
+    paged.write(p, rp, *parts, tab, None, None, kp, vp, table, starts, lengths, qo=parts[0])
+    assert torch.equal(parts[0], want) and torch.equal(parts[1], k) and torch.equal(parts[2], v)
+    for call in (lambda: paged.attend(p, want, kp, vp, table, starts, lengths, y=want),
+                 lambda: paged.write(p, rp, q, k, v, tab, None, None, kp, kp, table, starts, lengths)):
+        with pytest.raises(B.ElsaaError) as e:
+            call()
+        assert e.value.code == 1

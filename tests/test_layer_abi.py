@@ -149,6 +149,35 @@ def test_paged_refusals():
         assert code == 1, kw
 
 
+def test_outputs_that_start_where_another_tensor_does():
+    """Refused before anything is launched (each output in turn in the place of each other tensor)."""
+    L, at = B.lib(), [(i + 1) << 24 for i in range(11)]
+    p, w = win(), window.workspace_bytes(win(), True)
+    for o, i in ((3, 0), (3, 1), (3, 2)):
+        t = list(at)
+        t[o] = t[i]
+        assert L.elsaa_window_forward(ctypes.byref(p), *t[:3], NULL, NULL, t[3], t[4], t[5], w, NULL) == 1
+    for o in (5, 6, 7):
+        for i in range(o):
+            t = list(at)
+            t[o] = t[i]
+            q, k, v, y, dy, dq, dk, dv, lse, ws = t[:10]
+            assert L.elsaa_window_backward(ctypes.byref(p), q, k, v, NULL, NULL, y, lse, dy, dq, dk, dv, ws, w,
+                                           NULL) == 1, (o, i)
+    p, w = pag(), paged.workspace_bytes(pag())
+    for i in range(3):
+        q, kp, vp, pt, st, ln, y, ws = at[:8]
+        y = at[i]
+        assert L.elsaa_paged_attend(ctypes.byref(p), q, NULL, kp, vp, NULL, pt, st, ln, y, ws, w, NULL) == 1
+    r = rot()
+    for o, i in ((3, 1), (3, 2), (4, 0), (4, 1), (4, 2), (4, 3), (5, 0), (5, 1), (5, 2), (5, 3), (5, 4)):
+        t = list(at)
+        t[o] = t[i]
+        q, k, v, qo, kp, vp, table, pt, st, ln, ws = t
+        assert L.elsaa_paged_write(ctypes.byref(p), ctypes.byref(r), q, k, v, NULL, table, NULL, NULL, qo, kp, vp, NULL,
+                                   pt, st, ln, ws, w, NULL) == 1, (o, i)
+
+
 def test_python_checks():
     x = torch.zeros(1, 4, 8, 32)
     with pytest.raises(ValueError):          # no CPU path
