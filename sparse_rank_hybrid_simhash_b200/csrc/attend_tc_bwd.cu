@@ -25,9 +25,16 @@
 // columns.  The products of one block run under the elementwise work of the
 // previous one: dV and the next S under dS, dK and the next dP under P.
 //
-// Bound at d = 128: 2048 (dkv) and 1536 (dq) cycles of products a block against
-// 1024 of exponentials and about as many of other instructions; at d = 64 the
-// elementwise work.  stats_kernel (rows of y and dy once) is bound by HBM.
+// P and dS are rounded to bf16, the other operand's type, before the gradients'
+// products (half a step each, random; the sums are fp32): dq, dk and dv are off by
+// 0.0024 of their norm against 64 bits (their own rounding alone: 0.0017).
+//
+// Bound: a block's floor at d = 128 is 2048 (dkv) and 1536 (dq) cycles of products,
+// at d = 64 half of that, against 1024 of exponentials and about as many of other
+// instructions.  At d = 64 nothing is full (issue slots 38 and 41 % active, the tensor
+// pipe 33 %): what counts is the latency of the chain of a block (S read from TMEM,
+// exponentials, P written, dP read, dS written), with one block's worth in flight.
+// stats_kernel (rows of y and dy once) is bound by HBM.
 // Measured: 8192 tokens, 32 query and 8 key heads, window 4096: d = 128 1306 us (790
 // TFLOP/s by the formulas' five products), d = 64 927 us; text-32k (2 x 12 heads of
 // d = 64, 32768 tokens) at window 1024: dkv 685 us, dq 512, stats 49.

@@ -10,12 +10,17 @@
 // and O += P V by 16 x 8 x 16 tensor instructions (a 128-row tcgen05 tile holds 8 to
 // 16 live rows here, its S, P and O go through TMEM with a barrier each way, and the
 // blocks that wait there take the ring's slots: 50 % of the bandwidth at contexts of
-// 1000 to 5000 keys).  The row reference grows only by more than 2^8.
+// 1000 to 5000 keys).  The row reference grows only by more than 2^8.  P is rounded to bf16,
+// V's type, for its product (half a step of a probability, random: the error of y against 64
+// bits 0.0021 to 0.0023 of its norm, y's own rounding alone 0.0016); P in two bf16 parts
+// would leave that alone, at 416 -> 444 us for 64 sequences over up to 16k keys: not taken.
 // Measured against that kernel: 64 sequences over up to 16k keys (32 query and 8 key
 // heads of d = 128) 361 against 398 us, 93 % of the copy bandwidth; 87 over a window of
 // 1318 151 against 214; one sequence 13.6 against 18.5.  A long chunk among single
-// tokens adds no more than a second tile a sequence (the average bounds their number),
-// and the tiles of one sequence find its keys in L2.
+// tokens comes here too where the average stays small, which bounds the number of tiles
+// but not their keys: each walks its sequence's context, out of L2 behind the first.  900
+// tokens beside 63 single ones, 8 heads of d = 128 over contexts of 4000: 293 us, against
+// 172 for the tokens and 54 for the chunk in two calls.
 //
 // Items (row tile, key head) are cut into equal runs of 64-key blocks (paged_runs.cuh);
 // the four warps' rows are joined in shared memory at an item's end, cut items by the

@@ -16,8 +16,11 @@
 // head, key block) units cut into equal runs, one per CTA; an item cut between CTAs
 // leaves unnormalised partial rows, which the last CTA to get there adds up in the
 // CTAs' order.
-// Bound: the fp32 products (FMA pipe) and the shared-memory reads that feed them
-// (a 4 x 4 score tile reads 8 vectors for 64 FMA a thread).
+// Bound: the shared-memory reads that feed the products (a 4 x 4 score tile reads 8
+// vectors for 64 FMA a thread) and instruction issue.  fp32, 8 heads of d = 64, 8192 tokens,
+// window 512, 4 sinks, forward 368 us: L1 and shared memory 76 % busy, issue slots 72 %, the
+// FMA pipe 55 %; warps wait for shared reads (1.3 an issue), then for their turn, and for a
+// block's copy and its barriers (0.5), which two CTAs an SM cover (at d = 128 there is one).
 #include <math.h>
 
 #include "attend.cuh"

@@ -118,7 +118,8 @@ class WindowFunction(torch.autograd.Function):
 
 
 def window_attention(q, k, v, window=0, sinks=0, lengths=None, scale=0.0, ws=None):
-    """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d].
+    """Differentiable window attention of q [B, H, N, d] over k, v [B, Hkv, N, d]; ``lengths``
+    int32 [B] on the device.
 
     ``ws`` (``alloc_workspace``) serves the forward and the backward; what they record on the
     device (a wait that gave up) is read with ``binding.check(ws)``.  Without it each makes its
