@@ -108,13 +108,13 @@ def backward(p: RotaryParams, q, k, table, q_weight, k_weight, dqo, dko, positio
     if dq is None:
         dq = layer.like(q)
     if k is None:
-        if dko is not None or dk is not None:
-            raise ValueError("dko or dk without k")
-        dk_weight = None
+        if dko is not None or dk is not None or dk_weight is not None:
+            raise ValueError("dko, dk or dk_weight without k")
     elif dk is None:
         dk = layer.like(k)
     if not p.norm:
-        dq_weight = dk_weight = None
+        if dq_weight is not None or dk_weight is not None:
+            raise ValueError("gradients of weights without the norm")
     else:
         if dq_weight is None:
             dq_weight = torch.empty(p.d, dtype=torch.float32, device=dev)

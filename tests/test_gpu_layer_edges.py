@@ -403,3 +403,20 @@ def test_paged_write_in_place(cuda_device):
         with pytest.raises(B.ElsaaError) as e:
             call()
         assert e.value.code == 1
+
+
+def test_rotary_refuses_gradients_it_does_not_write(cuda_device):
+    """A caller's buffer is written or refused, never left as it was."""
+    q, k = rand((1, 2, 9, 64), torch.float32, 1), rand((1, 1, 9, 64), torch.float32, 2)
+    tab, w = rotary.angle_table(9, 64, device=cuda_device), torch.ones(64, device=cuda_device)
+    plain = rotary.RotaryParams.make(1, 2, 1, 9, 64, "f32", 64, 9, norm=False)
+    normed = rotary.RotaryParams.make(1, 2, 1, 9, 64, "f32", 64, 9)
+    for kw in (dict(dq_weight=w), dict(dk_weight=w)):
+        with pytest.raises(ValueError):
+            rotary.backward(plain, q, k, tab, None, None, q, k, **kw)
+    with pytest.raises(ValueError):
+        rotary.backward(normed, q, None, tab, w, None, q, None, dk_weight=w)
+    into = torch.full((2, 64), 7.0, device=cuda_device)
+    got = rotary.backward(normed, q, k, tab, w, w, q, k, dq_weight=into[0], dk_weight=into[1])
+    want = rotary.backward(normed, q, k, tab, w, w, q, k)
+    assert torch.equal(into[0], want[2]) and torch.equal(into[1], want[3]) and got[2] is not None
