@@ -13,11 +13,12 @@
 // used so far (P <= 2^8 otherwise; bf16 keeps the same relative precision there,
 // and the final division cancels the reference): a rare event after the first
 // blocks, where a rescaling of every block costs a pass over O.  P is rounded to bf16,
-// the type of V and so of both operands of P V: half a step (2^-8) of every probability, in
-// both directions, takes the error of y against 64 bits from its own rounding's 0.0016 of its
-// norm to 0.0021 .. 0.0023.  P as two bf16 parts (P V twice; they fit over S) would leave y's
-// own rounding, at 1035 -> 1365 us for a 16k prefill (32 and 8 heads of d = 128, window 4096), 168 -> 207 for prompt
-// chunks and 1781 -> 1880 for text-32k with its backward: not taken.  Sums and maxima are fp32.
+// the type of V and so of both operands of P V: half a step (2^-8) of every probability,
+// in both directions, takes the error of y against 64 bits from its own rounding's
+// 0.0016 of its norm to 0.0021 .. 0.0023.  P as two bf16 parts (P V twice; they fit over
+// S) would leave y's own rounding, at 1035 -> 1365 us for a 16k prefill (32 and 8 heads
+// of d = 128, window 4096), 168 -> 207 for prompt chunks and 1781 -> 1880 for text-32k
+// with its backward: not taken.  Sums and maxima are fp32.
 //
 // Streams of an item:
 //   window, g even    two query heads of one key head at the same 128 tokens

@@ -159,9 +159,9 @@ class NormRotateFunction(torch.autograd.Function):
 def norm_rotate(q, k, table=None, q_weight=None, k_weight=None, positions=None, rot_dim=None,
                 interleaved=False, norm=True, eps=1e-6, ws=None):
     """Differentiable norm and rotation of q [B, H, N, d] and k [B, Hkv, N, d]; ``table`` as
-    ``angle_table`` makes it (None: norm only), with a row for every token where there are no
-    int32 ``positions`` [B, N].  The weights are fp32 [d] (None: ones) and belong to the norm:
-    without it they are not used.  ``ws`` (``alloc_workspace``) serves the forward and the backward; what they
+    ``angle_table`` makes it (None: norm only), with a row for every token where there are no int32
+    ``positions`` [B, N].  The weights are fp32 [d] (None: ones) and belong to the norm: without it
+    they are not used.  ``ws`` (``alloc_workspace``) serves the forward and the backward; what they
     record on the device (positions outside the table, whose rows are zeros) is read with
     ``binding.check(ws)``.  Without it each makes its own, and the record is lost with it.  In a
     captured step as ``window.window_attention``."""
